@@ -35,7 +35,9 @@ EXPORTED = ("rglru_state_init", "rglru_prefill_workspace_size", "rglru_block_pre
             "rglru_block_backward", "rglru_backward_plan", "rglru_decode_steps_workspace_size",
             "rglru_block_decode_steps", "rglru_decode_steps_plan", "rglru_layer_workspace_size",
             "rglru_layer_forward", "rglru_layer_plan", "rglru_mqa_workspace_size", "rglru_mqa_prefill",
-            "rglru_mqa_decode")
+            "rglru_mqa_decode", "rglru_mqa_save_size", "rglru_mqa_train_workspace_size", "rglru_mqa_forward",
+            "rglru_mqa_backward", "rglru_mqa_cache8_write", "rglru_mqa_decode8_workspace_size", "rglru_mqa_decode8",
+            "rglru_mqa_cache8_read")
 
 # Fields of rglru_grads, in order (fp32 device tensors).
 GRAD_FIELDS = ("dx", "dy", "dh0", "dtail0", "dconv_w", "dconv_b", "dw_a", "dw_x", "db_a", "db_x",
@@ -151,6 +153,19 @@ def load(build_if_missing: bool = True):
     lib.rglru_mqa_prefill.restype = I
     lib.rglru_mqa_decode.argtypes = [PM, V, V, V, V, V, V, V, S, V]
     lib.rglru_mqa_decode.restype = I
+    for fn in (lib.rglru_mqa_save_size, lib.rglru_mqa_train_workspace_size, lib.rglru_mqa_decode8_workspace_size):
+        fn.argtypes = [PM]
+        fn.restype = S
+    lib.rglru_mqa_forward.argtypes = [PM, V, V, V, V, I, V, V, S, V, S, V]
+    lib.rglru_mqa_forward.restype = I
+    lib.rglru_mqa_backward.argtypes = [PM, V, V, V, V, S, V, V, V, V, S, V]
+    lib.rglru_mqa_backward.restype = I
+    lib.rglru_mqa_cache8_write.argtypes = [PM, V, V, V, I, V, V, V]
+    lib.rglru_mqa_cache8_write.restype = I
+    lib.rglru_mqa_decode8.argtypes = [PM, V, V, V, V, V, V, V, V, S, V]
+    lib.rglru_mqa_decode8.restype = I
+    lib.rglru_mqa_cache8_read.argtypes = [PM, V, V, V, V, V]
+    lib.rglru_mqa_cache8_read.restype = I
     lib.rglru_last_cuda_error.argtypes = [ctypes.POINTER(ctypes.c_char_p)]
     lib.rglru_last_cuda_error.restype = I
     lib.rglru_abi_version.argtypes = []
@@ -336,6 +351,114 @@ def mqa_decode(dims: MqaDims, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     rc = load().rglru_mqa_decode(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(pos), _ptr(cache), _ptr(out),
                                  _ptr(workspace), workspace.numel(), _stream(stream))
     _check(rc, "rglru_mqa_decode")
+
+
+def _expect(where: str, *wanted):
+    """wanted: (name, tensor or None, shape, dtypes).  The C ABI sees addresses only, so a tensor of another
+    shape, type or device than the dims say is refused here."""
+    device = None
+    for name, t, shape, dtypes in wanted:
+        if t is None:
+            continue
+        if not t.is_cuda or (device is not None and t.device != device):
+            raise ValueError(f"{where}: {name} must be a CUDA tensor on the same device as the others, got {t.device}")
+        device = t.device
+        if t.dtype not in dtypes:
+            raise ValueError(f"{where}: {name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if device is not None and device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+_BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+_CODES, _BYTES = (torch.float8_e4m3fn, torch.uint8), (torch.uint8,)
+
+
+def _expect_buffer(where: str, name: str, t: torch.Tensor, like: torch.Tensor):
+    if not t.is_cuda or t.device != like.device or t.dtype != torch.uint8:
+        raise ValueError(f"{where}: {name} must be a uint8 CUDA tensor on {like.device}")
+
+
+def mqa_save_size(dims: MqaDims) -> int:
+    return load().rglru_mqa_save_size(ctypes.byref(dims))
+
+
+def mqa_train_workspace_size(dims: MqaDims) -> int:
+    return load().rglru_mqa_train_workspace_size(ctypes.byref(dims))
+
+
+def mqa_forward(dims: MqaDims, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                save: torch.Tensor, workspace: torch.Tensor, pos0: int = 0, reset: Optional[torch.Tensor] = None,
+                stream=None):
+    """rglru_mqa_forward: q [B, T, H, d], k, v [B, T, d], reset [B, T] uint8 or None -> out [B, T, H, d]; ``save``
+    (mqa_save_size bytes) keeps what mqa_backward needs."""
+    B, T, H, d = dims.batch, dims.seq_len, dims.q_heads, dims.head_dim
+    where = "rglru_mqa_forward"
+    _expect(where, ("q", q, (B, T, H, d), _BF16), ("k", k, (B, T, d), _BF16), ("v", v, (B, T, d), _BF16),
+            ("out", out, (B, T, H, d), _BF16), ("reset", reset, (B, T), _BYTES))
+    _expect_buffer(where, "save", save, q)
+    _expect_buffer(where, "workspace", workspace, q)
+    rc = load().rglru_mqa_forward(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(reset), int(pos0), _ptr(out),
+                                  _ptr(save), save.numel(), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, where)
+
+
+def mqa_backward(dims: MqaDims, v: torch.Tensor, out: torch.Tensor, dout: torch.Tensor, save: torch.Tensor,
+                 dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """rglru_mqa_backward: out, dout [B, T, H, d], v [B, T, d] -> dq [B, T, H, d], dk, dv [B, T, d]."""
+    B, T, H, d = dims.batch, dims.seq_len, dims.q_heads, dims.head_dim
+    where = "rglru_mqa_backward"
+    _expect(where, ("v", v, (B, T, d), _BF16), ("out", out, (B, T, H, d), _BF16), ("dout", dout, (B, T, H, d), _BF16),
+            ("dq", dq, (B, T, H, d), _BF16), ("dk", dk, (B, T, d), _BF16), ("dv", dv, (B, T, d), _BF16))
+    _expect_buffer(where, "save", save, v)
+    _expect_buffer(where, "workspace", workspace, v)
+    rc = load().rglru_mqa_backward(ctypes.byref(dims), _ptr(v), _ptr(out), _ptr(dout), _ptr(save), save.numel(),
+                                   _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, where)
+
+
+def mqa_cache8_write(dims: MqaDims, k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                     pos0: int = 0, lengths: Optional[torch.Tensor] = None, stream=None):
+    """rglru_mqa_cache8_write: k, v [B, T, d], lengths [B] int32 or None -> codes [B, 2, w, d] (float8_e4m3fn, or
+    its bytes), scales [B, 2, w] fp32."""
+    B, T, w, d = dims.batch, dims.seq_len, dims.window, dims.head_dim
+    where = "rglru_mqa_cache8_write"
+    _expect(where, ("k", k, (B, T, d), _BF16), ("v", v, (B, T, d), _BF16), ("codes", codes, (B, 2, w, d), _CODES),
+            ("scales", scales, (B, 2, w), _F32), ("lengths", lengths, (B,), _I32))
+    rc = load().rglru_mqa_cache8_write(ctypes.byref(dims), _ptr(k), _ptr(v), _ptr(lengths), int(pos0), _ptr(codes),
+                                       _ptr(scales), _stream(stream))
+    _check(rc, where)
+
+
+def mqa_decode8_workspace_size(dims: MqaDims) -> int:
+    return load().rglru_mqa_decode8_workspace_size(ctypes.byref(dims))
+
+
+def mqa_decode8(dims: MqaDims, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
+                codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """rglru_mqa_decode8: q [B, H, d], k, v [B, d], pos [B] int32 (device) -> out [B, H, d]; the 8-bit ring (codes
+    [B, 2, w, d], scales [B, 2, w]) receives the new slot."""
+    B, H, w, d = dims.batch, dims.q_heads, dims.window, dims.head_dim
+    where = "rglru_mqa_decode8"
+    _expect(where, ("q", q, (B, H, d), _BF16), ("k", k, (B, d), _BF16), ("v", v, (B, d), _BF16), ("pos", pos, (B,), _I32),
+            ("codes", codes, (B, 2, w, d), _CODES), ("scales", scales, (B, 2, w), _F32), ("out", out, (B, H, d), _BF16))
+    _expect_buffer(where, "workspace", workspace, q)
+    rc = load().rglru_mqa_decode8(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(pos), _ptr(codes), _ptr(scales),
+                                  _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, where)
+
+
+def mqa_cache8_read(dims: MqaDims, codes: torch.Tensor, scales: torch.Tensor, cache: torch.Tensor,
+                    pos: Optional[torch.Tensor] = None, stream=None):
+    """rglru_mqa_cache8_read: the 8-bit ring as the bf16 ring cache [B, 2, w, d]; pos [B] int32 or None."""
+    B, w, d = dims.batch, dims.window, dims.head_dim
+    where = "rglru_mqa_cache8_read"
+    _expect(where, ("codes", codes, (B, 2, w, d), _CODES), ("scales", scales, (B, 2, w), _F32),
+            ("cache", cache, (B, 2, w, d), _BF16), ("pos", pos, (B,), _I32))
+    rc = load().rglru_mqa_cache8_read(ctypes.byref(dims), _ptr(codes), _ptr(scales), _ptr(pos), _ptr(cache),
+                                      _stream(stream))
+    _check(rc, where)
 
 
 def backward_workspace_size(dims: Dims) -> int:

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "common.cuh"
@@ -368,6 +369,108 @@ rglru_status rglru_mqa_decode(const rglru_mqa_dims* dims, const void* q, const v
     if ((st = check_workspace(workspace, workspace_bytes, rglru_mqa_workspace_size(dims, 1))) != RGLRU_OK) return st;
     return cuda_status(rglru::launch_mqa_decode(dims, q, k, v, pos, cache, out, workspace, workspace_bytes,
                                                 static_cast<cudaStream_t>(stream)));
+}
+
+static rglru_status check_mqa_train(const rglru_mqa_dims* d) {
+    rglru_status st = check_mqa(d, false);
+    if (st != RGLRU_OK) return st;
+    if (d->batch > 65535 || (long long)d->seq_len * d->q_heads > (1LL << 30)) return RGLRU_ERR_UNSUPPORTED;
+    return RGLRU_OK;
+}
+
+static rglru_status check_mqa_cache8(const rglru_mqa_dims* d, bool tokens) {
+    rglru_status st = check_mqa(d, !tokens);
+    if (st != RGLRU_OK) return st;
+    if (d->batch > 65535 || (long long)d->batch * d->window > (1LL << 31)) return RGLRU_ERR_UNSUPPORTED;
+    return RGLRU_OK;
+}
+
+static bool positions_fit(int pos0, int n) { return pos0 >= 0 && (long long)pos0 + n <= 0x7fffffffLL; }
+
+// every pointer given, 16-byte aligned; no output (the last n_out) equal to another pointer
+static rglru_status check_tensors(const void* const* p, int n, int n_out) {
+    for (int i = 0; i < n; ++i) {
+        if (!p[i] || !aligned(p[i], 16)) return RGLRU_ERR_INVALID_ARG;
+        for (int j = std::max(i + 1, n - n_out); j < n; ++j)
+            if (p[i] == p[j]) return RGLRU_ERR_INVALID_ARG;
+    }
+    return RGLRU_OK;
+}
+
+size_t rglru_mqa_save_size(const rglru_mqa_dims* dims) {
+    return check_mqa_train(dims) == RGLRU_OK ? rglru::mqa_save_bytes(dims) : 0;
+}
+
+size_t rglru_mqa_train_workspace_size(const rglru_mqa_dims* dims) {
+    return check_mqa_train(dims) == RGLRU_OK ? rglru::mqa_train_workspace(dims) : 0;
+}
+
+rglru_status rglru_mqa_forward(const rglru_mqa_dims* dims, const void* q, const void* k, const void* v,
+                               const uint8_t* reset, int pos0, void* out, void* save, size_t save_bytes,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+    rglru_status st = check_mqa_train(dims);
+    if (st != RGLRU_OK) return st;
+    const void* t[] = {q, k, v, out};
+    if ((st = check_tensors(t, 4, 1)) != RGLRU_OK) return st;
+    if (!positions_fit(pos0, dims->seq_len) || (save && save == workspace)) return RGLRU_ERR_INVALID_ARG;
+    if ((st = check_workspace(save, save_bytes, rglru_mqa_save_size(dims))) != RGLRU_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, rglru_mqa_train_workspace_size(dims))) != RGLRU_OK) return st;
+    return cuda_status(rglru::launch_mqa_forward(dims, q, k, v, reset, pos0, out, save, workspace,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+rglru_status rglru_mqa_backward(const rglru_mqa_dims* dims, const void* v, const void* out, const void* dout,
+                                const void* save, size_t save_bytes, void* dq, void* dk, void* dv, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    rglru_status st = check_mqa_train(dims);
+    if (st != RGLRU_OK) return st;
+    const void* t[] = {v, out, dout, dq, dk, dv};
+    if ((st = check_tensors(t, 6, 3)) != RGLRU_OK) return st;
+    if (save && save == workspace) return RGLRU_ERR_INVALID_ARG;
+    if ((st = check_workspace(const_cast<void*>(save), save_bytes, rglru_mqa_save_size(dims))) != RGLRU_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, rglru_mqa_train_workspace_size(dims))) != RGLRU_OK) return st;
+    return cuda_status(rglru::launch_mqa_backward(dims, v, out, dout, save, dq, dk, dv, workspace,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+rglru_status rglru_mqa_cache8_write(const rglru_mqa_dims* dims, const void* k, const void* v, const int* lengths,
+                                    int pos0, void* codes, float* scales, void* stream) {
+    rglru_status st = check_mqa_cache8(dims, true);
+    if (st != RGLRU_OK) return st;
+    const void* t[] = {k, v, codes};
+    if ((st = check_tensors(t, 3, 1)) != RGLRU_OK) return st;
+    if (!scales || !aligned(scales, 4) || !aligned(lengths, 4) || !positions_fit(pos0, dims->seq_len))
+        return RGLRU_ERR_INVALID_ARG;
+    return cuda_status(rglru::launch_mqa_cache8_write(dims, k, v, lengths, pos0, codes, scales,
+                                                      static_cast<cudaStream_t>(stream)));
+}
+
+size_t rglru_mqa_decode8_workspace_size(const rglru_mqa_dims* dims) {
+    return check_mqa_cache8(dims, false) == RGLRU_OK ? rglru::mqa_decode8_workspace(dims) : 0;
+}
+
+rglru_status rglru_mqa_decode8(const rglru_mqa_dims* dims, const void* q, const void* k, const void* v, const int* pos,
+                               void* codes, float* scales, void* out, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    rglru_status st = check_mqa_cache8(dims, false);
+    if (st != RGLRU_OK) return st;
+    const void* t[] = {q, k, v, codes, out};
+    if ((st = check_tensors(t, 5, 2)) != RGLRU_OK) return st;
+    if (!pos || !aligned(pos, 4) || !scales || !aligned(scales, 4)) return RGLRU_ERR_INVALID_ARG;
+    if ((st = check_workspace(workspace, workspace_bytes, rglru_mqa_decode8_workspace_size(dims))) != RGLRU_OK) return st;
+    return cuda_status(rglru::launch_mqa_decode8(dims, q, k, v, pos, codes, scales, out, workspace,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+rglru_status rglru_mqa_cache8_read(const rglru_mqa_dims* dims, const void* codes, const float* scales, const int* pos,
+                                   void* cache, void* stream) {
+    rglru_status st = check_mqa_cache8(dims, false);
+    if (st != RGLRU_OK) return st;
+    const void* t[] = {codes, cache};
+    if ((st = check_tensors(t, 2, 1)) != RGLRU_OK) return st;
+    if (!scales || !aligned(scales, 4) || !aligned(pos, 4)) return RGLRU_ERR_INVALID_ARG;
+    return cuda_status(rglru::launch_mqa_cache8_read(dims, codes, scales, pos, cache,
+                                                     static_cast<cudaStream_t>(stream)));
 }
 
 size_t rglru_backward_workspace_size(const rglru_dims* dims) {

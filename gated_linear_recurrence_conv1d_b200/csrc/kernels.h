@@ -69,6 +69,23 @@ cudaError_t launch_mqa_prefill(const rglru_mqa_dims* d, const void* q, const voi
 cudaError_t launch_mqa_decode(const rglru_mqa_dims* d, const void* q, const void* k, const void* v, const int* pos,
                               void* cache, void* out, void* ws, size_t ws_bytes, cudaStream_t s);
 
+// The same attention in training (mqa_train.cu): the forward keeps mqa_save_bytes() for the backward.
+size_t mqa_save_bytes(const rglru_mqa_dims* d);
+size_t mqa_train_workspace(const rglru_mqa_dims* d);
+cudaError_t launch_mqa_forward(const rglru_mqa_dims* d, const void* q, const void* k, const void* v,
+                               const uint8_t* reset, int pos0, void* out, void* save, void* ws, cudaStream_t s);
+cudaError_t launch_mqa_backward(const rglru_mqa_dims* d, const void* v, const void* out, const void* dout,
+                                const void* save, void* dq, void* dk, void* dv, void* ws, cudaStream_t s);
+
+// Its 8-bit ring cache (mqa_cache8.cu).
+size_t mqa_decode8_workspace(const rglru_mqa_dims* d);
+cudaError_t launch_mqa_cache8_write(const rglru_mqa_dims* d, const void* k, const void* v, const int* lengths, int pos0,
+                                    void* codes, float* scales, cudaStream_t s);
+cudaError_t launch_mqa_decode8(const rglru_mqa_dims* d, const void* q, const void* k, const void* v, const int* pos,
+                               void* codes, float* scales, void* out, void* ws, cudaStream_t s);
+cudaError_t launch_mqa_cache8_read(const rglru_mqa_dims* d, const void* codes, const float* scales, const int* pos,
+                                   void* cache, cudaStream_t s);
+
 // Tensor-core decode step (bf16, head_dim 256): one launch of 4-CTA clusters (conv + history
 // shift per channel quarter, conv blocks shared over distributed shared memory, tcgen05 gates,
 // the state update).  Needs the workspace fused_decode_workspace() (the status word).

@@ -264,6 +264,68 @@ RGLRU_API rglru_status rglru_mqa_decode(const rglru_mqa_dims* dims, const void* 
                                         const void* v, const int* pos, void* cache, void* out,
                                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- the local attention in training ----
+ * The same attention with packed documents, in a forward that keeps what its gradient needs and a
+ * backward that recomputes the softmax weights from it.  Dims as for rglru_mqa_prefill, and
+ * seq_len * q_heads <= 2^30, batch <= 65535 (else UNSUPPORTED); pos0 >= 0, pos0 + seq_len <= 2^31 - 1.
+ *   reset   [B, T] uint8 or NULL: nonzero = that token starts a document, and tokens from it on
+ *           do not attend to the tokens before it (as rglru_block_prefill's reset).  The tokens
+ *           keep their positions pos0 + t: scores depend on differences of positions only.
+ *   save    rglru_mqa_save_size bytes, 256-byte aligned, owned by the caller: written by the forward,
+ *           read by the backward, which needs it unchanged and the same dims.  It holds the
+ *           rotated queries and keys, so q and k may be freed or overwritten in between.
+ * Both calls take a workspace of rglru_mqa_train_workspace_size bytes (scratch: nothing in it has
+ * to survive from the forward to the backward).  Every input value has to be finite (a masked
+ * key still enters the tensor-core products, with weight 0). */
+RGLRU_API size_t rglru_mqa_save_size(const rglru_mqa_dims* dims);
+RGLRU_API size_t rglru_mqa_train_workspace_size(const rglru_mqa_dims* dims);
+
+/* q [B, T, H, d], k, v [B, T, d] -> out [B, T, H, d], and *save.  Errors as rglru_mqa_prefill; a save
+ * that is missing or smaller than the queried size is WORKSPACE. */
+RGLRU_API rglru_status rglru_mqa_forward(const rglru_mqa_dims* dims, const void* q, const void* k, const void* v,
+                                         const uint8_t* reset, int pos0, void* out, void* save, size_t save_bytes,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* With v the forward's values, out its output and dout [B, T, H, d] = dL/dout, writes the gradients
+ * of L: dq [B, T, H, d], dk, dv [B, T, d] (bf16, overwritten; dk and dv are summed over the query
+ * heads and every query that sees the key, in fp32).  The result does not depend on the order in
+ * which the GPU runs its blocks: the same call gives the same bits.  Outputs must not alias inputs
+ * or each other.  Errors as rglru_mqa_forward. */
+RGLRU_API rglru_status rglru_mqa_backward(const rglru_mqa_dims* dims, const void* v, const void* out, const void* dout,
+                                          const void* save, size_t save_bytes, void* dq, void* dk, void* dv,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- the local attention's ring cache in 8 bits ----
+ * Half the bytes of the bf16 ring, for the decode step that is bound by reading it:
+ *   codes   [B][2][window][head_dim] e4m3 bytes, slots as in the bf16 ring (rotated keys, values);
+ *   scales  [B][2][window] fp32: value = code * scale, with scale = max(amax, 448 * 2^-126) / 448
+ *           over the slot's 256 elements and code = x / scale rounded to e4m3 (nearest even).
+ * A slot with an infinity or a NaN has scale and values that are not finite.  Dims as for
+ * rglru_mqa_decode (codes, cache: 16-byte aligned; scales: 4-byte), batch <= 65535,
+ * batch * window <= 2^31. */
+
+/* Quantises the last min(len, window) tokens of every row into their slots: k, v [B, T, d] at
+ * positions pos0 .. pos0 + T - 1 (pos0 >= 0, pos0 + T <= 2^31 - 1), len = lengths[b] (device int32
+ * [B], clamped to 0 .. T: prompts padded on the right) or T where lengths is NULL.  Other slots
+ * keep what they hold.  q_heads and scale of dims are not used.  One launch. */
+RGLRU_API rglru_status rglru_mqa_cache8_write(const rglru_mqa_dims* dims, const void* k, const void* v,
+                                              const int* lengths, int pos0, void* codes, float* scales, void* stream);
+
+/* One decode token per row against the 8-bit ring: as rglru_mqa_decode, with the new key and value
+ * quantised into slot pos[b] mod w before the token attends to the ring's values (its own
+ * among them).  pos[b] < 0 marks a row without a token: its out is zero, its ring untouched.  Slots
+ * past a ring that is not full yet may hold anything. */
+RGLRU_API size_t rglru_mqa_decode8_workspace_size(const rglru_mqa_dims* dims);
+RGLRU_API rglru_status rglru_mqa_decode8(const rglru_mqa_dims* dims, const void* q, const void* k, const void* v,
+                                         const int* pos, void* codes, float* scales, void* out, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* The ring's values in bf16: cache [B][2][window][head_dim], the ring that rglru_mqa_decode takes.
+ * pos: NULL, or the device int32 [B] of each row's last position: then only the slots that it has
+ * reached, 0 .. min(pos[b], w - 1), are written, and the others of cache are left.  One launch. */
+RGLRU_API rglru_status rglru_mqa_cache8_read(const rglru_mqa_dims* dims, const void* codes, const float* scales,
+                                             const int* pos, void* cache, void* stream);
+
 /* Prefill for callers that cannot allocate device memory.  The pages have no counterpart:
  * this is a deployment variant of rglru_block_prefill, not a step of the method.
  *
