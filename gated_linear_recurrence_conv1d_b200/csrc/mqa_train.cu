@@ -12,19 +12,27 @@
 // dq, dk are dq~, dk~ turned back by their positions (the rotation is orthogonal).
 #include <algorithm>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "common.cuh"
 #include "kernels.h"
+#include "pair.cuh"
+#include "tma_maps.h"
 
 namespace rglru {
 namespace mt {
 
+using namespace pr;
+
 constexpr int D = 256;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxClusters = 74;       // 2-CTA clusters of 148 SMs
 
 // ---------------------------------------------------------------- rotary embedding, documents ----
 // cosine and sine of position pos0 + t, pair j, angle and reduction in fp64: [T][d/2]
@@ -36,28 +44,70 @@ __global__ void __launch_bounds__(D / 2) mqa_angles_kernel(int pos0, float base,
     cs[(size_t)t * (D / 2) + j] = make_float2((float)c, (float)s);
 }
 
-// lo[b][t] = max(0, t - w + 1, start of t's document): a running maximum along the row
-__global__ void __launch_bounds__(1024) mqa_first_key_kernel(int T, int w, const uint8_t* reset, int* lo) {
-    __shared__ int warp_max[32];
+// Per row: the first key of every token, lo = max(0, t - w + 1, start of its document), and the last
+// token that sees it, last = min(T - 1, t + w - 1, end of its document): a running maximum forwards and a
+// running minimum backwards over the tokens that start a document.
+constexpr int kScanThreads = 1024, kScanPer = 8, kScanChunk = kScanThreads * kScanPer;
+__global__ void __launch_bounds__(kScanThreads) mqa_documents_kernel(int T, int w, const uint8_t* reset, int* lo, int* last) {
+    __shared__ int warp_v[32];
     const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint8_t* rs = reset ? reset + (size_t)b * T : nullptr;
+    lo += (size_t)b * T;
+    last += (size_t)b * T;
+    const int chunks = (T + kScanChunk - 1) / kScanChunk;
     int carry = 0;
-    for (int t0 = 0; t0 < T; t0 += 1024) {
-        const int t = t0 + threadIdx.x;
-        int v = (t < T && reset && reset[(size_t)b * T + t]) ? t : 0;
+    for (int c = 0; c < chunks; ++c) {
+        const int t0 = c * kScanChunk + threadIdx.x * kScanPer;
+        int v[kScanPer], run = 0;
+#pragma unroll
+        for (int e = 0; e < kScanPer; ++e) v[e] = t0 + e < T && rs && rs[t0 + e] ? t0 + e : 0;
+#pragma unroll
+        for (int e = 0; e < kScanPer; ++e) v[e] = run = max(run, v[e]);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v = max(v, u);
+            const int u = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run = max(run, u);
         }
-        if (lane == 31) warp_max[warp] = v;
+        if (lane == 31) warp_v[warp] = run;
+        int before = __shfl_up_sync(0xffffffffu, run, 1);
+        if (lane == 0) before = 0;
         __syncthreads();
-        int base = carry, all = carry;
+        int base = max(before, carry);
         for (int i = 0; i < 32; ++i) {
-            if (i < warp) base = max(base, warp_max[i]);
-            all = max(all, warp_max[i]);
+            if (i < warp) base = max(base, warp_v[i]);
+            carry = max(carry, warp_v[i]);
         }
-        if (t < T) lo[(size_t)b * T + t] = max(max(base, v), t - w + 1);
-        carry = all;
+#pragma unroll
+        for (int e = 0; e < kScanPer; ++e)
+            if (t0 + e < T) lo[t0 + e] = max(max(base, v[e]), t0 + e - w + 1);
+        __syncthreads();
+    }
+    carry = T;                          // the first document start after the tokens seen so far, going back
+    for (int c = chunks - 1; c >= 0; --c) {
+        const int t0 = c * kScanChunk + threadIdx.x * kScanPer;
+        int v[kScanPer], run = T;       // v[e]: the first start after t0 + e, inside this thread's tokens
+#pragma unroll
+        for (int e = kScanPer - 1; e >= 0; --e) {
+            v[e] = run;
+            if (t0 + e < T && rs && rs[t0 + e]) run = t0 + e;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_down_sync(0xffffffffu, run, o);
+            if (lane + o < 32) run = min(run, u);
+        }
+        if (lane == 0) warp_v[warp] = run;
+        int after = __shfl_down_sync(0xffffffffu, run, 1);
+        if (lane == 31) after = T;
+        __syncthreads();
+        int base = min(after, carry);
+        for (int i = 0; i < 32; ++i) {
+            if (i > warp) base = min(base, warp_v[i]);
+            carry = min(carry, warp_v[i]);
+        }
+#pragma unroll
+        for (int e = 0; e < kScanPer; ++e)
+            if (t0 + e < T) last[t0 + e] = (int)min((long long)min(min(base, v[e]), T) - 1, (long long)t0 + e + w - 1);
         __syncthreads();
     }
 }
@@ -78,179 +128,1202 @@ __global__ void __launch_bounds__(D / 2) mqa_turn_kernel(int T, int H, const flo
     }
 }
 
+// ---------------------------------------------------------------- tensor-core kernels: shared ---------
 struct Args {
-    int B, T, H;
+    int B, T, H, TH, THp;       // TH = T H query rows of a batch row; THp: their pitch in lse, delta
+    int ntr;                    // 256-row pair tiles of a batch row
     float scale, scale_log2;
-    const __nv_bfloat16 *q_rot, *k_rot, *v, *dout;
-    const float2* cs;
-    const int* lo;
-    float* lse;                 // [B, T H], log2 domain
-    float* delta;
+    const int* lo;              // [B, T]
+    const float2* cs;           // [T, d/2]
+    float* lse;                 // [B, THp], log2 domain
+    float* delta;               // [B, THp]
+    const long long* cum;       // [B nkt + 1]: 64-row tiles before each key tile
+    float* part;                // partial dk, dv of (cluster, key tile)
+    int nkt;                    // 128-key tiles of a batch row
     __nv_bfloat16 *out, *dq, *dk, *dv;
+    DeviceStatus* status;
+    unsigned long long timeout_ns;
 };
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
-}
-// lane l holds elements 8 l .. 8 l + 7; its pair partner (element +- d/2) is lane l ^ 16
-__device__ __forceinline__ void turn_back_store(float (&g)[8], const float2* cs, int lane, __nv_bfloat16* p) {
-    __align__(16) __nv_bfloat16 o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float other = __shfl_xor_sync(0xffffffffu, g[i], 16);
-        const float2 a = cs[(8 * lane + i) & (D / 2 - 1)];
-        // the inverse turn: (x1, x2) = (y1 c + y2 s, y2 c - y1 s)
-        o[i] = __float2bfloat16_rn(g[i] * a.x + (lane < 16 ? other : -other) * a.y);
-    }
-    *reinterpret_cast<uint4*>(p + 8 * lane) = *reinterpret_cast<const uint4*>(o);
-}
-__device__ __forceinline__ void store8(const float (&v)[8], __nv_bfloat16* p) {
-    __align__(16) __nv_bfloat16 o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = __float2bfloat16_rn(v[i]);
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(o);
+// Pair tiles in the order of falling position (the longest rows of a causal window first), dealt to
+// the CTA pairs forwards and backwards in turn, so that every pair gets long and short ones alike.
+// lo_t is non-decreasing in t, so a tile's keys are [lo of its first token, its last token].
+struct QTile {
+    int b, r0, lo, n;           // batch row, first query row of the pair, first key, key tiles
+};
+template <int BK>
+__device__ __forceinline__ bool q_tile(const Args& a, int pair, int npairs, int k, QTile& t) {
+    const int p = k * npairs + ((k & 1) ? npairs - 1 - pair : pair);
+    if (p >= a.B * a.ntr) return false;
+    t.b = p % a.B;
+    t.r0 = (a.ntr - 1 - p / a.B) * 256;
+    const int t0 = t.r0 / a.H, t1 = min(t.r0 + 255, a.TH - 1) / a.H;
+    t.lo = a.lo[(size_t)t.b * a.T + t0];
+    t.n = (t1 + 1 - t.lo + BK - 1) / BK;
+    return true;
 }
 
-// warp = one query row: one pass over its keys with the running maximum and sum
-__global__ void __launch_bounds__(128) mqa_fwd_kernel(Args a) {
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= (long long)a.B * a.T * a.H) return;
-    const long long tok = row / a.H;
-    const long long b = tok / a.T;
-    const int t = (int)(tok % a.T);
-    float q[8], o[8] = {};
-    load8(a.q_rot + row * D + 8 * lane, q);
-    float m = -INFINITY, l = 0.f;
-    for (int i = a.lo[tok]; i <= t; ++i) {
-        float k[8], v[8];
-        load8(a.k_rot + (b * a.T + i) * D + 8 * lane, k);
-        load8(a.v + (b * a.T + i) * D + 8 * lane, v);
-        const float s = dot8(q, k) * a.scale_log2;
-        const float mn = fmaxf(m, s), f = exp2f(m - mn), p = exp2f(s - mn);
-        m = mn;
-        l = fmaf(l, f, p);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = fmaf(o[e], f, p * v[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] /= l;
-    store8(o, a.out + row * D + 8 * lane);
-    if (lane == 0) a.lse[row] = m + log2f(l);
-}
+// ---------------------------------------------------------------- forward -----------------------------
+// A CTA pair (cta_group::2) takes 256 query rows, 128 a CTA, and walks the keys that any of them sees in tiles of 128:
+//   S = Q K^T   (M 256, N 128, K 256; Q and K from shared memory)      two TMEM buffers of 128 columns
+//   O += P V    (M 256, N 256, K 128; P in TMEM over its S, V from shared memory)    256 columns
+// Each CTA loads half of every K tile (64 keys) and of every V tile (128 of its columns), so a key tile costs
+// an SM 64 KB for 2048 tensor cycles: half of what a CTA alone would pull from L2.  8 softmax warps, thread =
+// (row, 64 of the 128 keys): P = 2^(c s - m) with a reference maximum m that moves only when a score
+// passes it by 2^8 (then O and the sum are rescaled; the two threads of a row meet for that only).  P is
+// rounded to bf16 for the MMA; the sum adds the fp32 values.  The S of the next tile runs under the
+// softmax of this one.
+namespace fw {
+constexpr int BK = 128;
+constexpr uint32_t SLOT = 32768;
+constexpr int NSLOT = 5;
+constexpr uint32_t OFF_Q = 0, OFF_SLOT = 65536, OFF_X = OFF_SLOT + NSLOT * SLOT, OFF_BAR = OFF_X + 1024;
+constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+constexpr uint32_t TM_O = 0, TM_S = 256;
+constexpr int kThreads = 320, kSoft = 256, kWarpTma = 8, kWarpMma = 9;
+}  // namespace fw
 
-// warp = one query row: delta, then dq
-__global__ void __launch_bounds__(128) mqa_dq_kernel(Args a) {
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= (long long)a.B * a.T * a.H) return;
-    const long long tok = row / a.H;
-    const long long b = tok / a.T;
-    const int t = (int)(tok % a.T);
-    float q[8], od[8], g[8] = {}, x[8];
-    load8(a.q_rot + row * D + 8 * lane, q);
-    load8(a.dout + row * D + 8 * lane, od);
-    load8(a.out + row * D + 8 * lane, x);
-    const float delta = dot8(od, x), lse = a.lse[row];
-    if (lane == 0) a.delta[row] = delta;
-    for (int i = a.lo[tok]; i <= t; ++i) {
-        float k[8], v[8];
-        load8(a.k_rot + (b * a.T + i) * D + 8 * lane, k);
-        load8(a.v + (b * a.T + i) * D + 8 * lane, v);
-        const float p = exp2f(dot8(q, k) * a.scale_log2 - lse);
-        const float ds = p * (dot8(od, v) - delta);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = fmaf(ds, k[e], g[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] *= a.scale;
-    turn_back_store(g, a.cs + (size_t)t * (D / 2), lane, a.dq + row * D);
-}
+__global__ void __launch_bounds__(fw::kThreads, 1)
+mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v, const Args a) {
+    using namespace fw;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    const uint32_t bars = sb + OFF_BAR;
+    const uint32_t q_full = bars, q_empty = bars + 8, o_free = bars + 16, mma_done = bars + 24;
+    auto s_full = [&](uint32_t i) { return bars + 32 + 8 * i; };
+    auto p_full = [&](uint32_t i) { return bars + 48 + 8 * i; };
+    auto o_done = [&](uint32_t i) { return bars + 64 + 8 * i; };
+    auto full = [&](uint32_t s) { return bars + 80 + 8 * s; };
+    auto empty = [&](uint32_t s) { return bars + 80 + 8 * NSLOT + 8 * s; };
+    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 80 + 16 * NSLOT);
+    float* xch = reinterpret_cast<float*>(smem + OFF_X);
+    const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 96 + 16 * NSLOT), a.status, a.timeout_ns};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
-// warp = one key: every query row that sees it (lo_t is non-decreasing in t)
-__global__ void __launch_bounds__(128) mqa_dkv_kernel(Args a) {
-    const long long key = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (key >= (long long)a.B * a.T) return;
-    const long long b = key / a.T;
-    const int i = (int)(key % a.T);
-    float k[8], v[8], gk[8] = {}, gv[8] = {};
-    load8(a.k_rot + key * D + 8 * lane, k);
-    load8(a.v + key * D + 8 * lane, v);
-    for (int t = i; t < a.T && a.lo[b * a.T + t] <= i; ++t)
-        for (int h = 0; h < a.H; ++h) {
-            const long long row = (b * a.T + t) * a.H + h;
-            float q[8], od[8];
-            load8(a.q_rot + row * D + 8 * lane, q);
-            load8(a.dout + row * D + 8 * lane, od);
-            const float p = exp2f(dot8(q, k) * a.scale_log2 - a.lse[row]);
-            const float ds = p * (dot8(od, v) - a.delta[row]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                gk[e] = fmaf(ds, q[e], gk[e]);
-                gv[e] = fmaf(p, od[e], gv[e]);
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(o_free, 16);
+        mbar_init(mma_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(p_full(i), 16);
+            mbar_init(o_done(i), 1);
+        }
+        for (int i = 0; i < NSLOT; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        *g.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc_pair(smem_u32((const void*)tmem_s), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_s;
+    QTile t{};
+
+    if (warp == kWarpTma) {
+        if (lane == 0) {
+            const uint32_t lead = map_to_rank(bars, 0) - bars;      // this CTA's barrier address -> the leader's
+            uint32_t L = 0;
+            int k = 0;
+            bool ok = true;
+            // key tile j of the values (v) or keys into the next slot
+            auto load = [&](bool v, int j) {
+                const uint32_t s = L % NSLOT, u = L / NSLOT;
+                if (u > 0 && !wait(empty(s), (u - 1) & 1, g, 1)) return false;
+                if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * SLOT);
+                const uint32_t dst = sb + OFF_SLOT + s * SLOT, bar = full(s) + lead;
+                const int key0 = t.lo + j * BK;
+                if (v) {
+                    for (int c = 0; c < 2; ++c)
+                        tma_load_3d_pair(dst + c * 16384, &map_v, (int)rank * 128 + c * 64, key0, t.b, bar);
+                } else {
+                    for (int c = 0; c < 4; ++c)
+                        tma_load_3d_pair(dst + c * 8192, &map_k, c * 64, key0 + (int)rank * 64, t.b, bar);
+                }
+                ++L;
+                return true;
+            };
+            for (; ok && q_tile<BK>(a, pair, npairs, k, t); ++k) {
+                ok = load(false, 0);                                 // keys first: Q's buffer frees later
+                if (ok && k > 0) ok = wait(q_empty, (k - 1) & 1, g, 2);
+                if (!ok) break;
+                if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * 65536);
+                for (int c = 0; c < 4; ++c)
+                    tma_load_3d_pair(sb + OFF_Q + c * 16384, &map_q, c * 64, t.r0 + (int)rank * 128, t.b, q_full + lead);
+                for (int j = 1; ok && j <= t.n; ++j) {
+                    if (j < t.n) ok = load(false, j);
+                    if (ok) ok = load(true, j - 1);
+                }
+            }
+            // no bulk copy may still be writing shared memory at the exit: the leader sees both CTAs' land
+            if (rank == 0) {
+                const uint64_t t0 = globaltimer_ns();
+                for (uint32_t l = L > NSLOT ? L - NSLOT : 0; l < L; ++l)
+                    while (!mbar_try_wait_cluster(full(l % NSLOT), (l / NSLOT) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
+                    }
+                if (k > 0)
+                    while (!mbar_try_wait_cluster(q_full, (k - 1) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
+                    }
             }
         }
+    } else if (warp == kWarpMma) {
+        if (rank == 0) {
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t id_s = idesc_bf16(256, BK, 0), id_o = idesc_bf16(256, D, 1);
+            uint32_t L = 0, gt = 0;                                  // slots used, key tiles before this query tile
+            bool ok = true;
+            for (int k = 0; ok && q_tile<BK>(a, pair, npairs, k, t); ++k) {
+                if (!(ok = wait_w(q_full, k & 1, g, 3))) break;
+                for (int j = 0; ok && j <= t.n; ++j) {
+                    if (j < t.n) {                                   // S_j
+                        const uint32_t s = L % NSLOT, buf = (gt + j) & 1;
+                        if (!(ok = wait_w(full(s), (L / NSLOT) & 1, g, 4))) break;
+                        ++L;
+                        tc_fence_after();
+                        if (elect_one()) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) gk[e] *= a.scale;
-    store8(gv, a.dv + key * D + 8 * lane);
-    turn_back_store(gk, a.cs + (size_t)i * (D / 2), lane, a.dk + key * D);
+                            for (int ks = 0; ks < D / 16; ++ks)
+                                mma_ss_pair(tm + TM_S + buf * BK, desc_k_sw128(sb + OFF_Q + (ks >> 2) * 16384 + (ks & 3) * 32),
+                                            desc_k_sw128(sb + OFF_SLOT + s * SLOT + (ks >> 2) * 8192 + (ks & 3) * 32), id_s,
+                                            ks > 0 ? 1u : 0u);
+                            mma_commit_pair(s_full(buf));
+                            mma_commit_pair(empty(s));
+                            if (j == t.n - 1) mma_commit_pair(q_empty);
+                        }
+                        __syncwarp();
+                    }
+                    if (j >= 1) {                                    // O += P_{j-1} V_{j-1}
+                        const uint32_t i = gt + j - 1, buf = i & 1, s = L % NSLOT;
+                        if (j == 1 && k > 0 && !(ok = wait_w(o_free, (k - 1) & 1, g, 5))) break;
+                        if (!(ok = wait_w(p_full(buf), (i >> 1) & 1, g, 6))) break;
+                        if (!(ok = wait_w(full(s), (L / NSLOT) & 1, g, 7))) break;
+                        ++L;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            // P of keys [16 ks, 16 ks + 16): the two halves of a row sit 64 columns apart
+#pragma unroll
+                            for (int ks = 0; ks < BK / 16; ++ks)
+                                mma_ts_pair(tm + TM_O, tm + TM_S + buf * BK + (ks >> 2) * 64 + (ks & 3) * 8,
+                                            desc_mn_sw128(sb + OFF_SLOT + s * SLOT + ks * 2048, 16384), id_o,
+                                            (j > 1 || ks > 0) ? 1u : 0u);
+                            mma_commit_pair(o_done(buf));
+                            mma_commit_pair(empty(s));
+                        }
+                        __syncwarp();
+                    }
+                }
+                gt += t.n;
+            }
+            if (elect_one()) mma_commit_pair(mma_done);              // every MMA is over before TMEM is released
+            __syncwarp();
+        }
+        if (lane == 0) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait_cluster(mma_done, 0) && globaltimer_ns() - t0 < 4 * a.timeout_ns) {
+            }
+        }
+        __syncwarp();
+    } else {
+        // softmax: row r of this CTA's 128, keys [64 half, 64 half + 64) of each tile
+        const int r = (warp & 3) * 32 + lane, half = warp >> 2;
+        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t lead_p = map_to_rank(p_full(0), 0), lead_free = map_to_rank(o_free, 0);
+        uint32_t gt = 0;
+        bool ok = true, stop = false;
+        for (int k = 0; !stop && q_tile<BK>(a, pair, npairs, k, t); ++k) {
+            const int row0 = t.r0 + (int)rank * 128, row = row0 + r;
+            const int tok = min(row, a.TH - 1) / a.H;
+            const int lo_row = a.lo[(size_t)t.b * a.T + tok];
+            // a tile inside every row's keys needs no mask: [lo of the CTA's last token, its first token]
+            const int full_lo = a.lo[(size_t)t.b * a.T + min(row0 + 127, a.TH - 1) / a.H], full_hi = min(row0, a.TH - 1) / a.H;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < t.n; ++j) {
+                const uint32_t i = gt + j, buf = i & 1;
+                ok = ok && wait_w(s_full(buf), (i >> 1) & 1, g, 8);
+                tc_fence_after();
+                float s[64];
+                tmem_ld32(tl + TM_S + buf * BK + half * 64, s);
+                tmem_ld32(tl + TM_S + buf * BK + half * 64 + 32, s + 32);
+                tmem_wait_ld();
+                const int key0 = t.lo + j * BK + half * 64;
+                float mx = -INFINITY;
+                if (t.lo + j * BK >= full_lo && t.lo + j * BK + BK - 1 <= full_hi) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) mx = fmaxf(mx, s[c]);
+                } else {
+                    const int c_lo = lo_row - key0, c_hi = tok - key0;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) {
+                        s[c] = (c >= c_lo && c <= c_hi) ? s[c] : -INFINITY;
+                        mx = fmaxf(mx, s[c]);
+                    }
+                }
+                mx *= a.scale_log2;
+                if (bar_or(mx > m + 8.0f || !ok, kSoft)) {           // some row of the CTA moves (or a wait failed)
+                    xch[half * 128 + r] = mx;
+                    if (bar_or(!ok, kSoft)) {
+                        stop = true;
+                        break;
+                    }
+                    mx = fmaxf(xch[r], xch[128 + r]);
+                    const bool move = mx > m + 8.0f;
+                    const float f = move && m != -INFINITY ? ex2_approx(m - mx) : 1.0f;
+                    if (move) m = mx;
+                    l *= f;
+                    if (j > 0) {
+                        ok = wait_w(o_done((i - 1) & 1), ((i - 1) >> 1) & 1, g, 9);
+                        tc_fence_after();
+                        if (__any_sync(0xffffffffu, f != 1.0f)) {
+#pragma unroll 1
+                            for (int c = half * 128; c < half * 128 + 128; c += 16) {
+                                float o[16];
+                                tmem_ld16(tl + TM_O + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] *= f;
+                                tmem_st16f(tl + TM_O + c, o);
+                            }
+                        }
+                    }
+                }
+                const float nm = m == -INFINITY ? 0.f : -m;
+                uint32_t p[32];
+                float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float p0 = ex2_approx(fmaf(s[2 * c], a.scale_log2, nm));
+                    const float p1 = ex2_approx(fmaf(s[2 * c + 1], a.scale_log2, nm));
+                    l0 += p0;
+                    l1 += p1;
+                    p[c] = bf16x2(p0, p1);
+                }
+                l += l0 + l1;
+                tmem_st32(tl + TM_S + buf * BK + half * 64, p);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(lead_p + 8 * buf);
+            }
+            if (stop) break;
+            // the row's sum from its two threads, then out = O / l
+            const uint32_t i = gt + t.n - 1;
+            ok = ok && wait_w(o_done(i & 1), (i >> 1) & 1, g, 10);
+            xch[half * 128 + r] = l;
+            if (bar_or(!ok, kSoft)) break;
+            l = xch[r] + xch[128 + r];
+            tc_fence_after();
+            const float inv = 1.0f / l;
+            __nv_bfloat16* orow = a.out + ((size_t)t.b * a.TH + row) * D + half * 128;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                float o[32];
+                tmem_ld32(tl + TM_O + half * 128 + c, o);
+                tmem_wait_ld();
+                if (row < a.TH) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        reinterpret_cast<uint4*>(orow + c)[e] =
+                            make_uint4(bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                       bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                }
+            }
+            if (half == 0 && row < a.TH) a.lse[(size_t)t.b * a.THp + row] = m + log2f(l);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead_free);
+            gt += t.n;
+        }
+        tmem_wait_ld();
+        tmem_wait_st();
+    }
+    // no CTA of the pair leaves while the other may still reach its shared memory or TMEM
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
 }
 
-// What the forward keeps: lse, first keys, angles, the rotated queries and keys.
+// ---------------------------------------------------------------- backward: dq ------------------------
+// A CTA pair takes 256 query rows again and walks their keys in tiles of 64:
+//   S = Q K^T,  dP = dO V^T   (M 256, N 64, K 256; Q in TMEM, dO in shared memory)
+//   dQ += dS K                (M 256, N 256, K 64; dS in TMEM over its dP)
+// TMEM: dQ 256 columns, Q 128, S 64, dP 64.  A CTA loads 32 keys of every K and V tile and 128 columns of
+// every K tile (48 KB per 64 keys).  8 warps, thread = (row, 32 of the 64 keys): P = 2^(c s - L) and
+// dS = P (dP - delta) with the row's L and delta in registers.  The tensor pipe runs S of tile j + 1 while
+// dS of tile j is formed, and dQ of tile j and dP of tile j + 1 while P of tile j + 1 is.
+namespace bq {
+constexpr int BK = 64;
+constexpr uint32_t SLOT = 16384;
+constexpr int NSLOT = 10;
+constexpr uint32_t OFF_DO = 0, OFF_SLOT = 65536, OFF_BAR = OFF_SLOT + NSLOT * SLOT;
+constexpr uint32_t SMEM_BYTES = OFF_BAR + 512 + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+constexpr uint32_t TM_DQ = 0, TM_Q = 256, TM_S = 384, TM_DP = 448;
+constexpr int kThreads = 320, kWarpTma = 8, kWarpMma = 9;
+}  // namespace bq
+
+__global__ void __launch_bounds__(bq::kThreads, 1)
+mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+              const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUtensorMap map_vs,
+              const __grid_constant__ CUtensorMap map_kd, const Args a) {
+    using namespace bq;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    const uint32_t bars = sb + OFF_BAR;
+    const uint32_t q_full = bars, q_tmem = bars + 8, do_full = bars + 16, do_empty = bars + 24, s_full = bars + 32,
+                   s_free = bars + 40, dp_full = bars + 48, ds_full = bars + 56, dq_done = bars + 64, dq_free = bars + 72,
+                   mma_done = bars + 80;
+    auto full = [&](uint32_t s) { return bars + 96 + 8 * s; };
+    auto empty = [&](uint32_t s) { return bars + 96 + 8 * NSLOT + 8 * s; };
+    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 96 + 16 * NSLOT);
+    const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 112 + 16 * NSLOT), a.status, a.timeout_ns};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_tmem, 16);
+        mbar_init(do_full, 1);
+        mbar_init(do_empty, 1);
+        mbar_init(s_full, 1);
+        mbar_init(s_free, 16);
+        mbar_init(dp_full, 1);
+        mbar_init(ds_full, 16);
+        mbar_init(dq_done, 1);
+        mbar_init(dq_free, 16);
+        mbar_init(mma_done, 1);
+        for (int i = 0; i < NSLOT; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        *g.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc_pair(smem_u32((const void*)tmem_s), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_s;
+    QTile t{};
+
+    // Slots in order, per query tile: the four 64-wide column blocks of Q (to TMEM), then Ks_0, Vs_0 and for
+    // every j >= 1 Ks_j, Kd_{j-1}, Vs_j, and Kd_{n-1}: the order of the MMAs.
+    if (warp == kWarpTma) {
+        if (lane == 0) {
+            const uint32_t lead = map_to_rank(bars, 0) - bars;
+            uint32_t L = 0;
+            int k = 0;
+            bool ok = true;
+            auto next = [&](uint32_t& s) {                           // wait until the next slot is free
+                s = L % NSLOT;
+                const uint32_t u = L / NSLOT;
+                ++L;
+                return u == 0 || wait(empty(s), (u - 1) & 1, g, 1);
+            };
+            auto load = [&](const CUtensorMap* m, int j) {           // 32 keys of tile j, all columns
+                uint32_t s;
+                if (!next(s)) return false;
+                if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * SLOT);
+                for (int c = 0; c < 4; ++c)
+                    tma_load_3d_pair(sb + OFF_SLOT + s * SLOT + c * 4096, m, c * 64, t.lo + j * BK + (int)rank * 32, t.b,
+                                     full(s) + lead);
+                return true;
+            };
+            auto load_d = [&](int j) {                               // all 64 keys of tile j, 128 columns
+                uint32_t s;
+                if (!next(s)) return false;
+                if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * SLOT);
+                for (int c = 0; c < 2; ++c)
+                    tma_load_3d_pair(sb + OFF_SLOT + s * SLOT + c * 8192, &map_kd, (int)rank * 128 + c * 64, t.lo + j * BK, t.b,
+                                     full(s) + lead);
+                return true;
+            };
+            for (; ok && q_tile<BK>(a, pair, npairs, k, t); ++k) {
+                // Q's blocks complete on a barrier of this CTA: its own warps move them to TMEM
+                if (k > 0 && !(ok = wait(q_full, (k - 1) & 1, g, 13))) break;   // its last phase is over
+                mbar_arrive_expect_tx(q_full, 4 * SLOT);
+                for (int c = 0; ok && c < 4; ++c) {
+                    uint32_t s;
+                    if (!(ok = next(s))) break;
+                    if (rank == 0) mbar_arrive(full(s));             // keeps the slot's phase in step
+                    tma_load_3d(sb + OFF_SLOT + s * SLOT, &map_q, c * 64, t.r0 + (int)rank * 128, t.b, q_full);
+                }
+                ok = ok && load(&map_ks, 0);
+                if (ok && k > 0) ok = wait(do_empty, (k - 1) & 1, g, 2);
+                if (!ok) break;
+                if (rank == 0) mbar_arrive_expect_tx(do_full, 2 * 65536);
+                for (int c = 0; c < 4; ++c)
+                    tma_load_3d_pair(sb + OFF_DO + c * 16384, &map_do, c * 64, t.r0 + (int)rank * 128, t.b, do_full + lead);
+                ok = load(&map_vs, 0);
+                for (int j = 1; ok && j <= t.n; ++j) {
+                    if (j < t.n) ok = load(&map_ks, j);
+                    ok = ok && load_d(j - 1);
+                    if (j < t.n) ok = ok && load(&map_vs, j);
+                }
+            }
+            // no bulk copy may still be writing shared memory at the exit
+            const uint64_t t0 = globaltimer_ns();
+            if (k > 0)
+                while (!mbar_try_wait_cluster(q_full, (k - 1) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
+                }
+            if (rank == 0) {
+                for (uint32_t l = L > NSLOT ? L - NSLOT : 0; l < L; ++l)
+                    while (!mbar_try_wait_cluster(full(l % NSLOT), (l / NSLOT) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
+                    }
+                if (k > 0)
+                    while (!mbar_try_wait_cluster(do_full, (k - 1) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
+                    }
+            }
+        }
+    } else if (warp == kWarpMma) {
+        if (rank == 0) {
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t id_s = idesc_bf16(256, BK, 0), id_q = idesc_bf16(256, D, 1);
+            uint32_t L = 0, gt = 0;
+            bool ok = true;
+            auto ready = [&](uint32_t& s) {                          // the next slot's data
+                s = L % NSLOT;
+                const uint32_t u = L / NSLOT;
+                ++L;
+                return wait_w(full(s), u & 1, g, 3);
+            };
+            auto issue_s = [&]() {
+                uint32_t s;
+                if (!ready(s)) return false;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_ts_pair(tm + TM_S, tm + TM_Q + ks * 8,
+                                    desc_k_sw128(sb + OFF_SLOT + s * SLOT + (ks >> 2) * 4096 + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
+                    mma_commit_pair(s_full);
+                    mma_commit_pair(empty(s));
+                }
+                __syncwarp();
+                return true;
+            };
+            auto issue_dp = [&](bool last) {
+                uint32_t s;
+                if (!ready(s)) return false;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_ss_pair(tm + TM_DP, desc_k_sw128(sb + OFF_DO + (ks >> 2) * 16384 + (ks & 3) * 32),
+                                    desc_k_sw128(sb + OFF_SLOT + s * SLOT + (ks >> 2) * 4096 + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
+                    mma_commit_pair(dp_full);
+                    mma_commit_pair(empty(s));
+                    if (last) mma_commit_pair(do_empty);
+                }
+                __syncwarp();
+                return true;
+            };
+            for (int k = 0; ok && q_tile<BK>(a, pair, npairs, k, t); ++k) {
+                if (!(ok = wait_w(q_tmem, k & 1, g, 4))) break;      // both CTAs' Q are in TMEM
+                tc_fence_after();
+                if (elect_one())
+                    for (int c = 0; c < 4; ++c) mma_commit_pair(empty((L + c) % NSLOT));
+                __syncwarp();
+                L += 4;
+                if (!(ok = issue_s())) break;
+                if (!(ok = wait_w(do_full, k & 1, g, 5))) break;
+                if (!(ok = issue_dp(t.n == 1))) break;
+                for (int j = 0; ok && j < t.n; ++j) {
+                    const uint32_t par = (gt + j) & 1;
+                    if (j + 1 < t.n) {
+                        if (!(ok = wait_w(s_free, par, g, 6))) break;
+                        if (!(ok = issue_s())) break;
+                    }
+                    if (!(ok = wait_w(ds_full, par, g, 7))) break;
+                    if (j == 0 && k > 0 && !(ok = wait_w(dq_free, (k - 1) & 1, g, 8))) break;
+                    uint32_t s;
+                    if (!(ok = ready(s))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        // dS of keys [16 ks, 16 ks + 16): the two halves of a row sit 32 columns apart
+#pragma unroll
+                        for (int ks = 0; ks < BK / 16; ++ks)
+                            mma_ts_pair(tm + TM_DQ, tm + TM_DP + (ks >> 1) * 32 + (ks & 1) * 8,
+                                        desc_mn_sw128(sb + OFF_SLOT + s * SLOT + ks * 2048, 8192), id_q,
+                                        (j > 0 || ks > 0) ? 1u : 0u);
+                        mma_commit_pair(empty(s));
+                        if (j == t.n - 1) mma_commit_pair(dq_done);
+                    }
+                    __syncwarp();
+                    if (j + 1 < t.n && !(ok = issue_dp(j + 2 == t.n))) break;
+                }
+                gt += t.n;
+            }
+            if (elect_one()) mma_commit_pair(mma_done);
+            __syncwarp();
+        }
+        if (lane == 0) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait_cluster(mma_done, 0) && globaltimer_ns() - t0 < 4 * a.timeout_ns) {
+            }
+        }
+        __syncwarp();
+    } else {
+        const int r = (warp & 3) * 32 + lane, half = warp >> 2;
+        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t lead = map_to_rank(bars, 0) - bars;
+        uint32_t L = 0, gt = 0;
+        for (int k = 0; q_tile<BK>(a, pair, npairs, k, t); ++k) {
+            const int row0 = t.r0 + (int)rank * 128, row = row0 + r;
+            const bool live = row < a.TH;
+            const int tok = min(row, a.TH - 1) / a.H;
+            const int lo_row = live ? a.lo[(size_t)t.b * a.T + tok] : 0x7fffffff;   // a row past the end sees no key
+            const int full_lo = row0 + 127 < a.TH ? a.lo[(size_t)t.b * a.T + (row0 + 127) / a.H] : 0x7fffffff;
+            const int full_hi = min(row0, a.TH - 1) / a.H;
+            const float lse = live ? a.lse[(size_t)t.b * a.THp + row] : 0.f;
+            const float delta = live ? a.delta[(size_t)t.b * a.THp + row] : 0.f;
+            // Q: shared memory (rows of 128 bytes, 16-byte chunks swizzled by the row) to TMEM
+            if (!wait_w(q_full, k & 1, g, 9)) break;
+            for (int c = 2 * half; c < 2 * half + 2; ++c) {
+                const uint8_t* src = smem + OFF_SLOT + ((L + c) % NSLOT) * SLOT + r * 128;
+                uint32_t v[32];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    *reinterpret_cast<uint4*>(v + 4 * e) = *reinterpret_cast<const uint4*>(src + ((e ^ (r & 7)) << 4));
+                tmem_st32(tl + TM_Q + c * 32, v);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(q_tmem + lead);
+            L += 4 + 3 * t.n;
+            bool ok = true;
+            for (int j = 0; j < t.n; ++j) {
+                const uint32_t par = (gt + j) & 1;
+                if (!(ok = wait_w(s_full, par, g, 10))) break;
+                tc_fence_after();
+                float s[32], dp[32];
+                tmem_ld32(tl + TM_S + half * 32, s);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(s_free + lead);
+                const int key0 = t.lo + j * BK;
+                const bool whole = key0 >= full_lo && key0 + BK - 1 <= full_hi;
+                const int c_lo = lo_row - (key0 + half * 32), c_hi = tok - (key0 + half * 32);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    s[c] = ex2_approx(fmaf(s[c], a.scale_log2, -lse));
+                    if (!whole) s[c] = (c >= c_lo && c <= c_hi) ? s[c] : 0.f;
+                }
+                if (!(ok = wait_w(dp_full, par, g, 11))) break;
+                tc_fence_after();
+                tmem_ld32(tl + TM_DP + half * 32, dp);
+                tmem_wait_ld();
+                uint32_t v[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    v[c] = bf16x2(s[2 * c] * (dp[2 * c] - delta), s[2 * c + 1] * (dp[2 * c + 1] - delta));
+                tmem_st16(tl + TM_DP + half * 32, v);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(ds_full + lead);
+            }
+            if (!ok || !wait_w(dq_done, k & 1, g, 12)) break;
+            gt += t.n;
+            tc_fence_after();
+            // turn back: columns [64 half, +64) and their partners 128 further
+            __nv_bfloat16* orow = a.dq + ((size_t)t.b * a.TH + row) * D + half * 64;
+            const float4* cs = reinterpret_cast<const float4*>(a.cs + (size_t)tok * (D / 2) + half * 64);
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 16) {
+                float x1[16], x2[16];
+                tmem_ld16(tl + TM_DQ + half * 64 + c, x1);
+                tmem_ld16(tl + TM_DQ + 128 + half * 64 + c, x2);
+                tmem_wait_ld();
+                if (live) {
+                    uint32_t o1[8], o2[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 f = cs[c / 2 + e];              // (cos, sin) of two pairs
+                        const float y0 = x1[2 * e] * a.scale, y1 = x1[2 * e + 1] * a.scale;
+                        const float z0 = x2[2 * e] * a.scale, z1 = x2[2 * e + 1] * a.scale;
+                        o1[e] = bf16x2(y0 * f.x + z0 * f.y, y1 * f.z + z1 * f.w);
+                        o2[e] = bf16x2(z0 * f.x - y0 * f.y, z1 * f.z - y1 * f.w);
+                    }
+                    reinterpret_cast<uint4*>(orow + c)[0] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+                    reinterpret_cast<uint4*>(orow + c)[1] = make_uint4(o1[4], o1[5], o1[6], o1[7]);
+                    reinterpret_cast<uint4*>(orow + 128 + c)[0] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+                    reinterpret_cast<uint4*>(orow + 128 + c)[1] = make_uint4(o2[4], o2[5], o2[6], o2[7]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(dq_free + lead);
+        }
+        tmem_wait_ld();
+        tmem_wait_st();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- backward: dk, dv --------------------
+// A cluster of two CTAs takes 128 keys and walks the query rows that see them in tiles of 64 rows:
+//   CTA 0:  S^T  = K Q^T   (M 128, N 64, K 256; K in TMEM),   dV += P^T dO    (M 128, N 256, K 64)
+//   CTA 1:  dP^T = V dO^T  (the same, V in TMEM),             dK += dS^T Q
+// The two fp32 accumulators of a key tile are 256 TMEM columns each, a CTA's whole TMEM together; so each CTA
+// keeps one, 128 columns of its stationary operand and two buffers of 64 for S^T or dP^T, over which
+// P^T or dS^T is written in bf16 as the A operand of the second product.  CTA 0 hands its P^T to CTA 1
+// through distributed shared memory (16 KB a tile, two buffers).  Thread = (key, 64 rows); two
+// warpgroups take every other tile.
+// The (key tile, row tile) products of all key tiles form one line, cut into equal pieces for the clusters
+// (cum = the line's length before each key tile), so that every cluster has the same work whatever the
+// documents; a piece of a key tile leaves its sums in fp32 as part number (cluster + key tile), and
+// mqa_dkv_sum_kernel adds the parts of a key tile in order: the same bits at every run.
+namespace bk {
+constexpr int BR = 64, BKEY = 128;
+constexpr uint32_t STAGE = 65536;
+constexpr int NST = 3;
+constexpr uint32_t OFF_P = NST * STAGE, OFF_VEC = OFF_P + 2 * 16384, OFF_BAR = OFF_VEC + NST * 256;
+constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+constexpr uint32_t TM_ACC = 0, TM_A = 256, TM_S = 384;
+constexpr int kThreads = 320, kWarpTma = 8, kWarpMma = 9;
+constexpr size_t PART_FLOATS = (size_t)BKEY * D;         // of one gradient: [D / 4][128 keys][4]
+}  // namespace bk
+
+// where the piece of cluster c of G begins; no piece is empty (clusters past the line's length have none)
+__device__ __forceinline__ int pieces(long long total, int G) { return (int)min((long long)G, total); }
+__device__ __forceinline__ long long piece(long long total, int c, int G) { return total * c / G; }
+
+struct Seg {
+    int j, b, key0, n;              // key tile, its batch row, its first key; row tiles of this piece
+    int r0;                         // first row
+};
+// walks the key tiles of a piece; cum has nk + 1 entries, strictly increasing
+struct Segs {
+    const long long* cum;
+    long long pos, end;
+    int j;
+    __device__ __forceinline__ Segs(const Args& a, int c, int G) : cum(a.cum) {
+        const int nk = a.B * a.nkt;
+        const long long total = cum[nk];
+        G = pieces(total, G);
+        j = 0;
+        pos = end = 0;
+        if (c >= G) return;
+        pos = piece(total, c, G);
+        end = piece(total, c + 1, G);
+        int lo = 0, hi = nk;                             // the last j with cum[j] <= pos
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cum[mid] <= pos) lo = mid; else hi = mid;
+        }
+        j = lo;
+    }
+    __device__ __forceinline__ bool next(const Args& a, Seg& s) {
+        if (pos >= end) return false;
+        const long long c0 = cum[j], c1 = cum[j + 1];
+        s.j = j;
+        s.b = j / a.nkt;
+        s.key0 = (j % a.nkt) * bk::BKEY;
+        s.r0 = s.key0 * a.H + (int)(pos - c0) * bk::BR;
+        s.n = (int)(min(c1, end) - pos);
+        pos += s.n;
+        ++j;
+        return true;
+    }
+};
+
+__global__ void __launch_bounds__(bk::kThreads, 1)
+mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+               const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+               const int* __restrict__ last_t, const Args a) {
+    using namespace bk;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    const uint32_t bars = sb + OFF_BAR;
+    auto full = [&](uint32_t s) { return bars + 8 * s; };
+    auto empty = [&](uint32_t s) { return bars + 24 + 8 * s; };
+    auto s_full = [&](uint32_t i) { return bars + 48 + 8 * i; };
+    auto p_full = [&](uint32_t i) { return bars + 64 + 8 * i; };
+    auto p_here = [&](uint32_t i) { return bars + 80 + 8 * i; };     // CTA 1: P^T has arrived
+    auto p_free = [&](uint32_t i) { return bars + 96 + 8 * i; };     // CTA 0: CTA 1 has read it
+    const uint32_t a_tmem = bars + 112, acc_done = bars + 120, mma_done = bars + 128;
+    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 144);
+    const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 160), a.status, a.timeout_ns};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int cl = blockIdx.x >> 1, G = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(p_full(i), 4);
+            mbar_init(p_here(i), 4);
+            mbar_init(p_free(i), 4);
+        }
+        mbar_init(a_tmem, 8);
+        mbar_init(acc_done, 1);
+        mbar_init(mma_done, 1);
+        *g.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_u32((const void*)tmem_s), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_s;
+    Segs segs(a, cl, G);
+    Seg sg{};
+
+    // Stages in order, per piece of a key tile: the stationary operand [128 keys], then per row tile Q and dO
+    // [64 rows] and the rows' L (CTA 0) or delta (CTA 1).
+    if (warp == kWarpTma) {
+        if (lane == 0) {
+            const CUtensorMap* map_a = rank == 0 ? &map_k : &map_v;
+            const float* vec = rank == 0 ? a.lse : a.delta;
+            uint32_t L = 0;
+            bool ok = true;
+            while (ok && segs.next(a, sg)) {
+                for (int j = -1; j < sg.n; ++j, ++L) {
+                    const uint32_t s = L % NST, u = L / NST, dst = sb + s * STAGE;
+                    if (u > 0 && !(ok = wait(empty(s), (u - 1) & 1, g, 1))) break;
+                    if (j < 0) {
+                        mbar_arrive_expect_tx(full(s), STAGE);
+                        for (int c = 0; c < 4; ++c) tma_load_3d(dst + c * 16384, map_a, c * 64, sg.key0, sg.b, full(s));
+                    } else {
+                        const int r = sg.r0 + j * BR;
+                        mbar_arrive_expect_tx(full(s), STAGE + 256);
+                        for (int c = 0; c < 4; ++c) tma_load_3d(dst + c * 8192, &map_q, c * 64, r, sg.b, full(s));
+                        for (int c = 0; c < 4; ++c) tma_load_3d(dst + 32768 + c * 8192, &map_do, c * 64, r, sg.b, full(s));
+                        bulk_load(sb + OFF_VEC + s * 256, vec + (size_t)sg.b * a.THp + r, 256, full(s));
+                    }
+                }
+            }
+            const uint64_t t0 = globaltimer_ns();
+            for (uint32_t l = L > NST ? L - NST : 0; l < L; ++l)
+                while (!mbar_try_wait(full(l % NST), (l / NST) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
+                }
+        }
+    } else if (warp == kWarpMma) {
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t id_s = idesc_bf16(128, BR, 0), id_a = idesc_bf16(128, D, 1);
+        const uint32_t off_1 = rank == 0 ? 0 : 32768, off_2 = 32768 - off_1;     // rows of the first, second product
+        uint32_t L = 0, gi = 0, ns = 0;
+        bool ok = true;
+        for (; ok && segs.next(a, sg); ++ns) {
+            if (!(ok = wait_w(a_tmem, ns & 1, g, 2))) break;
+            tc_fence_after();
+            if (elect_one()) mma_commit(empty(L % NST));
+            __syncwarp();
+            ++L;
+            for (int j = 0; ok && j <= sg.n; ++j) {
+                if (j < sg.n) {
+                    const uint32_t l = L + j, s = l % NST, buf = (gi + j) & 1;
+                    if (!(ok = wait_w(full(s), (l / NST) & 1, g, 3))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            mma_ts(tm + TM_S + buf * BR, tm + TM_A + ks * 8,
+                                   desc_k_sw128(sb + s * STAGE + off_1 + (ks >> 2) * 8192 + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
+                        mma_commit(s_full(buf));
+                    }
+                    __syncwarp();
+                }
+                if (j >= 1) {
+                    const uint32_t l = L + j - 1, s = l % NST, i = gi + j - 1, buf = i & 1;
+                    if (!(ok = wait_w(p_full(buf), (i >> 1) & 1, g, 4))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < BR / 16; ++ks)
+                            mma_ts(tm + TM_ACC, tm + TM_S + buf * BR + ks * 8,
+                                   desc_mn_sw128(sb + s * STAGE + off_2 + ks * 2048, 8192), id_a, (j > 1 || ks > 0) ? 1u : 0u);
+                        mma_commit(empty(s));
+                        if (j == sg.n) mma_commit(acc_done);
+                    }
+                    __syncwarp();
+                }
+            }
+            L += sg.n;
+            gi += sg.n;
+        }
+        if (elect_one()) mma_commit(mma_done);
+        __syncwarp();
+        if (lane == 0) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(mma_done, 0) && globaltimer_ns() - t0 < a.timeout_ns) {
+            }
+        }
+        __syncwarp();
+    } else {
+        const int r = (warp & 3) * 32 + lane, wg = warp >> 2;
+        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t peer_p = map_to_rank(sb + OFF_P, 1), peer_here = map_to_rank(p_here(0), 1),
+                       peer_free = map_to_rank(p_free(0), 0);
+        uint32_t L = 0, gi = 0, ns = 0;
+        bool ok = true;
+        for (; ok && segs.next(a, sg); ++ns) {
+            // the rows that this thread's key sees: [key H, (last + 1) H)
+            const int key = sg.key0 + r;
+            const int last_key = min(sg.key0 + BKEY, a.T) - 1;
+            const int* lt = last_t + (size_t)sg.b * a.T;
+            const int row_lo = key < a.T ? key * a.H : 0x7fffffff, row_hi = key < a.T ? (lt[key] + 1) * a.H - 1 : -1;
+            // rows that every key of the tile sees
+            const int all_lo = sg.key0 + BKEY <= a.T ? last_key * a.H : 0x7fffffff, all_hi = (lt[sg.key0] + 1) * a.H - 1;
+            if (!(ok = wait_w(full(L % NST), (L / NST) & 1, g, 5))) break;
+            for (int c = 2 * wg; c < 2 * wg + 2; ++c) {
+                const uint8_t* src = smem + (L % NST) * STAGE + c * 16384 + r * 128;
+                uint32_t v[32];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    *reinterpret_cast<uint4*>(v + 4 * e) = *reinterpret_cast<const uint4*>(src + ((e ^ (r & 7)) << 4));
+                tmem_st32(tl + TM_A + c * 32, v);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(a_tmem);
+            ++L;
+            for (int j = 0; j < sg.n; ++j) {
+                const uint32_t i = gi + j, buf = i & 1, u = i >> 1, l = L + j, st = l % NST;
+                if ((int)buf != wg) continue;
+                if (!(ok = wait_w(full(st), (l / NST) & 1, g, 6))) break;      // L or delta
+                if (!(ok = wait_w(s_full(buf), u & 1, g, 7))) break;
+                tc_fence_after();
+                float s[64];
+                tmem_ld32(tl + TM_S + buf * BR, s);
+                tmem_ld32(tl + TM_S + buf * BR + 32, s + 32);
+                const float4* vec = reinterpret_cast<const float4*>(smem + OFF_VEC + st * 256);
+                const int r0 = sg.r0 + j * BR;
+                const bool whole = r0 >= all_lo && r0 + BR - 1 <= all_hi;
+                const int c_lo = row_lo - r0, c_hi = row_hi - r0;
+                uint32_t v[32];
+                if (rank == 0) {
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float4 f = vec[c];
+                        s[4 * c] = ex2_approx(fmaf(s[4 * c], a.scale_log2, -f.x));
+                        s[4 * c + 1] = ex2_approx(fmaf(s[4 * c + 1], a.scale_log2, -f.y));
+                        s[4 * c + 2] = ex2_approx(fmaf(s[4 * c + 2], a.scale_log2, -f.z));
+                        s[4 * c + 3] = ex2_approx(fmaf(s[4 * c + 3], a.scale_log2, -f.w));
+                    }
+                    if (!whole) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) s[c] = (c >= c_lo && c <= c_hi) ? s[c] : 0.f;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[c] = bf16x2(s[2 * c], s[2 * c + 1]);
+                    tmem_st32(tl + TM_S + buf * BR, v);
+                    // the same to CTA 1, 16 bytes of every thread side by side
+                    if (u > 0 && !(ok = wait_w(p_free(buf), (u - 1) & 1, g, 8))) break;
+                    const uint32_t dst = peer_p + buf * 16384 + r * 16;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + c * 2048), "r"(v[4 * c]),
+                                     "r"(v[4 * c + 1]), "r"(v[4 * c + 2]), "r"(v[4 * c + 3])
+                                     : "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(peer_here + 8 * buf);
+                } else {
+                    if (!(ok = wait_w(p_here(buf), u & 1, g, 9))) break;
+                    const uint8_t* src = smem + OFF_P + buf * 16384 + r * 16;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(v + 4 * c) = *reinterpret_cast<const uint4*>(src + c * 2048);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(peer_free + 8 * buf);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float4 f = vec[c];
+                        s[4 * c] = __uint_as_float(v[2 * c] << 16) * (s[4 * c] - f.x);
+                        s[4 * c + 1] = __uint_as_float(v[2 * c] & 0xffff0000u) * (s[4 * c + 1] - f.y);
+                        s[4 * c + 2] = __uint_as_float(v[2 * c + 1] << 16) * (s[4 * c + 2] - f.z);
+                        s[4 * c + 3] = __uint_as_float(v[2 * c + 1] & 0xffff0000u) * (s[4 * c + 3] - f.w);
+                    }
+                    if (!whole) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) s[c] = (c >= c_lo && c <= c_hi) ? s[c] : 0.f;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[c] = bf16x2(s[2 * c], s[2 * c + 1]);
+                    tmem_st32(tl + TM_S + buf * BR, v);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(buf));
+            }
+            L += sg.n;
+            gi += sg.n;
+            if (!ok || !(ok = wait_w(acc_done, ns & 1, g, 10))) break;
+            tc_fence_after();
+            float4* part = reinterpret_cast<float4*>(a.part + ((size_t)(cl + sg.j) * 2 + rank) * PART_FLOATS);
+#pragma unroll 1
+            for (int c = wg * 128; c < wg * 128 + 128; c += 32) {
+                float o[32];
+                tmem_ld32(tl + TM_ACC + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    part[(c / 4 + e) * BKEY + r] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+            tc_fence_before();
+        }
+        tmem_wait_ld();
+        tmem_wait_st();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// The sum of a key tile's parts in the clusters' order; dk is scaled and turned back.  Block = (key tile,
+// 32 columns: 16 of the first half with their partners for dk), thread = key; z = 0: dv, 1: dk.
+__global__ void __launch_bounds__(bk::BKEY) mqa_dkv_sum_kernel(const Args a, int G) {
+    using namespace bk;
+    const int j = blockIdx.x, z = blockIdx.z, r = threadIdx.x;
+    const long long total = a.cum[a.B * a.nkt], x0 = a.cum[j], x1 = a.cum[j + 1] - 1;
+    G = pieces(total, G);
+    auto cluster_of = [&](long long x) {
+        int c = (int)(x * G / total);
+        while (piece(total, c + 1, G) <= x) ++c;
+        while (piece(total, c, G) > x) --c;
+        return c;
+    };
+    const int c0 = cluster_of(x0), c1 = cluster_of(x1);
+    const int b = j / a.nkt, key = (j % a.nkt) * BKEY + r;
+    const int col1 = z == 0 ? blockIdx.y * 32 : blockIdx.y * 16, col2 = z == 0 ? col1 + 16 : col1 + 128;
+    float x[16] = {}, y[16] = {};
+    for (int c = c0; c <= c1; ++c) {
+        const float4* part = reinterpret_cast<const float4*>(a.part + ((size_t)(c + j) * 2 + z) * PART_FLOATS);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float4 u = part[(col1 / 4 + e) * BKEY + r], v = part[(col2 / 4 + e) * BKEY + r];
+            x[4 * e] += u.x; x[4 * e + 1] += u.y; x[4 * e + 2] += u.z; x[4 * e + 3] += u.w;
+            y[4 * e] += v.x; y[4 * e + 1] += v.y; y[4 * e + 2] += v.z; y[4 * e + 3] += v.w;
+        }
+    }
+    if (key >= a.T) return;
+    if (z == 1) {
+        const float2* cs = a.cs + (size_t)key * (D / 2) + col1;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float2 f = cs[e];
+            const float u = x[e] * a.scale, v = y[e] * a.scale;
+            x[e] = u * f.x + v * f.y;
+            y[e] = v * f.x - u * f.y;
+        }
+    }
+    __nv_bfloat16* o = (z == 0 ? a.dv : a.dk) + ((size_t)b * a.T + key) * D;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        reinterpret_cast<uint4*>(o + col1)[e] =
+            make_uint4(pr::bf16x2(x[8 * e], x[8 * e + 1]), pr::bf16x2(x[8 * e + 2], x[8 * e + 3]),
+                       pr::bf16x2(x[8 * e + 4], x[8 * e + 5]), pr::bf16x2(x[8 * e + 6], x[8 * e + 7]));
+        reinterpret_cast<uint4*>(o + col2)[e] =
+            make_uint4(pr::bf16x2(y[8 * e], y[8 * e + 1]), pr::bf16x2(y[8 * e + 2], y[8 * e + 3]),
+                       pr::bf16x2(y[8 * e + 4], y[8 * e + 5]), pr::bf16x2(y[8 * e + 6], y[8 * e + 7]));
+    }
+}
+
+// ---------------------------------------------------------------- backward: delta, the dk / dv line ----
+// delta = dO . out per query row (a warp a row); the last block adds up the row tiles of the key tiles
+__global__ void __launch_bounds__(1024) mqa_delta_kernel(const Args a, const __nv_bfloat16* dout, const int* last_t,
+                                                         long long* cum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.x == gridDim.x - 1) {
+        __shared__ long long warp_v[32];
+        const int nk = a.B * a.nkt;
+        long long carry = 0;
+        if (threadIdx.x == 0) cum[0] = 0;
+        for (int j0 = 0; j0 < nk; j0 += 1024) {
+            const int j = j0 + threadIdx.x;
+            long long v = 0;
+            if (j < nk) {
+                // rows [key0 H, (last + 1) H): up to the last token that the tile's last key is seen by
+                const int b = j / a.nkt, key0 = (j % a.nkt) * bk::BKEY, key1 = min(key0 + bk::BKEY, a.T) - 1;
+                v = ((long long)(last_t[(size_t)b * a.T + key1] + 1 - key0) * a.H + bk::BR - 1) / bk::BR;
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (lane == 31) warp_v[warp] = v;
+            __syncthreads();
+            long long base = carry;
+            for (int i = 0; i < 32; ++i) {
+                if (i < warp) base += warp_v[i];
+                carry += warp_v[i];
+            }
+            if (j < nk) cum[j + 1] = base + v;
+            __syncthreads();
+        }
+        return;
+    }
+    const long long row = (long long)blockIdx.x * 32 + warp;
+    if (row >= (long long)a.B * a.TH) return;
+    const uint4 x = reinterpret_cast<const uint4*>(dout + row * D)[lane], y = reinterpret_cast<const uint4*>(a.out + row * D)[lane];
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
+        s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) a.delta[row / a.TH * a.THp + row % a.TH] = s;
+}
+
+// What the forward keeps: lse, first keys and last queries, angles, the rotated queries and keys.
 struct SaveLayout {
-    size_t lse, lo, cs, q_rot, k_rot, total;
+    size_t lse, lo, last, cs, q_rot, k_rot, total;
 };
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+inline size_t row_pitch(const rglru_mqa_dims* d) { return ((size_t)d->seq_len * d->q_heads + 63) & ~size_t(63); }
 inline SaveLayout save_layout(const rglru_mqa_dims* d) {
     const size_t tok = (size_t)d->batch * d->seq_len;
     SaveLayout l{};
     size_t o = 0;
-    l.lse = o; o = up256(o + tok * d->q_heads * 4);
+    l.lse = o; o = up256(o + d->batch * row_pitch(d) * 4);
     l.lo = o; o = up256(o + tok * 4);
+    l.last = o; o = up256(o + tok * 4);
     l.cs = o; o = up256(o + (size_t)d->seq_len * (D / 2) * sizeof(float2));
     l.q_rot = o; o = up256(o + tok * d->q_heads * D * 2);
     l.k_rot = o; o = up256(o + tok * D * 2);
     l.total = o;
     return l;
 }
+inline int key_tiles(const rglru_mqa_dims* d) { return (d->seq_len + bk::BKEY - 1) / bk::BKEY; }
 struct WsLayout {
-    size_t delta, total;
+    size_t delta, cum, part, total;
 };
 inline WsLayout ws_layout(const rglru_mqa_dims* d) {
+    const size_t nk = (size_t)d->batch * key_tiles(d);
     WsLayout l{};
     size_t o = 256;                    // the status word
-    l.delta = o; o = up256(o + (size_t)d->batch * d->seq_len * d->q_heads * 4);
+    l.delta = o; o = up256(o + d->batch * row_pitch(d) * 4);
+    l.cum = o; o = up256(o + (nk + 1) * 8);
+    l.part = o; o = up256(o + (nk + kMaxClusters) * 2 * bk::PART_FLOATS * 4);
     l.total = o;
     return l;
 }
 
-inline Args make_args(const rglru_mqa_dims* d, void* save) {
+inline Args make_args(const rglru_mqa_dims* d, void* save, void* ws) {
     const SaveLayout l = save_layout(d);
-    uint8_t* p = static_cast<uint8_t*>(save);
+    const WsLayout wl = ws_layout(d);
+    uint8_t *p = static_cast<uint8_t*>(save), *w = static_cast<uint8_t*>(ws);
     Args a{};
     a.B = d->batch; a.T = d->seq_len; a.H = d->q_heads;
+    a.TH = a.T * a.H; a.THp = (int)row_pitch(d);
+    a.ntr = (a.TH + 255) / 256;
+    a.nkt = key_tiles(d);
     a.scale = d->scale; a.scale_log2 = d->scale * kLog2e;
-    a.q_rot = reinterpret_cast<const __nv_bfloat16*>(p + l.q_rot);
-    a.k_rot = reinterpret_cast<const __nv_bfloat16*>(p + l.k_rot);
     a.cs = reinterpret_cast<const float2*>(p + l.cs);
     a.lo = reinterpret_cast<const int*>(p + l.lo);
     a.lse = reinterpret_cast<float*>(p + l.lse);
+    a.delta = reinterpret_cast<float*>(w + wl.delta);
+    a.cum = reinterpret_cast<const long long*>(w + wl.cum);
+    a.part = reinterpret_cast<float*>(w + wl.part);
+    a.status = static_cast<DeviceStatus*>(ws);
+    a.timeout_ns = 1000000000ull;
     return a;
+}
+
+// [B][rows][d] bf16, box 64 columns x box_rows, 128-byte swizzle; rows past a batch row's end read as zeros
+inline bool map_rows(CUtensorMap* m, const void* base, int rows, int B, int box_rows) {
+    return tc::make_map_3d_box_sw128(m, base, D, (uint64_t)rows, (uint64_t)B, 64, (uint32_t)box_rows, 1);
+}
+
+// how many 2-CTA clusters of a kernel fit on the device at once (asked once per kernel and device)
+template <typename K>
+cudaError_t resident_pairs(K kern, int threads, uint32_t smem, int which, int* pairs) {
+    static std::mutex mu;
+    static int cache[3][64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if ((e = set_smem_once(kern, (int)smem)) != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (cache[which][dev] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
+        if (n <= 0) return cudaErrorLaunchOutOfResources;
+        cache[which][dev] = std::min(n, kMaxClusters);
+    }
+    *pairs = cache[which][dev];
+    return cudaSuccess;
+}
+
+template <typename... KArgs, typename... Given>
+cudaError_t launch_pairs(void (*kern)(KArgs...), int pairs, int threads, uint32_t smem, cudaStream_t s, const Given&... given) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2u * (unsigned)pairs);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, given...);
 }
 
 }  // namespace mt
@@ -261,39 +1334,59 @@ size_t mqa_train_workspace(const rglru_mqa_dims* d) { return mt::ws_layout(d).to
 cudaError_t launch_mqa_forward(const rglru_mqa_dims* d, const void* q, const void* k, const void* v,
                                const uint8_t* reset, int pos0, void* out, void* save, void* ws, cudaStream_t s) {
     using namespace mt;
-    (void)ws;
     const SaveLayout l = save_layout(d);
     uint8_t* p = static_cast<uint8_t*>(save);
     const int B = d->batch, T = d->seq_len, H = d->q_heads;
+    int pairs = 0;
+    cudaError_t e = resident_pairs(mqa_forward_kernel, fw::kThreads, fw::SMEM_BYTES, 0, &pairs);
+    if (e != cudaSuccess) return e;
+    Args a = make_args(d, save, ws);
+    a.out = static_cast<__nv_bfloat16*>(out);
+    CUtensorMap mq, mk, mv;
+    if (!map_rows(&mq, p + l.q_rot, a.TH, B, 128) || !map_rows(&mk, p + l.k_rot, T, B, 64) || !map_rows(&mv, v, T, B, 128))
+        return cudaErrorInvalidValue;
     mqa_angles_kernel<<<T, D / 2, 0, s>>>(pos0, d->rope_base, reinterpret_cast<float2*>(p + l.cs));
-    mqa_first_key_kernel<<<B, 1024, 0, s>>>(T, d->window, reset, reinterpret_cast<int*>(p + l.lo));
-    mqa_turn_kernel<<<dim3(T, B), D / 2, 0, s>>>(T, H, reinterpret_cast<const float2*>(p + l.cs),
-                                                 static_cast<const __nv_bfloat16*>(q),
+    mqa_documents_kernel<<<B, kScanThreads, 0, s>>>(T, d->window, reset, reinterpret_cast<int*>(p + l.lo),
+                                                    reinterpret_cast<int*>(p + l.last));
+    mqa_turn_kernel<<<dim3(T, B), D / 2, 0, s>>>(T, H, a.cs, static_cast<const __nv_bfloat16*>(q),
                                                  static_cast<const __nv_bfloat16*>(k),
                                                  reinterpret_cast<__nv_bfloat16*>(p + l.q_rot),
                                                  reinterpret_cast<__nv_bfloat16*>(p + l.k_rot));
-    Args a = make_args(d, save);
-    a.v = static_cast<const __nv_bfloat16*>(v);
-    a.out = static_cast<__nv_bfloat16*>(out);
-    const long long rows = (long long)B * T * H;
-    mqa_fwd_kernel<<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(a);
-    return cudaGetLastError();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_pairs(mqa_forward_kernel, std::min(pairs, B * a.ntr), fw::kThreads, fw::SMEM_BYTES, s, mq, mk, mv, a);
 }
 
 cudaError_t launch_mqa_backward(const rglru_mqa_dims* d, const void* v, const void* out, const void* dout,
                                 const void* save, void* dq, void* dk, void* dv, void* ws, cudaStream_t s) {
     using namespace mt;
-    Args a = make_args(d, const_cast<void*>(save));
-    a.v = static_cast<const __nv_bfloat16*>(v);
+    const SaveLayout l = save_layout(d);
+    const uint8_t* p = static_cast<const uint8_t*>(save);
+    const int B = d->batch, T = d->seq_len;
+    int pq = 0, pk = 0;
+    cudaError_t e = resident_pairs(mqa_dq_kernel, bq::kThreads, bq::SMEM_BYTES, 1, &pq);
+    if (e == cudaSuccess) e = resident_pairs(mqa_dkv_kernel, bk::kThreads, bk::SMEM_BYTES, 2, &pk);
+    if (e != cudaSuccess) return e;
+    Args a = make_args(d, const_cast<void*>(save), ws);
     a.out = static_cast<__nv_bfloat16*>(const_cast<void*>(out));
-    a.dout = static_cast<const __nv_bfloat16*>(dout);
-    a.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ws_layout(d).delta);
     a.dq = static_cast<__nv_bfloat16*>(dq);
     a.dk = static_cast<__nv_bfloat16*>(dk);
     a.dv = static_cast<__nv_bfloat16*>(dv);
-    const long long rows = (long long)a.B * a.T * a.H, keys = (long long)a.B * a.T;
-    mqa_dq_kernel<<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(a);
-    mqa_dkv_kernel<<<(unsigned)((keys + 3) / 4), 128, 0, s>>>(a);
+    const int* last = reinterpret_cast<const int*>(p + l.last);
+    CUtensorMap q128, do128, k32, v32, k64, q64, do64, k128, v128;
+    if (!map_rows(&q128, p + l.q_rot, a.TH, B, 128) || !map_rows(&do128, dout, a.TH, B, 128) ||
+        !map_rows(&k32, p + l.k_rot, T, B, 32) || !map_rows(&v32, v, T, B, 32) || !map_rows(&k64, p + l.k_rot, T, B, 64) ||
+        !map_rows(&q64, p + l.q_rot, a.TH, B, 64) || !map_rows(&do64, dout, a.TH, B, 64) ||
+        !map_rows(&k128, p + l.k_rot, T, B, 128) || !map_rows(&v128, v, T, B, 128))
+        return cudaErrorInvalidValue;
+    const long long rows = (long long)B * a.TH;
+    mqa_delta_kernel<<<(unsigned)((rows + 31) / 32 + 1), 1024, 0, s>>>(a, static_cast<const __nv_bfloat16*>(dout), last,
+                                                                       const_cast<long long*>(a.cum));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_pairs(mqa_dq_kernel, std::min(pq, B * a.ntr), bq::kThreads, bq::SMEM_BYTES, s, q128, do128, k32, v32, k64, a);
+    if (e != cudaSuccess) return e;
+    e = launch_pairs(mqa_dkv_kernel, pk, bk::kThreads, bk::SMEM_BYTES, s, q64, do64, k128, v128, last, a);
+    if (e != cudaSuccess) return e;
+    mqa_dkv_sum_kernel<<<dim3(B * a.nkt, 8, 2), bk::BKEY, 0, s>>>(a, pk);
     return cudaGetLastError();
 }
 
