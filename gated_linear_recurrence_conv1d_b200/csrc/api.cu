@@ -381,7 +381,7 @@ static rglru_status check_mqa_train(const rglru_mqa_dims* d) {
 static rglru_status check_mqa_cache8(const rglru_mqa_dims* d, bool tokens) {
     rglru_status st = check_mqa(d, !tokens);
     if (st != RGLRU_OK) return st;
-    if (d->batch > 65535 || (long long)d->batch * d->window > (1LL << 31)) return RGLRU_ERR_UNSUPPORTED;
+    if (d->batch > 65535 || (long long)d->batch * d->window > (1LL << 29)) return RGLRU_ERR_UNSUPPORTED;
     return RGLRU_OK;
 }
 

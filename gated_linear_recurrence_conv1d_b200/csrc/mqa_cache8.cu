@@ -9,6 +9,7 @@
 // not depend on the rounding of a sine or a product next to a border between two codes.
 #include <algorithm>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -17,143 +18,141 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pair.cuh"
+#include "tma_maps.h"
 
 namespace rglru {
 namespace c8 {
 
-constexpr int D = 256;
+using namespace pr;
 
-// e4m3 codes of two fp32 values, lo in the low byte (round to nearest even, saturating)
-__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
+constexpr int D = 256;
+constexpr int kMaxH = 16;
+constexpr int kTile = 128;             // slots per tile (the MMA's M)
+constexpr double kFloor = 448.0 * 1.1754943508222875e-38;
+
+// ---- e4m3 ------------------------------------------------------------------------------------------
+// codes of two fp32 values, lo in the low byte (round to nearest even, saturating)
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+// the same in e5m2 (2 mantissa bits, down to 2^-16: the upper byte of an fp16)
+__device__ __forceinline__ uint32_t e5m2x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
 }
-__device__ __forceinline__ float warp_max(float v) {
+__device__ __forceinline__ float2 e5m2x2_values(uint32_t c) {
+    const uint32_t h = __byte_perm(c, 0, 0x1404);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// the values of two codes (exact in fp16)
+__device__ __forceinline__ float2 e4m3x2_values(uint32_t c) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+    return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+// ---- angles ------------------------------------------------------------------------------------------
+// base^(-2j/d) = 2^(-j log2(base) / 128) with log2(base) in two parts, the first short enough that
+// its product with j is exact: within 2 units of the last place of the power itself, at a fifth of
+// the fp64 operations of pow.
+struct Base {
+    double hi, lo;                     // log2(base)
+};
+__device__ __forceinline__ void cos_sin(Base base, int j, double p, double& c, double& s) {
+    const double x = exp2(base.hi * (-j / 128.0));
+    sincos(p * fma(x, base.lo * (-j / 128.0) * 0.69314718055994530942, x), &s, &c);
+}
+inline Base log2_base(float base) {
+    const long double l = log2l((long double)base);
+    Base b;
+    b.hi = (double)(float)l;           // 24 bits
+    b.lo = (double)(l - (long double)b.hi);
+    return b;
+}
+
+// ---- one slot by one warp ------------------------------------------------------------------------------
+// lane l holds the pairs j = 4 l .. 4 l + 3: elements j and j + 128
+__device__ __forceinline__ double max_nan(double a, double b) { return (a != a || b != b) ? a + b : fmax(a, b); }
+__device__ __forceinline__ void load_pairs(const __nv_bfloat16* p, int lane, float (&x)[8]) {
+    const uint2 u = reinterpret_cast<const uint2*>(p)[lane], v = reinterpret_cast<const uint2*>(p + D / 2)[lane];
+    const uint32_t w[4] = {u.x, u.y, v.x, v.y};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
-
-// 128 threads (thread j: elements j, j + d/2) quantise one row; x in fp64
-__device__ __forceinline__ void quantise_row(double x1, double x2, uint8_t* codes, float* scale, double* red) {
-    const int j = threadIdx.x;
-    double m = fmax(fabs(x1), fabs(x2));
-    // fmax drops a NaN: keep it, so that a slot with one is NaN as a whole
-    if (x1 != x1 || x2 != x2) m = x1 + x2;
-    for (int o = 16; o > 0; o >>= 1) {
-        const double u = __shfl_xor_sync(0xffffffffu, m, o);
-        m = (m != m || u != u) ? m + u : fmax(m, u);
+    for (int e = 0; e < 4; ++e) {
+        x[2 * e] = __uint_as_float(w[e] << 16);
+        x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
     }
-    if ((j & 31) == 0) red[j >> 5] = m;
-    __syncthreads();
-    m = red[0];
-    for (int i = 1; i < 4; ++i) m = (m != m || red[i] != red[i]) ? m + red[i] : fmax(m, red[i]);
-    if (!(m >= 448.0 * 1.1754943508222875e-38) && m == m) m = 448.0 * 1.1754943508222875e-38;
+}
+__device__ __forceinline__ void quantise_slot(const double (&x)[8], int lane, uint8_t* codes, float* scale) {
+    double m = 0.0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max_nan(m, fabs(x[e]));          // a NaN stays: the slot is NaN as a whole
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m < kFloor) m = kFloor;
     const float s = (float)(m / 448.0);
-    const uint16_t c = e4m3x2((float)(x1 / (double)s), (float)(x2 / (double)s));
-    codes[j] = (uint8_t)(c & 0xff);
-    codes[j + D / 2] = (uint8_t)(c >> 8);
-    if (j == 0) *scale = s;
-    __syncthreads();
+    float q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = (float)(x[e] / (double)s);
+    reinterpret_cast<uint32_t*>(codes)[lane] = e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16;
+    reinterpret_cast<uint32_t*>(codes + D / 2)[lane] = e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16;
+    if (lane == 0) *scale = s;
+}
+__device__ __forceinline__ void turn64(const float (&x)[8], const double2* cs, int lane, double (&y)[8]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const double2 a = cs[4 * lane + e];
+        y[e] = (double)x[e] * a.x - (double)x[4 + e] * a.y;
+        y[4 + e] = (double)x[4 + e] * a.x + (double)x[e] * a.y;
+    }
+}
+__device__ __forceinline__ void widen(const float (&x)[8], double (&y)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = (double)x[e];
 }
 
-__device__ __forceinline__ void turn64(double p, float base, int j, double x1, double x2, double& y1, double& y2) {
-    double s, c;
-    sincos(p * pow((double)base, -2.0 * j / D), &s, &c);
-    y1 = x1 * c - x2 * s;
-    y2 = x2 * c + x1 * s;
-}
-
-// block = (token, row): the last min(len, w) tokens of a row go into their slots
-__global__ void __launch_bounds__(D / 2) mqa_cache8_write_kernel(int T, int w, int pos0, float base, const int* lengths,
-                                                                 const __nv_bfloat16* k, const __nv_bfloat16* v,
-                                                                 uint8_t* codes, float* scales) {
-    __shared__ double red[4];
-    const int b = blockIdx.y, j = threadIdx.x;
-    const int len = lengths ? min(max(lengths[b], 0), T) : T;
-    const int t = max(0, len - w) + (int)blockIdx.x;
-    if (t >= len) return;
-    const size_t e = ((size_t)b * T + t) * D;
+// ---------------------------------------------------------------- write -------------------------------
+// Block = (token, up to kRows batch rows): the angles of the token's position once for all of them (they
+// are most of the arithmetic), then a warp per key or value.  The last min(len, w) tokens of a row
+// go into their slots.
+constexpr int kWriteRows = 8;
+__global__ void __launch_bounds__(128) mqa_cache8_write_kernel(int B, int T, int w, int pos0, Base base, const int* lengths,
+                                                               const __nv_bfloat16* k, const __nv_bfloat16* v,
+                                                               uint8_t* codes, float* scales) {
+    __shared__ double2 cs[D / 2];
+    const int t = blockIdx.x + (lengths ? 0 : max(0, T - w)), b0 = blockIdx.y * kWriteRows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int nb = min(kWriteRows, B - b0);
+    bool any = !lengths;
+    for (int i = 0; i < nb && !any; ++i) {
+        const int len = min(lengths[b0 + i], T);
+        any = t < len && t >= len - w;
+    }
+    if (!any) return;
     const long long p = (long long)pos0 + t;
-    const size_t ks = (size_t)b * 2 * w + (size_t)(p % w), vs = ks + w;
-    double y1, y2;
-    turn64((double)p, base, j, (double)__bfloat162float(k[e + j]), (double)__bfloat162float(k[e + j + D / 2]), y1, y2);
-    quantise_row(y1, y2, codes + ks * D, scales + ks, red);
-    quantise_row((double)__bfloat162float(v[e + j]), (double)__bfloat162float(v[e + j + D / 2]), codes + vs * D,
-                 scales + vs, red);
-}
-
-// block = row: rotated queries (fp32), the new slot
-__global__ void __launch_bounds__(D / 2) mqa_decode8_turn_kernel(int H, int w, float base, const int* pos,
-                                                                 const __nv_bfloat16* q, const __nv_bfloat16* k,
-                                                                 const __nv_bfloat16* v, float* q_rot, uint8_t* codes,
-                                                                 float* scales) {
-    __shared__ double red[4];
-    const int b = blockIdx.x, j = threadIdx.x, p = pos[b];
-    if (p < 0) return;
-    const size_t ks = (size_t)b * 2 * w + (size_t)(p % w), vs = ks + w;
-    double y1, y2, s, c;
-    sincos((double)p * pow((double)base, -2.0 * j / D), &s, &c);
-    for (int h = 0; h < H; ++h) {
-        const size_t e = ((size_t)b * H + h) * D;
-        const float x1 = __bfloat162float(q[e + j]), x2 = __bfloat162float(q[e + j + D / 2]);
-        q_rot[e + j] = x1 * (float)c - x2 * (float)s;
-        q_rot[e + j + D / 2] = x2 * (float)c + x1 * (float)s;
-    }
-    const double x1 = (double)__bfloat162float(k[(size_t)b * D + j]), x2 = (double)__bfloat162float(k[(size_t)b * D + j + D / 2]);
-    y1 = x1 * c - x2 * s;
-    y2 = x2 * c + x1 * s;
-    quantise_row(y1, y2, codes + ks * D, scales + ks, red);
-    quantise_row((double)__bfloat162float(v[(size_t)b * D + j]), (double)__bfloat162float(v[(size_t)b * D + j + D / 2]),
-                 codes + vs * D, scales + vs, red);
-}
-
-// block = (head, row), 8 warps over the slots, lane = 8 elements; one pass, running maximum and sum
-__global__ void __launch_bounds__(256) mqa_decode8_kernel(int H, int w, float scale_log2, const int* pos,
-                                                          const float* q_rot, const uint8_t* codes, const float* scales,
-                                                          __nv_bfloat16* out) {
-    __shared__ float sm[8], sl[8], so[8][D];
-    const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int p = pos[b], n = p < 0 ? 0 : min(p, w - 1) + 1;
-    const size_t e = ((size_t)b * H + h) * D;
-    float q[8], o[8] = {};
-    for (int i = 0; i < 8; ++i) q[i] = q_rot[e + 8 * lane + i];
-    float m = -INFINITY, l = 0.f;
-    for (int i = warp; i < n; i += 8) {
-        const size_t ks = (size_t)b * 2 * w + i, vs = ks + w;
-        const uint2 kc = *reinterpret_cast<const uint2*>(codes + ks * D + 8 * lane);
-        const uint2 vc = *reinterpret_cast<const uint2*>(codes + vs * D + 8 * lane);
-        float s = 0.f;
-        for (int x = 0; x < 8; ++x) s = fmaf(q[x], e4m3_value((uint8_t)((x < 4 ? kc.x : kc.y) >> (8 * (x & 3)))), s);
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= scales[ks] * scale_log2;
-        const float mn = fmaxf(m, s), f = exp2f(m - mn), pr = exp2f(s - mn);
-        m = mn;
-        l = fmaf(l, f, pr);
-        const float pv = pr * scales[vs];
-        for (int x = 0; x < 8; ++x) o[x] = fmaf(o[x], f, pv * e4m3_value((uint8_t)((x < 4 ? vc.x : vc.y) >> (8 * (x & 3)))));
-    }
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-    for (int x = 0; x < 8; ++x) so[warp][8 * lane + x] = o[x];
+    cos_sin(base, threadIdx.x, (double)p, cs[threadIdx.x].x, cs[threadIdx.x].y);
     __syncthreads();
-    float mx = -INFINITY, ls = 0.f, v = 0.f;
-    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, sm[i]);
-    for (int i = 0; i < 8; ++i) {
-        const float f = sl[i] == 0.f ? 0.f : exp2f(sm[i] - mx);
-        ls = fmaf(sl[i], f, ls);
-        v = fmaf(so[i][threadIdx.x], f, v);
+    const int slot = (int)(p % w);
+    for (int i = warp; i < 2 * nb; i += 4) {
+        const int b = b0 + (i >> 1), val = i & 1;
+        if (lengths) {
+            const int len = min(lengths[b], T);
+            if (t >= len || t < len - w) continue;
+        }
+        float x[8];
+        double y[8];
+        load_pairs((val ? v : k) + ((size_t)b * T + t) * D, lane, x);
+        if (val) widen(x, y); else turn64(x, cs, lane, y);
+        const size_t s = ((size_t)b * 2 + val) * w + slot;
+        quantise_slot(y, lane, codes + s * D, scales + s);
     }
-    out[e + threadIdx.x] = __float2bfloat16_rn(n > 0 ? v / ls : 0.f);
 }
 
-// thread = 8 elements of one slot
+// ---------------------------------------------------------------- read ---------------------------------
+// A warp per slot and lane = 8 elements
 __global__ void __launch_bounds__(256) mqa_cache8_read_kernel(long long slots, int w, const int* pos,
                                                               const uint8_t* codes, const float* scales,
                                                               __nv_bfloat16* cache) {
@@ -163,22 +162,628 @@ __global__ void __launch_bounds__(256) mqa_cache8_read_kernel(long long slots, i
     if (pos && s % w > pos[s / (2 * (long long)w)]) return;
     const uint2 c = *reinterpret_cast<const uint2*>(codes + s * D + 8 * lane);
     const float f = scales[s];
-    __align__(16) __nv_bfloat16 o[8];
-    for (int x = 0; x < 8; ++x) o[x] = __float2bfloat16_rn(f * e4m3_value((uint8_t)((x < 4 ? c.x : c.y) >> (8 * (x & 3)))));
-    *reinterpret_cast<uint4*>(cache + s * D + 8 * lane) = *reinterpret_cast<const uint4*>(o);
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 x = e4m3x2_values(((e < 2 ? c.x : c.y) >> (16 * (e & 1))) & 0xffffu);
+        o[e] = bf16x2(f * x.x, f * x.y);
+    }
+    *reinterpret_cast<uint4*>(cache + s * D + 8 * lane) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// ---------------------------------------------------------------- decode: queries and the new slot -----
+// Queries enter the score MMA as e4m3 too, in three parts: with 2^e the power of two that brings the head's
+// largest rotated element into (224, 448],  q~ = 2^e (x0 + x1 / 16 + x2 / 256) + r, x0 = e4m3(q~ 2^-e),
+// x1 = e4m3(16 (q~ 2^-e - x0)), ...: a part is off by at most 2^-4 of itself, so |r| <= 2^-12 |q~| (or
+// 2^-18 448 2^e where x2 is below e4m3's normal numbers), less than bf16 would leave.
+constexpr int kQParts = 3, kQRows = kQParts * kMaxH;
+__global__ void __launch_bounds__(256) mqa_decode8_turn_kernel(int H, int w, Base base, const int* pos,
+                                                               const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                                               const __nv_bfloat16* v, uint8_t* qp, float* qs,
+                                                               unsigned* done, uint8_t* codes, float* scales,
+                                                               __nv_bfloat16* out) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ double2 cs[D / 2];
+    const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int p = pos[b];
+    if (threadIdx.x == 0) done[b] = 0;
+    if (p < 0) {                                     // a row without a token
+        for (int e = threadIdx.x; e < H * D / 8; e += 256)
+            reinterpret_cast<uint4*>(out + (size_t)b * H * D)[e] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    float x[8];
+    if (threadIdx.x < D / 2) cos_sin(base, threadIdx.x, (double)p, cs[threadIdx.x].x, cs[threadIdx.x].y);
+    __syncthreads();
+    const int slot = p % w;
+    for (int i = warp; i < H + 2; i += 8) {
+        if (i >= H) {
+            const int val = i - H;
+            double y[8];
+            load_pairs((val ? v : k) + (size_t)b * D, lane, x);
+            if (val) widen(x, y); else turn64(x, cs, lane, y);
+            const size_t s = ((size_t)b * 2 + val) * w + slot;
+            quantise_slot(y, lane, codes + s * D, scales + s);
+            continue;
+        }
+        load_pairs(q + ((size_t)b * H + i) * D, lane, x);
+        float y[8], m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float c = (float)cs[4 * lane + e].x, s = (float)cs[4 * lane + e].y;
+            y[e] = x[e] * c - x[4 + e] * s;
+            y[4 + e] = x[4 + e] * c + x[e] * s;
+            m = fmaxf(m, fmaxf(fabsf(y[e]), fabsf(y[4 + e])));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // m / 448 rounded up to a power of two (at least 2^-100, so that its reciprocal is finite)
+        const float r448 = fminf(fmaxf(m, 448.0f * 7.9e-31f), 3.0e38f) * (1.0f / 448.0f);
+        int e2 = (__float_as_int(r448) >> 23) - 127;
+        if (__float_as_int(r448) & 0x7fffff) ++e2;
+        const float up = __int_as_float((e2 + 127) << 23), down = __int_as_float((127 - e2) << 23);
+        if (lane == 0) qs[b * kMaxH + i] = m < INFINITY ? up : __int_as_float(0x7fffffff);   // an infinity: NaN
+        uint32_t c[kQParts][2] = {};
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            float u = y[e] * down, z = y[e + 1] * down;
+#pragma unroll
+            for (int part = 0; part < kQParts; ++part) {
+                const uint32_t cc = e4m3x2(u, z);
+                const float2 f = e4m3x2_values(cc);
+                c[part][e >> 2] |= cc << (8 * (e & 2));
+                u = (u - f.x) * 16.0f;
+                z = (z - f.y) * 16.0f;
+            }
+        }
+#pragma unroll
+        for (int part = 0; part < kQParts; ++part) {
+            uint8_t* row = qp + ((size_t)b * kQRows + part * kMaxH + i) * D;
+            reinterpret_cast<uint32_t*>(row)[lane] = c[part][0];
+            reinterpret_cast<uint32_t*>(row + D / 2)[lane] = c[part][1];
+        }
+    }
+}
+
+// ---------------------------------------------------------------- decode: attention --------------------
+// The slots of a row are cut into tiles of 128 and the tiles of all rows laid out as one line, of which every
+// CTA takes an equal piece (a "segment" is a piece of one row): the rings' bytes are spread evenly
+// over the SMs whatever the rows' lengths.  Per tile
+//   S^T = K Qp^T   (M 128 slots, N 48 = 16 heads x 3 parts, K 256; e4m3, fp32 sums)
+//   O^T += V^T Wp^T (M 128 columns twice, N 48 = 16 heads x 3 parts, K 128 slots)
+// straight from the codes in shared memory (V^T is the value tile read MN-major).  4 warps, thread = slot:
+// s = (S0 + S1 / 16 + S2 / 256) 2^e c scale_k, p = 2^(s - m) with a reference maximum m per head that moves
+// when a score passes it by more than 8 times, and the weight p scale_v, normalised by a power of two
+// vref >= the value scales seen so far, as three e5m2 parts: off by at most 2^-9 of itself, half of what bf16
+// would leave, down to weights of 2^-29 (e4m3 parts end at 2^-16, which shows where one slot has nearly all
+// the weight and a small value).  p adds to the thread's own sum in fp32.  O stays in TMEM for the whole segment; when m or vref
+// moves it is rescaled there.  A row inside one segment is written at once; else the segments leave
+// (m, sum, O) and the one that finishes last adds them up in order.
+// The step reads every code once: bound by HBM.
+constexpr uint32_t TILE_BYTES = kTile * D;            // 32768: 2 boxes of [128 slots x 128 B]
+constexpr int kNBuf = 5;
+constexpr uint32_t Q_BYTES = kQRows * D;              // 12288: 2 boxes of [48 x 128 B]
+constexpr int kWParts = 3, kWRows = kWParts * kMaxH;
+constexpr uint32_t W_BYTES = kWRows * kTile;          // 6144: [48 x 128 slots]
+constexpr uint32_t OFF_Q = kNBuf * TILE_BYTES, OFF_W = OFF_Q + 2 * Q_BYTES, OFF_QS = OFF_W + 2 * W_BYTES;
+constexpr uint32_t OFF_RED = OFF_QS + 2 * 64, OFF_BAR = OFF_RED + 5 * kMaxH * 4 + 64;
+constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+constexpr uint32_t TM_S = 0, TM_O = 128, TMEM_COLS = 256;     // S: two buffers, 64 apart; O: two halves, 64 apart
+constexpr int kThreads = 192, kWarpTma = 4, kWarpMma = 5;
+constexpr float kAlpha = 4096.0f;                     // weights are held as alpha p: p <= 8 keeps them below 57344
+
+struct DecArgs {
+    int B, H, w;
+    float scale_log2;
+    const int* pos;
+    const float* scales;               // [B][2][w]
+    const float* qs;                   // [B][16]
+    unsigned* done;                    // [B]
+    float* part;                       // [B + CTAs][part_pitch]: O [H][d], m [16], sum [16]
+    __nv_bfloat16* out;
+    DeviceStatus* status;
+    unsigned long long timeout_ns;
+};
+
+__host__ __device__ constexpr int part_pitch(int H) { return H * D + 2 * kMaxH; }
+
+// e4m3 x e4m3 (b_e5m2 = 0) or e5m2 (1) -> fp32; A K-major (a_mn = 0) or MN-major (1), B K-major
+__device__ __forceinline__ constexpr uint32_t idesc_fp8(int n, int a_mn, int b_e5m2) {
+    return (1u << 4) | ((uint32_t)b_e5m2 << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+}
+__device__ __forceinline__ void mma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(id), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ int slots_of(const DecArgs& a, int b) {
+    const int p = a.pos[b];
+    return p < 0 ? 0 : min(p, a.w - 1) + 1;
+}
+struct Walk {
+    long long pos, end, total, row_beg;  // on the line; row_beg: where the current row begins
+    int G, row;
+};
+struct DecSeg {
+    int b, t0, nt, n, c0, c1;            // row, its first tile here, tiles here, slots of the row, the row's CTAs
+};
+__device__ __forceinline__ int owner(long long x, long long total, int G) {
+    int c = (int)(x * G / total);
+    while (total * (c + 1) / G <= x) ++c;
+    while (total * c / G > x) --c;
+    return c;
+}
+__device__ __forceinline__ bool next_seg(const DecArgs& a, Walk& k, DecSeg& s) {
+    if (k.pos >= k.end) return false;
+    int n, tiles;
+    for (;;) {                           // rows without tokens have no tiles
+        n = slots_of(a, k.row);
+        tiles = (n + kTile - 1) / kTile;
+        if (k.pos < k.row_beg + tiles) break;
+        k.row_beg += tiles;
+        ++k.row;
+    }
+    s.b = k.row;
+    s.n = n;
+    s.t0 = (int)(k.pos - k.row_beg);
+    s.nt = (int)(min(k.end, k.row_beg + tiles) - k.pos);
+    if (s.nt == tiles) {
+        s.c0 = s.c1 = blockIdx.x;
+    } else {
+        s.c0 = owner(k.row_beg, k.total, k.G);
+        s.c1 = owner(k.row_beg + tiles - 1, k.total, k.G);
+    }
+    k.pos += s.nt;
+    return true;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kv, const DecArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    const uint32_t bars = sb + OFF_BAR;
+    auto full = [&](uint32_t i) { return bars + 8 * i; };
+    auto empty = [&](uint32_t i) { return bars + 8 * kNBuf + 8 * i; };
+    auto s_full = [&](uint32_t i) { return bars + 16 * kNBuf + 8 * i; };
+    auto w_full = [&](uint32_t i) { return bars + 16 * kNBuf + 16 + 8 * i; };
+    auto o_done = [&](uint32_t i) { return bars + 16 * kNBuf + 32 + 8 * i; };
+    const uint32_t o_free = bars + 16 * kNBuf + 48, mma_done = o_free + 8;
+    auto q_free = [&](uint32_t i) { return bars + 16 * kNBuf + 64 + 8 * i; };
+    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 16 * kNBuf + 80);
+    const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 16 * kNBuf + 96), a.status, a.timeout_ns};
+    long long* scan = reinterpret_cast<long long*>(smem);            // before the first load: per-thread sums
+    float* red = reinterpret_cast<float*>(smem + OFF_RED);           // [4 warps][16 heads], [4] scales
+    Walk* walk_s = reinterpret_cast<Walk*>(smem + OFF_W);            // before the first weights
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kNBuf; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(w_full(i), 4);
+            mbar_init(o_done(i), 1);
+            mbar_init(q_free(i), 4);
+        }
+        mbar_init(o_free, 4);
+        mbar_init(mma_done, 1);
+        *g.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_u32((const void*)tmem_s), TMEM_COLS);
+        tmem_relinquish();
+    }
+    // this CTA's piece of the line of tiles: every thread counts the tiles of a run of rows
+    {
+        const int per = (a.B + kThreads - 1) / kThreads, r0 = min(a.B, (int)threadIdx.x * per), r1 = min(a.B, r0 + per);
+        long long mine = 0;
+        for (int b = r0; b < r1; ++b) mine += (slots_of(a, b) + kTile - 1) / kTile;
+        scan[threadIdx.x] = mine;
+        __syncthreads();
+        long long before = 0, total = 0;
+        for (int i = 0; i < kThreads; ++i) {
+            if (i < (int)threadIdx.x) before += scan[i];
+            total += scan[i];
+        }
+        Walk k;
+        k.total = total;
+        k.G = (int)min((long long)gridDim.x, total);
+        k.pos = k.end = 0;
+        k.row = 0;
+        k.row_beg = 0;
+        const bool some = (int)blockIdx.x < k.G;
+        if (some) {
+            k.pos = total * blockIdx.x / k.G;
+            k.end = total * (blockIdx.x + 1) / k.G;
+        }
+        if (some ? (before <= k.pos && k.pos < before + mine) : threadIdx.x == 0) {
+            k.row = r0;
+            k.row_beg = before;
+            *walk_s = k;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_s;
+    Walk k = *walk_s;
+    __syncthreads();                                                 // walk_s and scan give way to the tiles
+    DecSeg sg{};
+
+    if (warp == kWarpTma) {
+        if (lane == 0) {
+            uint32_t L = 0, ns = 0;
+            bool ok = true, waited = false;
+            uint32_t q_bar = 0;                                      // a barrier that still expects the first queries
+            auto load_q = [&](uint32_t bar) {
+                for (int c = 0; c < 2; ++c)
+                    tma_load_2d(sb + OFF_Q + (ns & 1) * Q_BYTES + c * (Q_BYTES / 2), &map_q, c * 128, sg.b * kQRows, bar);
+                bulk_load(sb + OFF_QS + (ns & 1) * 64, a.qs + sg.b * kMaxH, 64, bar);
+            };
+            // the kernel before this one writes the queries and the new slots: what does not hold them is
+            // loaded before it is waited for
+            auto previous = [&]() {
+                if (waited) return;
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                waited = true;
+                if (q_bar) load_q(q_bar);
+            };
+            for (; ok && next_seg(a, k, sg); ++ns) {
+                const int slot = a.pos[sg.b] % a.w;
+                for (int t = 0; ok && t < sg.nt; ++t)
+                    for (int kv = 0; kv < 2; ++kv, ++L) {
+                        const uint32_t s = L % kNBuf, u = L / kNBuf;
+                        const bool q = t == 0 && kv == 0;
+                        const int row = (sg.t0 + t) * kTile;
+                        if (u > 0 || (q && ns > 0) || (slot >= row && slot < row + kTile)) previous();
+                        if (u > 0 && !(ok = wait(empty(s), (u - 1) & 1, g, 1))) break;
+                        if (q && ns > 1 && !(ok = wait(q_free(ns & 1), ((ns >> 1) - 1) & 1, g, 10))) break;
+                        mbar_arrive_expect_tx(full(s), TILE_BYTES + (q ? Q_BYTES + 64 : 0));
+                        for (int c = 0; c < 2; ++c)
+                            tma_load_2d(sb + s * TILE_BYTES + c * 16384, &map_kv, c * 128, (2 * sg.b + kv) * a.w + row, full(s));
+                        if (q) {
+                            if (waited) load_q(full(s)); else q_bar = full(s);
+                        }
+                    }
+                previous();
+            }
+            const uint64_t t0 = globaltimer_ns();
+            for (uint32_t l = L > kNBuf ? L - kNBuf : 0; l < L; ++l)
+                while (!mbar_try_wait(full(l % kNBuf), (l / kNBuf) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
+                }
+        }
+    } else if (warp == kWarpMma) {
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t id_s = idesc_fp8(kQRows, 0, 0), id_o = idesc_fp8(kWRows, 1, 1);
+        uint32_t gt = 0, ns = 0;
+        bool ok = true;
+        for (; ok && next_seg(a, k, sg); ++ns) {
+            for (int t = 0; ok && t <= sg.nt; ++t) {
+                if (t < sg.nt) {
+                    const uint32_t i = gt + t, l = 2 * i, s = l % kNBuf, buf = i & 1;
+                    if (!(ok = wait_w(full(s), (l / kNBuf) & 1, g, 2))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < D / 32; ++ks)
+                            mma_fp8(tm + TM_S + buf * 64, desc_k_sw128(sb + s * TILE_BYTES + (ks >> 2) * 16384 + (ks & 3) * 32),
+                                     desc_k_sw128(sb + OFF_Q + (ns & 1) * Q_BYTES + (ks >> 2) * (Q_BYTES / 2) + (ks & 3) * 32), id_s,
+                                     ks > 0 ? 1u : 0u);
+                        mma_commit(s_full(buf));
+                        mma_commit(empty(s));
+                    }
+                    __syncwarp();
+                }
+                if (t >= 1) {
+                    const uint32_t i = gt + t - 1, l = 2 * i + 1, s = l % kNBuf, buf = i & 1;
+                    if (t == 1 && ns > 0 && !(ok = wait_w(o_free, (ns - 1) & 1, g, 3))) break;
+                    if (!(ok = wait_w(full(s), (l / kNBuf) & 1, g, 4))) break;
+                    if (!(ok = wait_w(w_full(buf), (i >> 1) & 1, g, 5))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh)               // columns [128 hh, 128 hh + 128)
+#pragma unroll
+                            for (int ks = 0; ks < kTile / 32; ++ks)
+                                mma_fp8(tm + TM_O + hh * 64, desc_mn_sw128(sb + s * TILE_BYTES + hh * 16384 + ks * 4096, 16384),
+                                         desc_k_sw128(sb + OFF_W + buf * W_BYTES + ks * 32), id_o, (t > 1 || ks > 0) ? 1u : 0u);
+                        mma_commit(o_done(buf));
+                        mma_commit(empty(s));
+                    }
+                    __syncwarp();
+                }
+            }
+            gt += sg.nt;
+        }
+        if (elect_one()) mma_commit(mma_done);
+        __syncwarp();
+        if (lane == 0) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(mma_done, 0) && globaltimer_ns() - t0 < a.timeout_ns) {
+            }
+        }
+        __syncwarp();
+    } else {
+        const int r = threadIdx.x, H = a.H;              // slot of a tile, then column
+        const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // the new slot's scales, the rows' counters
+        uint32_t gt = 0, ns = 0;
+        bool ok = true, stop = false;
+        for (; !stop && next_seg(a, k, sg); ++ns) {
+            const float *sk = a.scales + (size_t)sg.b * 2 * a.w, *sv = sk + a.w;
+            float m[kMaxH], l[kMaxH], vref = 0.f;
+#pragma unroll
+            for (int h = 0; h < kMaxH; ++h) {
+                m[h] = -INFINITY;
+                l[h] = 0.f;
+            }
+            int x = sg.t0 * kTile + r;
+            float k_next = x < sg.n ? sk[x] : 0.f, v_next = x < sg.n ? sv[x] : 0.f;
+            for (int t = 0; t < sg.nt; ++t) {
+                const uint32_t i = gt + t, buf = i & 1;
+                const bool valid = x < sg.n;
+                const float ks = k_next * a.scale_log2, vs = v_next;
+                x += kTile;                               // the next tile's scales while this one is worked on
+                k_next = x < sg.n ? sk[x] : 0.f;
+                v_next = x < sg.n ? sv[x] : 0.f;
+                ok = ok && wait_w(s_full(buf), (i >> 1) & 1, g, 6);
+                // a tile's last slots may be past the ring's: their codes could be NaN, weight 0 or not
+                const int cnt = min(kTile, sg.n - (sg.t0 + t) * kTile);
+                if (cnt < kTile) {
+                    const uint32_t lv = 2 * i + 1;
+                    ok = ok && wait_w(full(lv % kNBuf), (lv / kNBuf) & 1, g, 7);
+                    if (ok && !valid)
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            *reinterpret_cast<uint4*>(smem + (lv % kNBuf) * TILE_BYTES + (c >> 3) * 16384 + r * 128 + (c & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                }
+                tc_fence_after();
+                const float* qs = reinterpret_cast<const float*>(smem + OFF_QS + (ns & 1) * 64);
+                float s[kMaxH];
+                bool move = vs > vref;
+                {
+                    float s0[16], s1[16], s2[16];
+                    tmem_ld16(tl + TM_S + buf * 64, s0);
+                    tmem_ld16(tl + TM_S + buf * 64 + 16, s1);
+                    tmem_ld16(tl + TM_S + buf * 64 + 32, s2);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int h = 0; h < kMaxH; ++h) {
+                        s[h] = -INFINITY;
+                        if (h < H) {
+                            const float d = fmaf(s2[h], 1.0f / 256.0f, fmaf(s1[h], 1.0f / 16.0f, s0[h]));
+                            if (valid) s[h] = d * (qs[h] * ks);
+                            move |= s[h] > m[h] + 3.0f;
+                        }
+                    }
+                }
+                if (bar_or(move || !ok, 128)) {
+                    // the new reference values from the 4 warps' maxima; O and the sums follow
+#pragma unroll
+                    for (int h = 0; h < kMaxH; ++h)
+                        if (h < H) {
+                            float v = s[h];
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+                            if (lane == 0) red[warp * kMaxH + h] = v;
+                        }
+                    float v = vs;
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+                    if (lane == 0) red[4 * kMaxH + warp] = v;
+                    if (bar_or(!ok, 128)) {
+                        stop = true;
+                        break;
+                    }
+                    v = fmaxf(fmaxf(red[4 * kMaxH], red[4 * kMaxH + 1]), fmaxf(red[4 * kMaxH + 2], red[4 * kMaxH + 3]));
+                    float fv = 1.0f;
+                    if (v > vref) {                       // the next power of two, twice over (infinity stays)
+                        // (at least 2^-114: alpha / vref is finite, vref / alpha a normal number)
+                        const unsigned e2 = (__float_as_uint(v) & 0x7f800000u) + 0x01000000u;
+                        const float p2 = __uint_as_float(max(min(e2, 0x7f000000u), 13u << 23));
+                        fv = vref == 0.f ? 1.0f : vref / p2;
+                        vref = p2;
+                    }
+                    float f[kMaxH];
+                    bool any = fv != 1.0f;
+#pragma unroll
+                    for (int h = 0; h < kMaxH; ++h) {
+                        f[h] = 1.0f;
+                        if (h < H) {
+                            const float mx = fmaxf(fmaxf(red[h], red[kMaxH + h]), fmaxf(red[2 * kMaxH + h], red[3 * kMaxH + h]));
+                            if (mx > m[h] + 3.0f) {
+                                f[h] = m[h] == -INFINITY ? 1.0f : ex2_approx(m[h] - mx);
+                                m[h] = mx;
+                                any = true;
+                            }
+                            l[h] *= f[h];
+                        }
+                    }
+                    if (t > 0 && any) {
+                        ok = wait_w(o_done((i - 1) & 1), ((i - 1) >> 1) & 1, g, 8);
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < 2 * kWParts; ++c) {
+                            const uint32_t col = tl + TM_O + (c / kWParts) * 64 + (c % kWParts) * 16;
+                            float o[16];
+                            tmem_ld16(col, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int h = 0; h < kMaxH; ++h) o[h] *= f[h] * fv;
+                            tmem_st16f(col, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    bar_or(false, 128);                   // red is read before the next use
+                }
+                // weights: row part * 16 + head, byte = slot, in 128-byte rows swizzled by the row
+                uint8_t* wb = smem + OFF_W + buf * W_BYTES;
+                const float wv = fmaf(vs, kAlpha / vref, vs - vs);    // a scale that is not finite: NaN
+                const uint32_t ch = (uint32_t)(r >> 4), lo = (uint32_t)(r & 15);
+#pragma unroll
+                for (int h = 0; h < kMaxH; h += 2) {
+                    uint32_t c[kWParts] = {};
+                    if (h < H) {
+                        const float p0 = valid ? ex2_approx(s[h] - m[h]) : 0.f, p1 = valid && h + 1 < H ? ex2_approx(s[h + 1] - m[h + 1]) : 0.f;
+                        l[h] += p0;
+                        l[h + 1] += p1;
+                        float w0 = valid ? p0 * wv : 0.f, w1 = valid && h + 1 < H ? p1 * wv : 0.f;
+#pragma unroll
+                        for (int part = 0; part < kWParts; ++part) {
+                            c[part] = e5m2x2(w0, w1);
+                            const float2 y = e5m2x2_values(c[part]);
+                            w0 = (w0 - y.x) * 8.0f;
+                            w1 = (w1 - y.y) * 8.0f;
+                        }
+                    }
+                    const uint32_t a0 = h * 128 + ((ch ^ (h & 7)) << 4) + lo, a1 = (h + 1) * 128 + ((ch ^ ((h + 1) & 7)) << 4) + lo;
+#pragma unroll
+                    for (int part = 0; part < kWParts; ++part) {
+                        wb[a0 + part * (kMaxH * kTile)] = (uint8_t)c[part];
+                        wb[a1 + part * (kMaxH * kTile)] = (uint8_t)(c[part] >> 8);
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(w_full(buf));
+            }
+            if (stop) break;
+            if (lane == 0) mbar_arrive(q_free(ns & 1));   // this segment's queries and their scales are done with
+            const uint32_t last = gt + sg.nt - 1;
+            gt += sg.nt;
+            // sums over the slots: lanes, then warps
+#pragma unroll
+            for (int h = 0; h < kMaxH; ++h)
+                if (h < H) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+                    if (lane == 0) red[warp * kMaxH + h] = l[h];
+                }
+            ok = ok && wait_w(o_done(last & 1), (last >> 1) & 1, g, 9);
+            if (bar_or(!ok, 128)) break;
+            tc_fence_after();
+            float o[2][kMaxH];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                float y1[16], y2[16];
+                tmem_ld16(tl + TM_O + hh * 64, o[hh]);
+                tmem_ld16(tl + TM_O + hh * 64 + 16, y1);
+                tmem_ld16(tl + TM_O + hh * 64 + 32, y2);
+                tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < kMaxH; ++h)
+                    o[hh][h] = fmaf(y2[h], 1.0f / 64.0f, fmaf(y1[h], 1.0f / 8.0f, o[hh][h])) * (vref * (1.0f / kAlpha));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+#pragma unroll
+            for (int h = 0; h < kMaxH; ++h)
+                if (h < H) l[h] = (red[h] + red[kMaxH + h]) + (red[2 * kMaxH + h] + red[3 * kMaxH + h]);
+            if (sg.c0 == sg.c1) {
+#pragma unroll
+                for (int h = 0; h < kMaxH; ++h)
+                    if (h < H) {
+                        const float inv = 1.0f / l[h];
+                        __nv_bfloat16* y = a.out + ((size_t)sg.b * H + h) * D + r;
+                        y[0] = __float2bfloat16_rn(o[0][h] * inv);
+                        y[128] = __float2bfloat16_rn(o[1][h] * inv);
+                    }
+                bar_or(false, 128);                       // red is read before the next use
+                continue;
+            }
+            const int pitch = part_pitch(H);
+            float* part = a.part + (size_t)(blockIdx.x + sg.b) * pitch;
+#pragma unroll
+            for (int h = 0; h < kMaxH; ++h)
+                if (h < H) {
+                    part[h * D + r] = o[0][h];
+                    part[h * D + 128 + r] = o[1][h];
+                    if (r == 0) {
+                        part[H * D + h] = m[h];
+                        part[H * D + kMaxH + h] = l[h];
+                    }
+                }
+            __threadfence();
+            bar_or(false, 128);
+            unsigned n = 0;
+            if (r == 0) n = atomicAdd(a.done + sg.b, 1u);
+            const unsigned want = (unsigned)(sg.c1 - sg.c0);
+            if (bar_or(r == 0 && n == want, 128)) {       // the last of the row: the parts in their order
+                __threadfence();
+                const float* p0 = a.part + (size_t)(sg.c0 + sg.b) * pitch;
+                const int np = sg.c1 - sg.c0 + 1;
+                for (int e = r; e < H * (D / 4); e += 128) {
+                    const int h = e / (D / 4);
+                    float mx = -INFINITY, ls = 0.f;
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int c = 0; c < np; ++c) mx = fmaxf(mx, __ldcg(p0 + (size_t)c * pitch + H * D + h));
+                    for (int c = 0; c < np; ++c) {
+                        const float* pc = p0 + (size_t)c * pitch;
+                        const float f = ex2_approx(__ldcg(pc + H * D + h) - mx);
+                        const float4 z = __ldcg(reinterpret_cast<const float4*>(pc) + e);
+                        ls = fmaf(__ldcg(pc + H * D + kMaxH + h), f, ls);
+                        y.x = fmaf(z.x, f, y.x);
+                        y.y = fmaf(z.y, f, y.y);
+                        y.z = fmaf(z.z, f, y.z);
+                        y.w = fmaf(z.w, f, y.w);
+                    }
+                    const float inv = 1.0f / ls;
+                    reinterpret_cast<uint2*>(a.out + (size_t)sg.b * H * D)[e] =
+                        make_uint2(bf16x2(y.x * inv, y.y * inv), bf16x2(y.z * inv, y.w * inv));
+                }
+            }
+        }
+        tmem_wait_ld();
+        tmem_wait_st();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+struct DecLayout {
+    size_t done, qs, qp, part, total;
+};
+constexpr int kMaxCtas = 148;
+inline DecLayout dec_layout(const rglru_mqa_dims* d) {
+    auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+    const size_t B = (size_t)d->batch;
+    DecLayout l{};
+    size_t o = 256;                    // the status word
+    l.done = o; o = up(o + B * 4);
+    l.qs = o; o = up(o + B * kMaxH * 4);
+    l.qp = o; o = up(o + B * kQRows * D);
+    l.part = o; o = up(o + (B + kMaxCtas) * part_pitch(d->q_heads) * 4);
+    l.total = o;
+    return l;
 }
 
 }  // namespace c8
 
-size_t mqa_decode8_workspace(const rglru_mqa_dims* d) {
-    return 256 + (size_t)d->batch * d->q_heads * c8::D * 4;
-}
+size_t mqa_decode8_workspace(const rglru_mqa_dims* d) { return c8::dec_layout(d).total; }
 
 cudaError_t launch_mqa_cache8_write(const rglru_mqa_dims* d, const void* k, const void* v, const int* lengths, int pos0,
                                     void* codes, float* scales, cudaStream_t s) {
     using namespace c8;
-    mqa_cache8_write_kernel<<<dim3(std::min(d->seq_len, d->window), d->batch), D / 2, 0, s>>>(
-        d->seq_len, d->window, pos0, d->rope_base, lengths, static_cast<const __nv_bfloat16*>(k),
+    // without lengths only the last min(T, w) tokens are written; with them any token may be
+    const int tokens = lengths ? d->seq_len : std::min(d->seq_len, d->window);
+    mqa_cache8_write_kernel<<<dim3(tokens, (d->batch + kWriteRows - 1) / kWriteRows), 128, 0, s>>>(
+        d->batch, d->seq_len, d->window, pos0, log2_base(d->rope_base), lengths, static_cast<const __nv_bfloat16*>(k),
         static_cast<const __nv_bfloat16*>(v), static_cast<uint8_t*>(codes), scales);
     return cudaGetLastError();
 }
@@ -186,15 +791,48 @@ cudaError_t launch_mqa_cache8_write(const rglru_mqa_dims* d, const void* k, cons
 cudaError_t launch_mqa_decode8(const rglru_mqa_dims* d, const void* q, const void* k, const void* v, const int* pos,
                                void* codes, float* scales, void* out, void* ws, cudaStream_t s) {
     using namespace c8;
-    float* q_rot = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
-    mqa_decode8_turn_kernel<<<d->batch, D / 2, 0, s>>>(
-        d->q_heads, d->window, d->rope_base, pos, static_cast<const __nv_bfloat16*>(q),
-        static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), q_rot,
-        static_cast<uint8_t*>(codes), scales);
-    mqa_decode8_kernel<<<dim3(d->q_heads, d->batch), 256, 0, s>>>(d->q_heads, d->window, d->scale * 1.4426950408889634f,
-                                                                  pos, q_rot, static_cast<const uint8_t*>(codes), scales,
-                                                                  static_cast<__nv_bfloat16*>(out));
-    return cudaGetLastError();
+    const DecLayout l = dec_layout(d);
+    uint8_t* p = static_cast<uint8_t*>(ws);
+    const int B = d->batch, w = d->window;
+    // the queries' parts as [B 48 rows][256 bytes] (box 128 x 48), the ring as [B 2 w slots][256 bytes] (box 128 x 128)
+    CUtensorMap mq, mkv;
+    if (!tc::make_map_2d_sw128_elem(&mq, p + l.qp, 1, D, (uint64_t)B * kQRows, D, 128, kQRows) ||
+        !tc::make_map_2d_sw128_elem(&mkv, codes, 1, D, (uint64_t)B * 2 * w, D, 128, kTile))
+        return cudaErrorInvalidValue;
+    cudaError_t e = set_smem_once(mqa_decode8_kernel, (int)SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    DecArgs a{};
+    a.B = B; a.H = d->q_heads; a.w = w;
+    a.scale_log2 = d->scale * 1.4426950408889634f;
+    a.pos = pos;
+    a.scales = scales;
+    a.qs = reinterpret_cast<const float*>(p + l.qs);
+    a.done = reinterpret_cast<unsigned*>(p + l.done);
+    a.part = reinterpret_cast<float*>(p + l.part);
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.status = static_cast<DeviceStatus*>(ws);
+    a.timeout_ns = 1000000000ull;
+    mqa_decode8_turn_kernel<<<B, 256, 0, s>>>(
+        d->q_heads, w, log2_base(d->rope_base), pos, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+        static_cast<const __nv_bfloat16*>(v), p + l.qp, reinterpret_cast<float*>(p + l.qs), a.done, static_cast<uint8_t*>(codes),
+        scales, a.out);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // the attention's launch, set-up and first tiles overlap the kernel before it
+    const long long tiles = (long long)B * ((w + kTile - 1) / kTile);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<long long>(tiles, std::min(sms, kMaxCtas)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mqa_decode8_kernel, mq, mkv, a);
 }
 
 cudaError_t launch_mqa_cache8_read(const rglru_mqa_dims* d, const void* codes, const float* scales, const int* pos,

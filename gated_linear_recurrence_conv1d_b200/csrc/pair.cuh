@@ -87,7 +87,7 @@ struct Guard {
     DeviceStatus* status;
     unsigned long long timeout_ns;
 };
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Guard& g, unsigned where) {
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Guard& g, unsigned where) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 0;; ++it) {
         if (mbar_try_wait_cluster(bar, parity)) return true;

@@ -21,7 +21,7 @@ bool make_map_3d_sw128(CUtensorMap* m, const void* base, int W, int D1, int D2, 
 bool make_map_3d_box_sw128(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0,
                            uint32_t b1, uint32_t b2);
 
-// 2-D map (inner x outer elements of bf16 or fp32, rows row_bytes apart) whose box rows are
+// 2-D map (inner x outer elements of bytes, bf16 or fp32, rows row_bytes apart) whose box rows are
 // exactly 128 bytes, loaded and stored in the 128-byte swizzle.
 bool make_map_2d_sw128_elem(CUtensorMap* m, const void* base, uint32_t elem_bytes, uint64_t inner, uint64_t outer,
                             uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);

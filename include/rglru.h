@@ -302,7 +302,7 @@ RGLRU_API rglru_status rglru_mqa_backward(const rglru_mqa_dims* dims, const void
  *           over the slot's 256 elements and code = x / scale rounded to e4m3 (nearest even).
  * A slot with an infinity or a NaN has scale and values that are not finite.  Dims as for
  * rglru_mqa_decode (codes, cache: 16-byte aligned; scales: 4-byte), batch <= 65535,
- * batch * window <= 2^31. */
+ * batch * window <= 2^29. */
 
 /* Quantises the last min(len, window) tokens of every row into their slots: k, v [B, T, d] at
  * positions pos0 .. pos0 + T - 1 (pos0 >= 0, pos0 + T <= 2^31 - 1), len = lengths[b] (device int32

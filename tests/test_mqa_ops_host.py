@@ -60,7 +60,7 @@ def test_bad_sizes():
     for fn in (forward, backward):
         assert fn(_dims(B=1, T=(1 << 30) // 3 + 1, H=3)) == 2          # T H > 2^30
     for fn in (write8, decode8, read8):
-        assert fn(_dims(B=4, w=(1 << 29) + 1)) == 2                     # B w > 2^31
+        assert fn(_dims(B=4, w=(1 << 27) + 1)) == 2                     # B w > 2^29
 
 
 @pytest.mark.parametrize("fn,names", [
