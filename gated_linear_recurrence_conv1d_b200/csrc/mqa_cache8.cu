@@ -29,6 +29,9 @@ using namespace pr;
 constexpr int D = 256;
 constexpr int kMaxH = 16;
 constexpr int kTile = 128;             // slots per tile (the MMA's M)
+constexpr int kHg = kMaxH / 2;         // heads of a group of warps
+// rows of the queries' and weights' operands, columns of S and O: the even heads, then the odd ones
+__host__ __device__ constexpr int head_row(int h) { return (h & 1) * kHg + (h >> 1); }
 constexpr double kFloor = 448.0 * 1.1754943508222875e-38;
 
 // ---- e4m3 ------------------------------------------------------------------------------------------
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(256) mqa_decode8_turn_kernel(int H, int w, Bas
     __shared__ double2 cs[D / 2];
     const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int p = pos[b];
-    if (threadIdx.x == 0) done[b] = 0;
+    if (threadIdx.x < 2) done[2 * b + threadIdx.x] = 0;
     if (p < 0) {                                     // a row without a token
         for (int e = threadIdx.x; e < H * D / 8; e += 256)
             reinterpret_cast<uint4*>(out + (size_t)b * H * D)[e] = make_uint4(0, 0, 0, 0);
@@ -222,7 +225,7 @@ __global__ void __launch_bounds__(256) mqa_decode8_turn_kernel(int H, int w, Bas
         int e2 = (__float_as_int(r448) >> 23) - 127;
         if (__float_as_int(r448) & 0x7fffff) ++e2;
         const float up = __int_as_float((e2 + 127) << 23), down = __int_as_float((127 - e2) << 23);
-        if (lane == 0) qs[b * kMaxH + i] = m < INFINITY ? up : __int_as_float(0x7fffffff);   // an infinity: NaN
+        if (lane == 0) qs[b * kMaxH + head_row(i)] = m < INFINITY ? up : __int_as_float(0x7fffffff);   // an infinity: NaN
         uint32_t c[kQParts][2] = {};
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(256) mqa_decode8_turn_kernel(int H, int w, Bas
         }
 #pragma unroll
         for (int part = 0; part < kQParts; ++part) {
-            uint8_t* row = qp + ((size_t)b * kQRows + part * kMaxH + i) * D;
+            uint8_t* row = qp + ((size_t)b * kQRows + part * kMaxH + head_row(i)) * D;
             reinterpret_cast<uint32_t*>(row)[lane] = c[part][0];
             reinterpret_cast<uint32_t*>(row + D / 2)[lane] = c[part][1];
         }
@@ -251,14 +254,15 @@ __global__ void __launch_bounds__(256) mqa_decode8_turn_kernel(int H, int w, Bas
 // over the SMs whatever the rows' lengths.  Per tile
 //   S^T = K Qp^T   (M 128 slots, N 48 = 16 heads x 3 parts, K 256; e4m3, fp32 sums)
 //   O^T += V^T Wp^T (M 128 columns twice, N 48 = 16 heads x 3 parts, K 128 slots)
-// straight from the codes in shared memory (V^T is the value tile read MN-major).  4 warps, thread = slot:
-// s = (S0 + S1 / 16 + S2 / 256) 2^e c scale_k, p = 2^(s - m) with a reference maximum m per head that moves
+// straight from the codes in shared memory (V^T is the value tile read MN-major).  Two groups of 4 warps, one for
+// the even and one for the odd heads, thread = slot: s = (S0 + S1 / 16 + S2 / 256) 2^e c scale_k, p = 2^(s - m) with a reference maximum m per head that moves
 // when a score passes it by more than 8 times, and the weight p scale_v, normalised by a power of two
 // vref >= the value scales seen so far, as three e5m2 parts: off by at most 2^-9 of itself, half of what bf16
 // would leave, down to weights of 2^-29 (e4m3 parts end at 2^-16, which shows where one slot has nearly all
 // the weight and a small value).  p adds to the thread's own sum in fp32.  O stays in TMEM for the whole segment; when m or vref
-// moves it is rescaled there.  A row inside one segment is written at once; else the segments leave
-// (m, sum, O) and the one that finishes last adds them up in order.
+// moves it is rescaled there (each group has its own vref and its own columns of S, W and O, so the groups
+// never meet).  A row inside one segment is written at once; else the segments leave (m, sum, O) and the
+// one that finishes last adds them up in order.
 // The step reads every code once: bound by HBM.
 constexpr uint32_t TILE_BYTES = kTile * D;            // 32768: 2 boxes of [128 slots x 128 B]
 constexpr int kNBuf = 5;
@@ -266,11 +270,15 @@ constexpr uint32_t Q_BYTES = kQRows * D;              // 12288: 2 boxes of [48 x
 constexpr int kWParts = 3, kWRows = kWParts * kMaxH;
 constexpr uint32_t W_BYTES = kWRows * kTile;          // 6144: [48 x 128 slots]
 constexpr uint32_t OFF_Q = kNBuf * TILE_BYTES, OFF_W = OFF_Q + 2 * Q_BYTES, OFF_QS = OFF_W + 2 * W_BYTES;
-constexpr uint32_t OFF_RED = OFF_QS + 2 * 64, OFF_BAR = OFF_RED + 5 * kMaxH * 4 + 64;
+constexpr uint32_t RED_BYTES = 256;                   // of a group: [4 warps][8 heads], [4] scales
+constexpr uint32_t OFF_RED = OFF_QS + 2 * 64, OFF_MRG = OFF_RED + 2 * RED_BYTES;
+constexpr int kMrgParts = 64;                         // parts whose factors a merge holds at a time
+constexpr uint32_t OFF_BAR = OFF_MRG + 2 * (kMrgParts + 2) * 8 * 4;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TM_S = 0, TM_O = 128, TMEM_COLS = 256;     // S: two buffers, 64 apart; O: two halves, 64 apart
-constexpr int kThreads = 192, kWarpTma = 4, kWarpMma = 5;
+constexpr int kThreads = 320, kWarpTma = 8, kWarpMma = 9;
+
 constexpr float kAlpha = 4096.0f;                     // weights are held as alpha p: p <= 8 keeps them below 57344
 
 struct DecArgs {
@@ -278,9 +286,9 @@ struct DecArgs {
     float scale_log2;
     const int* pos;
     const float* scales;               // [B][2][w]
-    const float* qs;                   // [B][16]
-    unsigned* done;                    // [B]
-    float* part;                       // [B + CTAs][part_pitch]: O [H][d], m [16], sum [16]
+    const float* qs;                   // [B][16], by head_row
+    unsigned* done;                    // [B][2 groups]
+    float* part;                       // [B + CTAs][part_pitch]: m [16], sum [16] by head_row, O [H][d]
     __nv_bfloat16* out;
     DeviceStatus* status;
     unsigned long long timeout_ns;
@@ -357,8 +365,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     auto q_free = [&](uint32_t i) { return bars + 16 * kNBuf + 64 + 8 * i; };
     volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 16 * kNBuf + 80);
     const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 16 * kNBuf + 96), a.status, a.timeout_ns};
-    long long* scan = reinterpret_cast<long long*>(smem);            // before the first load: per-thread sums
-    float* red = reinterpret_cast<float*>(smem + OFF_RED);           // [4 warps][16 heads], [4] scales
+    long long* scan = reinterpret_cast<long long*>(smem);            // before the first load: per-warp sums
     Walk* walk_s = reinterpret_cast<Walk*>(smem + OFF_W);            // before the first weights
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -369,11 +376,11 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 1);
-            mbar_init(w_full(i), 4);
+            mbar_init(w_full(i), 8);
             mbar_init(o_done(i), 1);
-            mbar_init(q_free(i), 4);
+            mbar_init(q_free(i), 8);
         }
-        mbar_init(o_free, 4);
+        mbar_init(o_free, 8);
         mbar_init(mma_done, 1);
         *g.abort = 0;
         fence_barrier_init();
@@ -387,11 +394,18 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const int per = (a.B + kThreads - 1) / kThreads, r0 = min(a.B, (int)threadIdx.x * per), r1 = min(a.B, r0 + per);
         long long mine = 0;
         for (int b = r0; b < r1; ++b) mine += (slots_of(a, b) + kTile - 1) / kTile;
-        scan[threadIdx.x] = mine;
+        long long sum = mine;                                        // through this thread, in the warp
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += u;
+        }
+        if (lane == 31) scan[warp] = sum;
         __syncthreads();
-        long long before = 0, total = 0;
-        for (int i = 0; i < kThreads; ++i) {
-            if (i < (int)threadIdx.x) before += scan[i];
+        long long before = sum - mine, total = 0;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) before += scan[i];
             total += scan[i];
         }
         Walk k;
@@ -513,16 +527,31 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         }
         __syncwarp();
     } else {
-        const int r = threadIdx.x, H = a.H;              // slot of a tile, then column
-        const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
-        asm volatile("griddepcontrol.wait;" ::: "memory");   // the new slot's scales, the rows' counters
+        const int grp = warp >> 2, r = threadIdx.x & 127;            // group; slot of a tile, then column
+        const int nh = (a.H + 1 - grp) >> 1;                         // this group's heads: 2 i + grp, i < nh
+        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + grp * kHg;
+        float* red = reinterpret_cast<float*>(smem + OFF_RED + grp * RED_BYTES);
+        auto grp_or = [&](bool v) {                                  // the OR of v over the group's 128 threads
+            uint32_t o;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.u32 q, %1, 0;\n\t"
+                "barrier.red.or.pred p, %2, 128, q;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(o)
+                : "r"((uint32_t)v), "r"(1 + grp)
+                : "memory");
+            return o != 0;
+        };
+        asm volatile("griddepcontrol.wait;" ::: "memory");           // the new slot's scales, the rows' counters
         uint32_t gt = 0, ns = 0;
         bool ok = true, stop = false;
         for (; !stop && next_seg(a, k, sg); ++ns) {
             const float *sk = a.scales + (size_t)sg.b * 2 * a.w, *sv = sk + a.w;
-            float m[kMaxH], l[kMaxH], vref = 0.f;
+            const float* qs = reinterpret_cast<const float*>(smem + OFF_QS + (ns & 1) * 64) + grp * kHg;
+            float m[kHg], l[kHg], vref = 0.f;
 #pragma unroll
-            for (int h = 0; h < kMaxH; ++h) {
+            for (int h = 0; h < kHg; ++h) {
                 m[h] = -INFINITY;
                 l[h] = 0.f;
             }
@@ -537,8 +566,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 v_next = x < sg.n ? sv[x] : 0.f;
                 ok = ok && wait_w(s_full(buf), (i >> 1) & 1, g, 6);
                 // a tile's last slots may be past the ring's: their codes could be NaN, weight 0 or not
-                const int cnt = min(kTile, sg.n - (sg.t0 + t) * kTile);
-                if (cnt < kTile) {
+                if (grp == 0 && sg.n - (sg.t0 + t) * kTile < kTile) {
                     const uint32_t lv = 2 * i + 1;
                     ok = ok && wait_w(full(lv % kNBuf), (lv / kNBuf) & 1, g, 7);
                     if (ok && !valid)
@@ -548,44 +576,39 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                 make_uint4(0, 0, 0, 0);
                 }
                 tc_fence_after();
-                const float* qs = reinterpret_cast<const float*>(smem + OFF_QS + (ns & 1) * 64);
-                float s[kMaxH];
+                float s[kHg];
                 bool move = vs > vref;
                 {
-                    float s0[16], s1[16], s2[16];
-                    tmem_ld16(tl + TM_S + buf * 64, s0);
-                    tmem_ld16(tl + TM_S + buf * 64 + 16, s1);
-                    tmem_ld16(tl + TM_S + buf * 64 + 32, s2);
+                    float s1[kHg], s2[kHg];
+                    tmem_ld8(tl + TM_S + buf * 64, s);
+                    tmem_ld8(tl + TM_S + buf * 64 + 16, s1);
+                    tmem_ld8(tl + TM_S + buf * 64 + 32, s2);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int h = 0; h < kMaxH; ++h) {
-                        s[h] = -INFINITY;
-                        if (h < H) {
-                            const float d = fmaf(s2[h], 1.0f / 256.0f, fmaf(s1[h], 1.0f / 16.0f, s0[h]));
-                            if (valid) s[h] = d * (qs[h] * ks);
-                            move |= s[h] > m[h] + 3.0f;
-                        }
+                    for (int h = 0; h < kHg; ++h) {
+                        const float d = fmaf(s2[h], 1.0f / 256.0f, fmaf(s1[h], 1.0f / 16.0f, s[h]));
+                        s[h] = valid && h < nh ? d * (qs[h] * ks) : -INFINITY;
+                        move |= s[h] > m[h] + 3.0f;
                     }
                 }
-                if (bar_or(move || !ok, 128)) {
+                if (grp_or(move || !ok)) {
                     // the new reference values from the 4 warps' maxima; O and the sums follow
 #pragma unroll
-                    for (int h = 0; h < kMaxH; ++h)
-                        if (h < H) {
-                            float v = s[h];
+                    for (int h = 0; h < kHg; ++h) {
+                        float v = s[h];
 #pragma unroll
-                            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-                            if (lane == 0) red[warp * kMaxH + h] = v;
-                        }
+                        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+                        if (lane == 0) red[(warp & 3) * kHg + h] = v;
+                    }
                     float v = vs;
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-                    if (lane == 0) red[4 * kMaxH + warp] = v;
-                    if (bar_or(!ok, 128)) {
+                    if (lane == 0) red[4 * kHg + (warp & 3)] = v;
+                    if (grp_or(!ok)) {
                         stop = true;
                         break;
                     }
-                    v = fmaxf(fmaxf(red[4 * kMaxH], red[4 * kMaxH + 1]), fmaxf(red[4 * kMaxH + 2], red[4 * kMaxH + 3]));
+                    v = fmaxf(fmaxf(red[4 * kHg], red[4 * kHg + 1]), fmaxf(red[4 * kHg + 2], red[4 * kHg + 3]));
                     float fv = 1.0f;
                     if (v > vref) {                       // the next power of two, twice over (infinity stays)
                         // (at least 2^-114: alpha / vref is finite, vref / alpha a normal number)
@@ -594,19 +617,18 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         fv = vref == 0.f ? 1.0f : vref / p2;
                         vref = p2;
                     }
-                    float f[kMaxH];
+                    float f[kHg];
                     bool any = fv != 1.0f;
 #pragma unroll
-                    for (int h = 0; h < kMaxH; ++h) {
-                        f[h] = 1.0f;
-                        if (h < H) {
-                            const float mx = fmaxf(fmaxf(red[h], red[kMaxH + h]), fmaxf(red[2 * kMaxH + h], red[3 * kMaxH + h]));
-                            if (mx > m[h] + 3.0f) {
-                                f[h] = m[h] == -INFINITY ? 1.0f : ex2_approx(m[h] - mx);
-                                m[h] = mx;
-                                any = true;
-                            }
-                            l[h] *= f[h];
+                    for (int h = 0; h < kHg; ++h) {
+                        f[h] = fv;
+                        const float mx = fmaxf(fmaxf(red[h], red[kHg + h]), fmaxf(red[2 * kHg + h], red[3 * kHg + h]));
+                        if (mx > m[h] + 3.0f) {
+                            const float e = m[h] == -INFINITY ? 1.0f : ex2_approx(m[h] - mx);
+                            m[h] = mx;
+                            l[h] *= e;
+                            f[h] *= e;
+                            any = true;
                         }
                     }
                     if (t > 0 && any) {
@@ -615,29 +637,29 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 #pragma unroll
                         for (int c = 0; c < 2 * kWParts; ++c) {
                             const uint32_t col = tl + TM_O + (c / kWParts) * 64 + (c % kWParts) * 16;
-                            float o[16];
-                            tmem_ld16(col, o);
+                            float o[kHg];
+                            tmem_ld8(col, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int h = 0; h < kMaxH; ++h) o[h] *= f[h] * fv;
-                            tmem_st16f(col, o);
+                            for (int h = 0; h < kHg; ++h) o[h] *= f[h];
+                            tmem_st8f(col, o);
                         }
                         tmem_wait_st();
                     }
-                    bar_or(false, 128);                   // red is read before the next use
+                    grp_or(false);                        // red is read before the next use
                 }
-                // weights: row part * 16 + head, byte = slot, in 128-byte rows swizzled by the row
-                uint8_t* wb = smem + OFF_W + buf * W_BYTES;
+                // weights: row part * 16 + head row, byte = slot, in 128-byte rows swizzled by the row
+                uint8_t* wb = smem + OFF_W + buf * W_BYTES + grp * (kHg * kTile) + (r & 15);
                 const float wv = fmaf(vs, kAlpha / vref, vs - vs);    // a scale that is not finite: NaN
-                const uint32_t ch = (uint32_t)(r >> 4), lo = (uint32_t)(r & 15);
+                const uint32_t ch = (uint32_t)(r >> 4);
 #pragma unroll
-                for (int h = 0; h < kMaxH; h += 2) {
+                for (int h = 0; h < kHg; h += 2) {
                     uint32_t c[kWParts] = {};
-                    if (h < H) {
-                        const float p0 = valid ? ex2_approx(s[h] - m[h]) : 0.f, p1 = valid && h + 1 < H ? ex2_approx(s[h + 1] - m[h + 1]) : 0.f;
+                    if (h < nh) {
+                        const float p0 = valid ? ex2_approx(s[h] - m[h]) : 0.f, p1 = valid && h + 1 < nh ? ex2_approx(s[h + 1] - m[h + 1]) : 0.f;
                         l[h] += p0;
                         l[h + 1] += p1;
-                        float w0 = valid ? p0 * wv : 0.f, w1 = valid && h + 1 < H ? p1 * wv : 0.f;
+                        float w0 = valid ? p0 * wv : 0.f, w1 = valid && h + 1 < nh ? p1 * wv : 0.f;
 #pragma unroll
                         for (int part = 0; part < kWParts; ++part) {
                             c[part] = e5m2x2(w0, w1);
@@ -646,11 +668,10 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             w1 = (w1 - y.y) * 8.0f;
                         }
                     }
-                    const uint32_t a0 = h * 128 + ((ch ^ (h & 7)) << 4) + lo, a1 = (h + 1) * 128 + ((ch ^ ((h + 1) & 7)) << 4) + lo;
 #pragma unroll
                     for (int part = 0; part < kWParts; ++part) {
-                        wb[a0 + part * (kMaxH * kTile)] = (uint8_t)c[part];
-                        wb[a1 + part * (kMaxH * kTile)] = (uint8_t)(c[part] >> 8);
+                        wb[part * (kMaxH * kTile) + h * 128 + ((ch ^ h) << 4)] = (uint8_t)c[part];
+                        wb[part * (kMaxH * kTile) + (h + 1) * 128 + ((ch ^ (h + 1)) << 4)] = (uint8_t)(c[part] >> 8);
                     }
                 }
                 fence_proxy_async_smem();
@@ -664,85 +685,119 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             gt += sg.nt;
             // sums over the slots: lanes, then warps
 #pragma unroll
-            for (int h = 0; h < kMaxH; ++h)
-                if (h < H) {
+            for (int h = 0; h < kHg; ++h) {
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-                    if (lane == 0) red[warp * kMaxH + h] = l[h];
-                }
+                for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+                if (lane == 0) red[(warp & 3) * kHg + h] = l[h];
+            }
             ok = ok && wait_w(o_done(last & 1), (last >> 1) & 1, g, 9);
-            if (bar_or(!ok, 128)) break;
+            if (grp_or(!ok)) break;
             tc_fence_after();
-            float o[2][kMaxH];
+            float o[2][kHg];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-                float y1[16], y2[16];
-                tmem_ld16(tl + TM_O + hh * 64, o[hh]);
-                tmem_ld16(tl + TM_O + hh * 64 + 16, y1);
-                tmem_ld16(tl + TM_O + hh * 64 + 32, y2);
+                float y1[kHg], y2[kHg];
+                tmem_ld8(tl + TM_O + hh * 64, o[hh]);
+                tmem_ld8(tl + TM_O + hh * 64 + 16, y1);
+                tmem_ld8(tl + TM_O + hh * 64 + 32, y2);
                 tmem_wait_ld();
 #pragma unroll
-                for (int h = 0; h < kMaxH; ++h)
+                for (int h = 0; h < kHg; ++h)
                     o[hh][h] = fmaf(y2[h], 1.0f / 64.0f, fmaf(y1[h], 1.0f / 8.0f, o[hh][h])) * (vref * (1.0f / kAlpha));
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free);
 #pragma unroll
-            for (int h = 0; h < kMaxH; ++h)
-                if (h < H) l[h] = (red[h] + red[kMaxH + h]) + (red[2 * kMaxH + h] + red[3 * kMaxH + h]);
+            for (int h = 0; h < kHg; ++h) l[h] = (red[h] + red[kHg + h]) + (red[2 * kHg + h] + red[3 * kHg + h]);
             if (sg.c0 == sg.c1) {
 #pragma unroll
-                for (int h = 0; h < kMaxH; ++h)
-                    if (h < H) {
+                for (int h = 0; h < kHg; ++h)
+                    if (h < nh) {
                         const float inv = 1.0f / l[h];
-                        __nv_bfloat16* y = a.out + ((size_t)sg.b * H + h) * D + r;
+                        __nv_bfloat16* y = a.out + ((size_t)sg.b * a.H + 2 * h + grp) * D + r;
                         y[0] = __float2bfloat16_rn(o[0][h] * inv);
                         y[128] = __float2bfloat16_rn(o[1][h] * inv);
                     }
-                bar_or(false, 128);                       // red is read before the next use
+                grp_or(false);                            // red is read before the next use
                 continue;
             }
-            const int pitch = part_pitch(H);
+            const int pitch = part_pitch(a.H);
             float* part = a.part + (size_t)(blockIdx.x + sg.b) * pitch;
 #pragma unroll
-            for (int h = 0; h < kMaxH; ++h)
-                if (h < H) {
-                    part[h * D + r] = o[0][h];
-                    part[h * D + 128 + r] = o[1][h];
+            for (int h = 0; h < kHg; ++h)
+                if (h < nh) {
+                    part[2 * kMaxH + (2 * h + grp) * D + r] = o[0][h];
+                    part[2 * kMaxH + (2 * h + grp) * D + 128 + r] = o[1][h];
                     if (r == 0) {
-                        part[H * D + h] = m[h];
-                        part[H * D + kMaxH + h] = l[h];
+                        part[grp * kHg + h] = m[h];
+                        part[kMaxH + grp * kHg + h] = l[h];
                     }
                 }
             __threadfence();
-            bar_or(false, 128);
+            grp_or(false);
             unsigned n = 0;
-            if (r == 0) n = atomicAdd(a.done + sg.b, 1u);
-            const unsigned want = (unsigned)(sg.c1 - sg.c0);
-            if (bar_or(r == 0 && n == want, 128)) {       // the last of the row: the parts in their order
-                __threadfence();
-                const float* p0 = a.part + (size_t)(sg.c0 + sg.b) * pitch;
-                const int np = sg.c1 - sg.c0 + 1;
-                for (int e = r; e < H * (D / 4); e += 128) {
-                    const int h = e / (D / 4);
-                    float mx = -INFINITY, ls = 0.f;
-                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int c = 0; c < np; ++c) mx = fmaxf(mx, __ldcg(p0 + (size_t)c * pitch + H * D + h));
-                    for (int c = 0; c < np; ++c) {
-                        const float* pc = p0 + (size_t)c * pitch;
-                        const float f = ex2_approx(__ldcg(pc + H * D + h) - mx);
-                        const float4 z = __ldcg(reinterpret_cast<const float4*>(pc) + e);
-                        ls = fmaf(__ldcg(pc + H * D + kMaxH + h), f, ls);
-                        y.x = fmaf(z.x, f, y.x);
-                        y.y = fmaf(z.y, f, y.y);
-                        y.z = fmaf(z.z, f, y.z);
-                        y.w = fmaf(z.w, f, y.w);
+            if (r == 0) n = atomicAdd(a.done + 2 * sg.b + grp, 1u);
+            if (!grp_or(r == 0 && n == (unsigned)(sg.c1 - sg.c0))) continue;
+            // the last of the row's segments: their parts in order, kMrgParts at a time.  The factors
+            // 2^(m_c - max) / sum first (thread = part x head), then thread = 4 columns of a head
+            __threadfence();
+            const float* p0 = a.part + (size_t)(sg.c0 + sg.b) * pitch;
+            const int np = sg.c1 - sg.c0 + 1;
+            float* fac = reinterpret_cast<float*>(smem + OFF_MRG) + grp * (kMrgParts + 2) * 8;
+            float *mx_s = fac + kMrgParts * 8, *inv_s = mx_s + 8;
+            {
+                const int h = r & 7, c0 = r >> 3;          // 16 parts side by side
+                float mx = -INFINITY, ls = 0.f;
+                if (h < nh)
+                    for (int c = c0; c < np; c += 16) {
+                        const float mc = __ldcg(p0 + (size_t)c * pitch + grp * kHg + h);
+                        const float lc = __ldcg(p0 + (size_t)c * pitch + kMaxH + grp * kHg + h);
+                        const float mn = fmaxf(mx, mc);
+                        ls = mx == -INFINITY ? lc : fmaf(ls, ex2_approx(mx - mn), lc * ex2_approx(mc - mn));
+                        mx = mn;
                     }
-                    const float inv = 1.0f / ls;
-                    reinterpret_cast<uint2*>(a.out + (size_t)sg.b * H * D)[e] =
-                        make_uint2(bf16x2(y.x * inv, y.y * inv), bf16x2(y.z * inv, y.w * inv));
+                fac[r] = mx;
+                fac[128 + r] = ls;
+                grp_or(false);
+                if (r < 8) {
+                    float mm = -INFINITY, s = 0.f;
+                    for (int c = 0; c < 16; ++c) mm = fmaxf(mm, fac[c * 8 + r]);
+                    for (int c = 0; c < 16; ++c)
+                        if (fac[c * 8 + r] != -INFINITY) s = fmaf(fac[128 + c * 8 + r], ex2_approx(fac[c * 8 + r] - mm), s);
+                    mx_s[r] = mm;
+                    inv_s[r] = 1.0f / s;
                 }
+                grp_or(false);
+            }
+            float4 y[4] = {};                              // heads 2 j + (r >> 6) of the group, columns 4 (r & 63) ...
+            for (int cb = 0; cb < np; cb += kMrgParts) {
+                const int nc = min(kMrgParts, np - cb);
+                for (int e = r; e < nc * 8; e += 128)
+                    if ((e & 7) < nh)
+                        fac[e] = ex2_approx(__ldcg(p0 + (size_t)(cb + (e >> 3)) * pitch + grp * kHg + (e & 7)) - mx_s[e & 7]) * inv_s[e & 7];
+                grp_or(false);
+#pragma unroll 4
+                for (int c = 0; c < nc; ++c) {
+                    const float4* pc = reinterpret_cast<const float4*>(p0 + (size_t)(cb + c) * pitch + 2 * kMaxH) + (r & 63);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int h = 2 * j + (r >> 6);
+                        if (h < nh) {
+                            const float4 z = __ldcg(pc + (2 * h + grp) * (D / 4));
+                            const float f = fac[c * 8 + h];
+                            y[j] = make_float4(fmaf(z.x, f, y[j].x), fmaf(z.y, f, y[j].y), fmaf(z.z, f, y[j].z), fmaf(z.w, f, y[j].w));
+                        }
+                    }
+                }
+                grp_or(false);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int h = 2 * j + (r >> 6);
+                if (h < nh)
+                    reinterpret_cast<uint2*>(a.out + ((size_t)sg.b * a.H + 2 * h + grp) * D)[r & 63] =
+                        make_uint2(bf16x2(y[j].x, y[j].y), bf16x2(y[j].z, y[j].w));
             }
         }
         tmem_wait_ld();
@@ -765,7 +820,7 @@ inline DecLayout dec_layout(const rglru_mqa_dims* d) {
     const size_t B = (size_t)d->batch;
     DecLayout l{};
     size_t o = 256;                    // the status word
-    l.done = o; o = up(o + B * 4);
+    l.done = o; o = up(o + B * 8);
     l.qs = o; o = up(o + B * kMaxH * 4);
     l.qp = o; o = up(o + B * kQRows * D);
     l.part = o; o = up(o + (B + kMaxCtas) * part_pitch(d->q_heads) * 4);
