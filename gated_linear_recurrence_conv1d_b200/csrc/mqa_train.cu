@@ -415,7 +415,7 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(lead_p + 8 * buf);
+                if (lane == 0) mbar_arrive_pair(lead_p + 8 * buf);
             }
             if (stop) break;
             // the row's sum from its two threads, then out = O / l
@@ -443,7 +443,7 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             if (half == 0 && row < a.TH) a.lse[(size_t)t.b * a.THp + row] = m + log2f(l);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead_free);
+            if (lane == 0) mbar_arrive_pair(lead_free);
             gt += t.n;
         }
         tmem_wait_ld();
@@ -712,7 +712,7 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(q_tmem + lead);
+            if (lane == 0) mbar_arrive_pair(q_tmem + lead);
             L += 4 + 3 * t.n;
             bool ok = true;
             for (int j = 0; j < t.n; ++j) {
@@ -724,7 +724,7 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(s_free + lead);
+                if (lane == 0) mbar_arrive_pair(s_free + lead);
                 const int key0 = t.lo + j * BK;
                 const bool whole = key0 >= full_lo && key0 + BK - 1 <= full_hi;
                 const int c_lo = lo_row - (key0 + half * 32), c_hi = tok - (key0 + half * 32);
@@ -745,7 +745,7 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(ds_full + lead);
+                if (lane == 0) mbar_arrive_pair(ds_full + lead);
             }
             if (!ok || !wait_w(dq_done, k & 1, g, 12)) break;
             gt += t.n;
@@ -777,7 +777,7 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(dq_free + lead);
+            if (lane == 0) mbar_arrive_pair(dq_free + lead);
         }
         tmem_wait_ld();
         tmem_wait_st();
@@ -889,7 +889,7 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 1);
             mbar_init(p_full(i), 4);
-            mbar_init(p_here(i), 4);
+            mbar_init(p_here(i), 1);                     // CTA 1 expects the bytes
             mbar_init(p_free(i), 4);
         }
         mbar_init(a_tmem, 8);
@@ -1051,23 +1051,22 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 #pragma unroll
                     for (int c = 0; c < 32; ++c) v[c] = bf16x2(s[2 * c], s[2 * c + 1]);
                     tmem_st32(tl + TM_S + buf * BR, v);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full(buf));
                     // the same to CTA 1, 16 bytes of every thread side by side
                     if (u > 0 && !(ok = wait_w(p_free(buf), (u - 1) & 1, g, 8))) break;
                     const uint32_t dst = peer_p + buf * 16384 + r * 16;
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
-                        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + c * 2048), "r"(v[4 * c]),
-                                     "r"(v[4 * c + 1]), "r"(v[4 * c + 2]), "r"(v[4 * c + 3])
-                                     : "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(peer_here + 8 * buf);
+                        st_async_v4(dst + c * 2048, v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3], peer_here + 8 * buf);
                 } else {
+                    if ((warp & 3) == 0 && lane == 0) mbar_arrive_expect_tx(p_here(buf), 16384);
                     if (!(ok = wait_w(p_here(buf), u & 1, g, 9))) break;
                     const uint8_t* src = smem + OFF_P + buf * 16384 + r * 16;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(v + 4 * c) = *reinterpret_cast<const uint4*>(src + c * 2048);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(peer_free + 8 * buf);
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
@@ -1084,11 +1083,14 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 #pragma unroll
                     for (int c = 0; c < 32; ++c) v[c] = bf16x2(s[2 * c], s[2 * c + 1]);
                     tmem_st32(tl + TM_S + buf * BR, v);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(p_full(buf));
+                        mbar_arrive_pair(peer_free + 8 * buf);       // P^T has been used
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(buf));
             }
             L += sg.n;
             gi += sg.n;

@@ -81,6 +81,21 @@ __device__ __forceinline__ constexpr uint32_t idesc_bf16(int m, int n, int b_mn)
            ((uint32_t)(m >> 4) << 24);
 }
 
+// Arrive on a barrier of either CTA (a shared::cluster address).  What these arrivals hand over is TMEM contents
+// (ordered by the tcgen05 fences around them) or a buffer whose reads are complete, so they need no fence of
+// the other memories at cluster scope, which would hold the warp for hundreds of cycles.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+// 16 bytes into another CTA's shared memory, counted on a barrier there
+__device__ __forceinline__ void st_async_v4(uint32_t dst_cluster, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                            uint32_t bar_cluster) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                     dst_cluster),
+                 "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar_cluster)
+                 : "memory");
+}
+
 // Bounded waits: a wait that expires latches TIMEOUT (site, CTA) and makes every later wait of the CTA fail.
 struct Guard {
     volatile int* abort;               // shared memory, one per CTA
@@ -90,7 +105,7 @@ struct Guard {
 static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Guard& g, unsigned where) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 0;; ++it) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if (*g.abort) return false;
         if (it > 64) __nanosleep(100);
         if (globaltimer_ns() - t0 > g.timeout_ns) {
@@ -101,7 +116,7 @@ static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, con
     }
 }
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Guard& g, unsigned where) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     return wait_slow(bar, parity, g, where);
 }
 // the whole warp follows one wait
