@@ -461,20 +461,20 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 
 // ---------------------------------------------------------------- backward: dq ------------------------
 // A CTA pair takes 256 query rows again and walks their keys in tiles of 64:
-//   S = Q K^T,  dP = dO V^T   (M 256, N 64, K 256; Q in TMEM, dO in shared memory)
+//   S = Q K^T,  dP = dO V^T   (M 256, N 64, K 256; all from shared memory)
 //   dQ += dS K                (M 256, N 256, K 64; dS in TMEM over its dP)
-// TMEM: dQ 256 columns, Q 128, S 64, dP 64.  A CTA loads 32 keys of every K and V tile and 128 columns of
-// every K tile (48 KB per 64 keys).  8 warps, thread = (row, 32 of the 64 keys): P = 2^(c s - L) and
-// dS = P (dP - delta) with the row's L and delta in registers.  The tensor pipe runs S of tile j + 1 while
-// dS of tile j is formed, and dQ of tile j and dP of tile j + 1 while P of tile j + 1 is.
+// TMEM: dQ 256 columns, two buffers of 64 for S and two for dP.  A CTA loads 32 keys of every K and V tile and
+// 128 columns of every K tile (48 KB per 64 keys).  8 warps, thread = (row, 32 of the 64 keys):
+// P = 2^(c s - L) and dS = P (dP - delta) with the row's L and delta in registers.  The tensor pipe runs S
+// and dP of tile j + 1 while dS of tile j is formed.
 namespace bq {
 constexpr int BK = 64;
 constexpr uint32_t SLOT = 16384;
-constexpr int NSLOT = 10;
-constexpr uint32_t OFF_DO = 0, OFF_SLOT = 65536, OFF_BAR = OFF_SLOT + NSLOT * SLOT;
-constexpr uint32_t SMEM_BYTES = OFF_BAR + 512 + 1024;
+constexpr int NSLOT = 6;
+constexpr uint32_t OFF_Q = 0, OFF_DO = 65536, OFF_SLOT = 131072, OFF_BAR = OFF_SLOT + NSLOT * SLOT;
+constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-constexpr uint32_t TM_DQ = 0, TM_Q = 256, TM_S = 384, TM_DP = 448;
+constexpr uint32_t TM_DQ = 0, TM_S = 256, TM_DP = 384;
 constexpr int kThreads = 320, kWarpTma = 8, kWarpMma = 9;
 }  // namespace bq
 
@@ -487,12 +487,14 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
     const uint32_t bars = sb + OFF_BAR;
-    const uint32_t q_full = bars, q_tmem = bars + 8, do_full = bars + 16, do_empty = bars + 24, s_full = bars + 32,
-                   s_free = bars + 40, dp_full = bars + 48, ds_full = bars + 56, dq_done = bars + 64, dq_free = bars + 72,
-                   mma_done = bars + 80;
-    auto full = [&](uint32_t s) { return bars + 96 + 8 * s; };
-    auto empty = [&](uint32_t s) { return bars + 96 + 8 * NSLOT + 8 * s; };
-    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 96 + 16 * NSLOT);
+    const uint32_t q_full = bars, q_empty = bars + 8, do_full = bars + 16, do_empty = bars + 24, dq_done = bars + 32,
+                   dq_free = bars + 40, mma_done = bars + 48;
+    auto s_full = [&](uint32_t i) { return bars + 56 + 8 * i; };
+    auto dp_full = [&](uint32_t i) { return bars + 72 + 8 * i; };
+    auto ds_full = [&](uint32_t i) { return bars + 88 + 8 * i; };
+    auto full = [&](uint32_t s) { return bars + 104 + 8 * s; };
+    auto empty = [&](uint32_t s) { return bars + 104 + 8 * NSLOT + 8 * s; };
+    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 104 + 16 * NSLOT);
     const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 112 + 16 * NSLOT), a.status, a.timeout_ns};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -500,13 +502,14 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
-        mbar_init(q_tmem, 16);
+        mbar_init(q_empty, 1);
         mbar_init(do_full, 1);
         mbar_init(do_empty, 1);
-        mbar_init(s_full, 1);
-        mbar_init(s_free, 16);
-        mbar_init(dp_full, 1);
-        mbar_init(ds_full, 16);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(dp_full(i), 1);
+            mbar_init(ds_full(i), 16);
+        }
         mbar_init(dq_done, 1);
         mbar_init(dq_free, 16);
         mbar_init(mma_done, 1);
@@ -528,72 +531,49 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const uint32_t tmem = *tmem_s;
     QTile t{};
 
-    // Slots in order, per query tile: the four 64-wide column blocks of Q (to TMEM), then Ks_0, Vs_0 and for
-    // every j >= 1 Ks_j, Kd_{j-1}, Vs_j, and Kd_{n-1}: the order of the MMAs.
+    // Slots in order, per query tile: Ks_0, Vs_0 and, for every j >= 1, Ks_j, Vs_j, Kd_{j-1}, and Kd_{n-1}: the order
+    // of the MMAs.
     if (warp == kWarpTma) {
         if (lane == 0) {
             const uint32_t lead = map_to_rank(bars, 0) - bars;
             uint32_t L = 0;
             int k = 0;
             bool ok = true;
-            auto next = [&](uint32_t& s) {                           // wait until the next slot is free
-                s = L % NSLOT;
-                const uint32_t u = L / NSLOT;
+            // the next slot: 32 keys of tile j, all columns (nc = 4), or its 64 keys, 128 columns (nc = 2)
+            auto load = [&](const CUtensorMap* m, int j, int nc) {
+                const uint32_t s = L % NSLOT, u = L / NSLOT;
                 ++L;
-                return u == 0 || wait(empty(s), (u - 1) & 1, g, 1);
-            };
-            auto load = [&](const CUtensorMap* m, int j) {           // 32 keys of tile j, all columns
-                uint32_t s;
-                if (!next(s)) return false;
+                if (u > 0 && !wait(empty(s), (u - 1) & 1, g, 1)) return false;
                 if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * SLOT);
-                for (int c = 0; c < 4; ++c)
-                    tma_load_3d_pair(sb + OFF_SLOT + s * SLOT + c * 4096, m, c * 64, t.lo + j * BK + (int)rank * 32, t.b,
-                                     full(s) + lead);
+                const int col = nc == 4 ? 0 : (int)rank * 128, key = t.lo + j * BK + (nc == 4 ? (int)rank * 32 : 0);
+                for (int c = 0; c < nc; ++c)
+                    tma_load_3d_pair(sb + OFF_SLOT + s * SLOT + c * (SLOT / nc), m, col + c * 64, key, t.b, full(s) + lead);
                 return true;
             };
-            auto load_d = [&](int j) {                               // all 64 keys of tile j, 128 columns
-                uint32_t s;
-                if (!next(s)) return false;
-                if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * SLOT);
-                for (int c = 0; c < 2; ++c)
-                    tma_load_3d_pair(sb + OFF_SLOT + s * SLOT + c * 8192, &map_kd, (int)rank * 128 + c * 64, t.lo + j * BK, t.b,
-                                     full(s) + lead);
+            auto load_rows = [&](const CUtensorMap* m, uint32_t off, uint32_t bar, uint32_t freed) {
+                if (k > 0 && !wait(freed, (k - 1) & 1, g, 2)) return false;
+                if (rank == 0) mbar_arrive_expect_tx(bar, 2 * 65536);
+                for (int c = 0; c < 4; ++c)
+                    tma_load_3d_pair(sb + off + c * 16384, m, c * 64, t.r0 + (int)rank * 128, t.b, bar + lead);
                 return true;
             };
             for (; ok && q_tile<BK>(a, pair, npairs, k, t); ++k) {
-                // Q's blocks complete on a barrier of this CTA: its own warps move them to TMEM
-                if (k > 0 && !(ok = wait(q_full, (k - 1) & 1, g, 13))) break;   // its last phase is over
-                mbar_arrive_expect_tx(q_full, 4 * SLOT);
-                for (int c = 0; ok && c < 4; ++c) {
-                    uint32_t s;
-                    if (!(ok = next(s))) break;
-                    if (rank == 0) mbar_arrive(full(s));             // keeps the slot's phase in step
-                    tma_load_3d(sb + OFF_SLOT + s * SLOT, &map_q, c * 64, t.r0 + (int)rank * 128, t.b, q_full);
-                }
-                ok = ok && load(&map_ks, 0);
-                if (ok && k > 0) ok = wait(do_empty, (k - 1) & 1, g, 2);
-                if (!ok) break;
-                if (rank == 0) mbar_arrive_expect_tx(do_full, 2 * 65536);
-                for (int c = 0; c < 4; ++c)
-                    tma_load_3d_pair(sb + OFF_DO + c * 16384, &map_do, c * 64, t.r0 + (int)rank * 128, t.b, do_full + lead);
-                ok = load(&map_vs, 0);
+                ok = load(&map_ks, 0, 4) && load_rows(&map_q, OFF_Q, q_full, q_empty) && load(&map_vs, 0, 4) &&
+                     load_rows(&map_do, OFF_DO, do_full, do_empty);
                 for (int j = 1; ok && j <= t.n; ++j) {
-                    if (j < t.n) ok = load(&map_ks, j);
-                    ok = ok && load_d(j - 1);
-                    if (j < t.n) ok = ok && load(&map_vs, j);
+                    if (j < t.n) ok = load(&map_ks, j, 4) && load(&map_vs, j, 4);
+                    ok = ok && load(&map_kd, j - 1, 2);
                 }
             }
-            // no bulk copy may still be writing shared memory at the exit
-            const uint64_t t0 = globaltimer_ns();
-            if (k > 0)
-                while (!mbar_try_wait_cluster(q_full, (k - 1) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
-                }
+            // no bulk copy may still be writing shared memory at the exit: the leader sees both CTAs' land
             if (rank == 0) {
+                const uint64_t t0 = globaltimer_ns();
                 for (uint32_t l = L > NSLOT ? L - NSLOT : 0; l < L; ++l)
                     while (!mbar_try_wait_cluster(full(l % NSLOT), (l / NSLOT) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
                     }
                 if (k > 0)
-                    while (!mbar_try_wait_cluster(do_full, (k - 1) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
+                    while (!(mbar_try_wait_cluster(q_full, (k - 1) & 1) && mbar_try_wait_cluster(do_full, (k - 1) & 1)) &&
+                           globaltimer_ns() - t0 < a.timeout_ns) {
                     }
             }
         }
@@ -609,54 +589,38 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 ++L;
                 return wait_w(full(s), u & 1, g, 3);
             };
-            auto issue_s = [&]() {
+            // 256 rows (at off_a) times the 64 keys of the next slot
+            auto issue = [&](uint32_t off_a, uint32_t d, uint32_t done, uint32_t rows_free, bool last) {
                 uint32_t s;
                 if (!ready(s)) return false;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
-                        mma_ts_pair(tm + TM_S, tm + TM_Q + ks * 8,
+                        mma_ss_pair(tm + d, desc_k_sw128(sb + off_a + (ks >> 2) * 16384 + (ks & 3) * 32),
                                     desc_k_sw128(sb + OFF_SLOT + s * SLOT + (ks >> 2) * 4096 + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
-                    mma_commit_pair(s_full);
+                    mma_commit_pair(done);
                     mma_commit_pair(empty(s));
+                    if (last) mma_commit_pair(rows_free);
                 }
                 __syncwarp();
                 return true;
             };
-            auto issue_dp = [&](bool last) {
-                uint32_t s;
-                if (!ready(s)) return false;
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        mma_ss_pair(tm + TM_DP, desc_k_sw128(sb + OFF_DO + (ks >> 2) * 16384 + (ks & 3) * 32),
-                                    desc_k_sw128(sb + OFF_SLOT + s * SLOT + (ks >> 2) * 4096 + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
-                    mma_commit_pair(dp_full);
-                    mma_commit_pair(empty(s));
-                    if (last) mma_commit_pair(do_empty);
-                }
-                __syncwarp();
-                return true;
+            auto issue_s = [&](int j) {
+                const uint32_t buf = (gt + j) & 1;
+                return issue(OFF_Q, TM_S + buf * BK, s_full(buf), q_empty, j == t.n - 1);
+            };
+            auto issue_dp = [&](int j) {
+                const uint32_t buf = (gt + j) & 1;
+                return issue(OFF_DO, TM_DP + buf * BK, dp_full(buf), do_empty, j == t.n - 1);
             };
             for (int k = 0; ok && q_tile<BK>(a, pair, npairs, k, t); ++k) {
-                if (!(ok = wait_w(q_tmem, k & 1, g, 4))) break;      // both CTAs' Q are in TMEM
-                tc_fence_after();
-                if (elect_one())
-                    for (int c = 0; c < 4; ++c) mma_commit_pair(empty((L + c) % NSLOT));
-                __syncwarp();
-                L += 4;
-                if (!(ok = issue_s())) break;
-                if (!(ok = wait_w(do_full, k & 1, g, 5))) break;
-                if (!(ok = issue_dp(t.n == 1))) break;
+                if (!(ok = wait_w(q_full, k & 1, g, 4) && issue_s(0))) break;
+                if (!(ok = wait_w(do_full, k & 1, g, 5) && issue_dp(0))) break;
                 for (int j = 0; ok && j < t.n; ++j) {
-                    const uint32_t par = (gt + j) & 1;
-                    if (j + 1 < t.n) {
-                        if (!(ok = wait_w(s_free, par, g, 6))) break;
-                        if (!(ok = issue_s())) break;
-                    }
-                    if (!(ok = wait_w(ds_full, par, g, 7))) break;
+                    const uint32_t i = gt + j, buf = i & 1;
+                    if (j + 1 < t.n && !(ok = issue_s(j + 1) && issue_dp(j + 1))) break;
+                    if (!(ok = wait_w(ds_full(buf), (i >> 1) & 1, g, 7))) break;
                     if (j == 0 && k > 0 && !(ok = wait_w(dq_free, (k - 1) & 1, g, 8))) break;
                     uint32_t s;
                     if (!(ok = ready(s))) break;
@@ -665,14 +629,13 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         // dS of keys [16 ks, 16 ks + 16): the two halves of a row sit 32 columns apart
 #pragma unroll
                         for (int ks = 0; ks < BK / 16; ++ks)
-                            mma_ts_pair(tm + TM_DQ, tm + TM_DP + (ks >> 1) * 32 + (ks & 1) * 8,
+                            mma_ts_pair(tm + TM_DQ, tm + TM_DP + buf * BK + (ks >> 1) * 32 + (ks & 1) * 8,
                                         desc_mn_sw128(sb + OFF_SLOT + s * SLOT + ks * 2048, 8192), id_q,
                                         (j > 0 || ks > 0) ? 1u : 0u);
                         mma_commit_pair(empty(s));
                         if (j == t.n - 1) mma_commit_pair(dq_done);
                     }
                     __syncwarp();
-                    if (j + 1 < t.n && !(ok = issue_dp(j + 2 == t.n))) break;
                 }
                 gt += t.n;
             }
@@ -689,7 +652,7 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         const int r = (warp & 3) * 32 + lane, half = warp >> 2;
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t lead = map_to_rank(bars, 0) - bars;
-        uint32_t L = 0, gt = 0;
+        uint32_t gt = 0;
         for (int k = 0; q_tile<BK>(a, pair, npairs, k, t); ++k) {
             const int row0 = t.r0 + (int)rank * 128, row = row0 + r;
             const bool live = row < a.TH;
@@ -699,32 +662,14 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             const int full_hi = min(row0, a.TH - 1) / a.H;
             const float lse = live ? a.lse[(size_t)t.b * a.THp + row] : 0.f;
             const float delta = live ? a.delta[(size_t)t.b * a.THp + row] : 0.f;
-            // Q: shared memory (rows of 128 bytes, 16-byte chunks swizzled by the row) to TMEM
-            if (!wait_w(q_full, k & 1, g, 9)) break;
-            for (int c = 2 * half; c < 2 * half + 2; ++c) {
-                const uint8_t* src = smem + OFF_SLOT + ((L + c) % NSLOT) * SLOT + r * 128;
-                uint32_t v[32];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    *reinterpret_cast<uint4*>(v + 4 * e) = *reinterpret_cast<const uint4*>(src + ((e ^ (r & 7)) << 4));
-                tmem_st32(tl + TM_Q + c * 32, v);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_pair(q_tmem + lead);
-            L += 4 + 3 * t.n;
             bool ok = true;
             for (int j = 0; j < t.n; ++j) {
-                const uint32_t par = (gt + j) & 1;
-                if (!(ok = wait_w(s_full, par, g, 10))) break;
+                const uint32_t i = gt + j, buf = i & 1, par = (i >> 1) & 1;
+                if (!(ok = wait_w(s_full(buf), par, g, 10))) break;
                 tc_fence_after();
                 float s[32], dp[32];
-                tmem_ld32(tl + TM_S + half * 32, s);
+                tmem_ld32(tl + TM_S + buf * BK + half * 32, s);
                 tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(s_free + lead);
                 const int key0 = t.lo + j * BK;
                 const bool whole = key0 >= full_lo && key0 + BK - 1 <= full_hi;
                 const int c_lo = lo_row - (key0 + half * 32), c_hi = tok - (key0 + half * 32);
@@ -733,19 +678,19 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     s[c] = ex2_approx(fmaf(s[c], a.scale_log2, -lse));
                     if (!whole) s[c] = (c >= c_lo && c <= c_hi) ? s[c] : 0.f;
                 }
-                if (!(ok = wait_w(dp_full, par, g, 11))) break;
+                if (!(ok = wait_w(dp_full(buf), par, g, 11))) break;
                 tc_fence_after();
-                tmem_ld32(tl + TM_DP + half * 32, dp);
+                tmem_ld32(tl + TM_DP + buf * BK + half * 32, dp);
                 tmem_wait_ld();
                 uint32_t v[16];
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
                     v[c] = bf16x2(s[2 * c] * (dp[2 * c] - delta), s[2 * c + 1] * (dp[2 * c + 1] - delta));
-                tmem_st16(tl + TM_DP + half * 32, v);
+                tmem_st16(tl + TM_DP + buf * BK + half * 32, v);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_pair(ds_full + lead);
+                if (lane == 0) mbar_arrive_pair(ds_full(buf) + lead);
             }
             if (!ok || !wait_w(dq_done, k & 1, g, 12)) break;
             gt += t.n;
@@ -806,10 +751,10 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 // mqa_dkv_sum_kernel adds the parts of a key tile in order: the same bits at every run.
 namespace bk {
 constexpr int BR = 64, BKEY = 128;
-constexpr uint32_t STAGE = 65536;
-constexpr int NST = 3;
-constexpr uint32_t OFF_P = NST * STAGE, OFF_VEC = OFF_P + 2 * 16384, OFF_BAR = OFF_VEC + NST * 256;
-constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
+constexpr uint32_t SLOT = 32768;
+constexpr int NSLOT = 6, NVEC = 4;
+constexpr uint32_t OFF_P = NSLOT * SLOT, OFF_VEC = OFF_P + 2 * 16384, OFF_BAR = OFF_VEC + NVEC * 256;
+constexpr uint32_t SMEM_BYTES = OFF_BAR + 320 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TM_ACC = 0, TM_A = 256, TM_S = 384;
 constexpr int kThreads = 320, kWarpTma = 8, kWarpMma = 9;
@@ -868,23 +813,29 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
     const uint32_t bars = sb + OFF_BAR;
-    auto full = [&](uint32_t s) { return bars + 8 * s; };
-    auto empty = [&](uint32_t s) { return bars + 24 + 8 * s; };
-    auto s_full = [&](uint32_t i) { return bars + 48 + 8 * i; };
-    auto p_full = [&](uint32_t i) { return bars + 64 + 8 * i; };
-    auto p_here = [&](uint32_t i) { return bars + 80 + 8 * i; };     // CTA 1: P^T has arrived
-    auto p_free = [&](uint32_t i) { return bars + 96 + 8 * i; };     // CTA 0: CTA 1 has read it
-    const uint32_t a_tmem = bars + 112, acc_done = bars + 120, mma_done = bars + 128;
-    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 144);
-    const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 160), a.status, a.timeout_ns};
+    auto s_full = [&](uint32_t i) { return bars + 8 * i; };
+    auto p_full = [&](uint32_t i) { return bars + 16 + 8 * i; };
+    auto p_here = [&](uint32_t i) { return bars + 32 + 8 * i; };     // CTA 1: P^T has arrived
+    auto p_free = [&](uint32_t i) { return bars + 48 + 8 * i; };     // CTA 0: CTA 1 has read it
+    const uint32_t a_tmem = bars + 64, acc_done = bars + 72, mma_done = bars + 80;
+    auto v_full = [&](uint32_t i) { return bars + 96 + 8 * i; };
+    auto v_free = [&](uint32_t i) { return bars + 96 + 8 * NVEC + 8 * i; };
+    auto full = [&](uint32_t s) { return bars + 96 + 16 * NVEC + 8 * s; };
+    auto empty = [&](uint32_t s) { return bars + 96 + 16 * NVEC + 8 * NSLOT + 8 * s; };
+    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 96 + 16 * (NVEC + NSLOT));
+    const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 104 + 16 * (NVEC + NSLOT)), a.status, a.timeout_ns};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int cl = blockIdx.x >> 1, G = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NST; ++i) {
+        for (int i = 0; i < NSLOT; ++i) {
             mbar_init(full(i), 1);
             mbar_init(empty(i), 1);
+        }
+        for (int i = 0; i < NVEC; ++i) {
+            mbar_init(v_full(i), 1);
+            mbar_init(v_free(i), 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 1);
@@ -910,77 +861,95 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     Segs segs(a, cl, G);
     Seg sg{};
 
-    // Stages in order, per piece of a key tile: the stationary operand [128 keys], then per row tile Q and dO
-    // [64 rows] and the rows' L (CTA 0) or delta (CTA 1).
+    // Slots in order, per piece of a key tile: the stationary operand's two column halves, then the first
+    // product's rows X_0 and, for every j >= 1, X_j and the second product's rows Y_{j-1}, and Y_{n-1}: the order of
+    // the MMAs, which give an X back long before its Y (CTA 0: X = Q, Y = dO; CTA 1: the other way round).
+    // The rows' L (CTA 0) or delta (CTA 1) have a ring of their own.
     if (warp == kWarpTma) {
         if (lane == 0) {
-            const CUtensorMap* map_a = rank == 0 ? &map_k : &map_v;
+            const CUtensorMap *map_a = rank == 0 ? &map_k : &map_v, *map_x = rank == 0 ? &map_q : &map_do,
+                              *map_y = rank == 0 ? &map_do : &map_q;
             const float* vec = rank == 0 ? a.lse : a.delta;
-            uint32_t L = 0;
+            uint32_t L = 0, gi = 0;
             bool ok = true;
+            auto load = [&](const CUtensorMap* m, int row, uint32_t box, int c0, int nc) {   // nc boxes from column block c0
+                const uint32_t s = L % NSLOT, u = L / NSLOT;
+                ++L;
+                if (u > 0 && !wait(empty(s), (u - 1) & 1, g, 1)) return false;
+                mbar_arrive_expect_tx(full(s), SLOT);
+                for (int c = 0; c < nc; ++c) tma_load_3d(sb + s * SLOT + c * box, m, (c0 + c) * 64, row, sg.b, full(s));
+                return true;
+            };
             while (ok && segs.next(a, sg)) {
-                for (int j = -1; j < sg.n; ++j, ++L) {
-                    const uint32_t s = L % NST, u = L / NST, dst = sb + s * STAGE;
-                    if (u > 0 && !(ok = wait(empty(s), (u - 1) & 1, g, 1))) break;
-                    if (j < 0) {
-                        mbar_arrive_expect_tx(full(s), STAGE);
-                        for (int c = 0; c < 4; ++c) tma_load_3d(dst + c * 16384, map_a, c * 64, sg.key0, sg.b, full(s));
-                    } else {
+                ok = load(map_a, sg.key0, 16384, 0, 2) && load(map_a, sg.key0, 16384, 2, 2);
+                for (int j = 0; ok && j <= sg.n; ++j) {
+                    if (j < sg.n) {
+                        const uint32_t i = gi + j, ve = i % NVEC, u = i / NVEC;
                         const int r = sg.r0 + j * BR;
-                        mbar_arrive_expect_tx(full(s), STAGE + 256);
-                        for (int c = 0; c < 4; ++c) tma_load_3d(dst + c * 8192, &map_q, c * 64, r, sg.b, full(s));
-                        for (int c = 0; c < 4; ++c) tma_load_3d(dst + 32768 + c * 8192, &map_do, c * 64, r, sg.b, full(s));
-                        bulk_load(sb + OFF_VEC + s * 256, vec + (size_t)sg.b * a.THp + r, 256, full(s));
+                        if (!(ok = load(map_x, r, 8192, 0, 4))) break;
+                        if (u > 0 && !(ok = wait(v_free(ve), (u - 1) & 1, g, 11))) break;
+                        mbar_arrive_expect_tx(v_full(ve), 256);
+                        bulk_load(sb + OFF_VEC + ve * 256, vec + (size_t)sg.b * a.THp + r, 256, v_full(ve));
                     }
+                    if (j >= 1) ok = load(map_y, sg.r0 + (j - 1) * BR, 8192, 0, 4);
                 }
+                gi += sg.n;
             }
             const uint64_t t0 = globaltimer_ns();
-            for (uint32_t l = L > NST ? L - NST : 0; l < L; ++l)
-                while (!mbar_try_wait(full(l % NST), (l / NST) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
+            for (uint32_t l = L > NSLOT ? L - NSLOT : 0; l < L; ++l)
+                while (!mbar_try_wait(full(l % NSLOT), (l / NSLOT) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
+                }
+            for (uint32_t l = gi > NVEC ? gi - NVEC : 0; l < gi; ++l)
+                while (!mbar_try_wait(v_full(l % NVEC), (l / NVEC) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
                 }
         }
     } else if (warp == kWarpMma) {
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint32_t id_s = idesc_bf16(128, BR, 0), id_a = idesc_bf16(128, D, 1);
-        const uint32_t off_1 = rank == 0 ? 0 : 32768, off_2 = 32768 - off_1;     // rows of the first, second product
         uint32_t L = 0, gi = 0, ns = 0;
         bool ok = true;
         for (; ok && segs.next(a, sg); ++ns) {
             if (!(ok = wait_w(a_tmem, ns & 1, g, 2))) break;
             tc_fence_after();
-            if (elect_one()) mma_commit(empty(L % NST));
+            if (elect_one()) {
+                mma_commit(empty(L % NSLOT));
+                mma_commit(empty((L + 1) % NSLOT));
+            }
             __syncwarp();
-            ++L;
+            L += 2;
             for (int j = 0; ok && j <= sg.n; ++j) {
                 if (j < sg.n) {
-                    const uint32_t l = L + j, s = l % NST, buf = (gi + j) & 1;
-                    if (!(ok = wait_w(full(s), (l / NST) & 1, g, 3))) break;
+                    const uint32_t s = L % NSLOT, buf = (gi + j) & 1;
+                    if (!(ok = wait_w(full(s), (L / NSLOT) & 1, g, 3))) break;
+                    ++L;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks)
                             mma_ts(tm + TM_S + buf * BR, tm + TM_A + ks * 8,
-                                   desc_k_sw128(sb + s * STAGE + off_1 + (ks >> 2) * 8192 + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
+                                   desc_k_sw128(sb + s * SLOT + (ks >> 2) * 8192 + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
                         mma_commit(s_full(buf));
+                        mma_commit(empty(s));
                     }
                     __syncwarp();
                 }
                 if (j >= 1) {
-                    const uint32_t l = L + j - 1, s = l % NST, i = gi + j - 1, buf = i & 1;
+                    const uint32_t s = L % NSLOT, i = gi + j - 1, buf = i & 1;
+                    if (!(ok = wait_w(full(s), (L / NSLOT) & 1, g, 12))) break;
                     if (!(ok = wait_w(p_full(buf), (i >> 1) & 1, g, 4))) break;
+                    ++L;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < BR / 16; ++ks)
-                            mma_ts(tm + TM_ACC, tm + TM_S + buf * BR + ks * 8,
-                                   desc_mn_sw128(sb + s * STAGE + off_2 + ks * 2048, 8192), id_a, (j > 1 || ks > 0) ? 1u : 0u);
+                            mma_ts(tm + TM_ACC, tm + TM_S + buf * BR + ks * 8, desc_mn_sw128(sb + s * SLOT + ks * 2048, 8192), id_a,
+                                   (j > 1 || ks > 0) ? 1u : 0u);
                         mma_commit(empty(s));
                         if (j == sg.n) mma_commit(acc_done);
                     }
                     __syncwarp();
                 }
             }
-            L += sg.n;
             gi += sg.n;
         }
         if (elect_one()) mma_commit(mma_done);
@@ -1006,9 +975,11 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             const int row_lo = key < a.T ? key * a.H : 0x7fffffff, row_hi = key < a.T ? (lt[key] + 1) * a.H - 1 : -1;
             // rows that every key of the tile sees
             const int all_lo = sg.key0 + BKEY <= a.T ? last_key * a.H : 0x7fffffff, all_hi = (lt[sg.key0] + 1) * a.H - 1;
-            if (!(ok = wait_w(full(L % NST), (L / NST) & 1, g, 5))) break;
+            // the stationary operand's columns [128 wg, +128): shared memory (swizzled rows) to TMEM
+            const uint32_t la = L + wg;
+            if (!(ok = wait_w(full(la % NSLOT), (la / NSLOT) & 1, g, 5))) break;
             for (int c = 2 * wg; c < 2 * wg + 2; ++c) {
-                const uint8_t* src = smem + (L % NST) * STAGE + c * 16384 + r * 128;
+                const uint8_t* src = smem + (la % NSLOT) * SLOT + (c & 1) * 16384 + r * 128;
                 uint32_t v[32];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -1019,17 +990,17 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(a_tmem);
-            ++L;
+            L += 2 + 2 * sg.n;
             for (int j = 0; j < sg.n; ++j) {
-                const uint32_t i = gi + j, buf = i & 1, u = i >> 1, l = L + j, st = l % NST;
+                const uint32_t i = gi + j, buf = i & 1, u = i >> 1, ve = i % NVEC;
                 if ((int)buf != wg) continue;
-                if (!(ok = wait_w(full(st), (l / NST) & 1, g, 6))) break;      // L or delta
+                if (!(ok = wait_w(v_full(ve), (i / NVEC) & 1, g, 6))) break;   // L or delta
                 if (!(ok = wait_w(s_full(buf), u & 1, g, 7))) break;
                 tc_fence_after();
                 float s[64];
                 tmem_ld32(tl + TM_S + buf * BR, s);
                 tmem_ld32(tl + TM_S + buf * BR + 32, s + 32);
-                const float4* vec = reinterpret_cast<const float4*>(smem + OFF_VEC + st * 256);
+                const float4* vec = reinterpret_cast<const float4*>(smem + OFF_VEC + ve * 256);
                 const int r0 = sg.r0 + j * BR;
                 const bool whole = r0 >= all_lo && r0 + BR - 1 <= all_hi;
                 const int c_lo = row_lo - r0, c_hi = row_hi - r0;
@@ -1054,7 +1025,10 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(p_full(buf));
+                    if (lane == 0) {
+                        mbar_arrive(p_full(buf));
+                        mbar_arrive(v_free(ve));
+                    }
                     // the same to CTA 1, 16 bytes of every thread side by side
                     if (u > 0 && !(ok = wait_w(p_free(buf), (u - 1) & 1, g, 8))) break;
                     const uint32_t dst = peer_p + buf * 16384 + r * 16;
@@ -1088,11 +1062,11 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(p_full(buf));
+                        mbar_arrive(v_free(ve));
                         mbar_arrive_pair(peer_free + 8 * buf);       // P^T has been used
                     }
                 }
             }
-            L += sg.n;
             gi += sg.n;
             if (!ok || !(ok = wait_w(acc_done, ns & 1, g, 10))) break;
             tc_fence_after();
