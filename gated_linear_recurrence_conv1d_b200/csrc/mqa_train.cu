@@ -149,19 +149,36 @@ struct Args {
 // the CTA pairs forwards and backwards in turn, so that every pair gets long and short ones alike.
 // lo_t is non-decreasing in t, so a tile's keys are [lo of its first token, its last token].
 struct QTile {
-    int b, r0, lo, n;           // batch row, first query row of the pair, first key, key tiles
+    int b, r0, lo, t1;          // batch row, first query row of the pair, first key, last token
 };
+// walks a pair's tiles; the load of the next tile's first key is in flight while a tile is worked on
 template <int BK>
-__device__ __forceinline__ bool q_tile(const Args& a, int pair, int npairs, int k, QTile& t) {
-    const int p = k * npairs + ((k & 1) ? npairs - 1 - pair : pair);
-    if (p >= a.B * a.ntr) return false;
-    t.b = p % a.B;
-    t.r0 = (a.ntr - 1 - p / a.B) * 256;
-    const int t0 = t.r0 / a.H, t1 = min(t.r0 + 255, a.TH - 1) / a.H;
-    t.lo = a.lo[(size_t)t.b * a.T + t0];
-    t.n = (t1 + 1 - t.lo + BK - 1) / BK;
-    return true;
-}
+struct QTiles {
+    QTile t, nx;
+    int k, n;                   // number of the tile, its key tiles; k = -1 before the first advance()
+    bool has;
+    int pair, npairs;
+    __device__ __forceinline__ void fetch(const Args& a, int i) {
+        const int p = i * npairs + ((i & 1) ? npairs - 1 - pair : pair);
+        has = p < a.B * a.ntr;
+        if (!has) return;
+        nx.b = p % a.B;
+        nx.r0 = (a.ntr - 1 - p / a.B) * 256;
+        nx.t1 = min(nx.r0 + 255, a.TH - 1) / a.H;
+        nx.lo = a.lo[(size_t)nx.b * a.T + nx.r0 / a.H];
+    }
+    __device__ __forceinline__ QTiles(const Args& a, int pair_, int npairs_) : t{}, nx{}, k(-1), n(0), pair(pair_), npairs(npairs_) {
+        fetch(a, 0);
+    }
+    __device__ __forceinline__ bool advance(const Args& a) {
+        ++k;
+        if (!has) return false;
+        t = nx;
+        n = (t.t1 + 1 - t.lo + BK - 1) / BK;
+        fetch(a, k + 1);
+        return true;
+    }
+};
 
 // ---------------------------------------------------------------- forward -----------------------------
 // A CTA pair (cta_group::2) takes 256 query rows, 128 a CTA, and walks the keys that any of them sees in tiles of 128:
@@ -181,7 +198,7 @@ constexpr uint32_t OFF_Q = 0, OFF_SLOT = 65536, OFF_X = OFF_SLOT + NSLOT * SLOT,
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TM_O = 0, TM_S = 256;
-constexpr int kThreads = 320, kSoft = 256, kWarpTma = 8, kWarpMma = 9;
+constexpr int kThreads = 352, kSoft = 256, kWarpTma = 8, kWarpMma = 9, kWarpQ = 10;
 }  // namespace fw
 
 __global__ void __launch_bounds__(fw::kThreads, 1)
@@ -231,41 +248,48 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
-    QTile t{};
 
     if (warp == kWarpTma) {
         if (lane == 0) {
             const uint32_t lead = map_to_rank(bars, 0) - bars;      // this CTA's barrier address -> the leader's
             uint32_t L = 0;
-            int k = 0;
             bool ok = true;
             // key tile j of the values (v) or keys into the next slot
-            auto load = [&](bool v, int j) {
+            auto load = [&](bool v, const QTile& q, int j) {
                 const uint32_t s = L % NSLOT, u = L / NSLOT;
                 if (u > 0 && !wait(empty(s), (u - 1) & 1, g, 1)) return false;
                 if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * SLOT);
                 const uint32_t dst = sb + OFF_SLOT + s * SLOT, bar = full(s) + lead;
-                const int key0 = t.lo + j * BK;
+                const int key0 = q.lo + j * BK;
                 if (v) {
                     for (int c = 0; c < 2; ++c)
-                        tma_load_3d_pair(dst + c * 16384, &map_v, (int)rank * 128 + c * 64, key0, t.b, bar);
+                        tma_load_3d_pair(dst + c * 16384, &map_v, (int)rank * 128 + c * 64, key0, q.b, bar);
                 } else {
                     for (int c = 0; c < 4; ++c)
-                        tma_load_3d_pair(dst + c * 8192, &map_k, c * 64, key0 + (int)rank * 64, t.b, bar);
+                        tma_load_3d_pair(dst + c * 8192, &map_k, c * 64, key0 + (int)rank * 64, q.b, bar);
                 }
                 ++L;
                 return true;
             };
-            for (; ok && q_tile<BK>(a, pair, npairs, k, t); ++k) {
-                ok = load(false, 0);                                 // keys first: Q's buffer frees later
-                if (ok && k > 0) ok = wait(q_empty, (k - 1) & 1, g, 2);
-                if (!ok) break;
-                if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * 65536);
-                for (int c = 0; c < 4; ++c)
-                    tma_load_3d_pair(sb + OFF_Q + c * 16384, &map_q, c * 64, t.r0 + (int)rank * 128, t.b, q_full + lead);
-                for (int j = 1; ok && j <= t.n; ++j) {
-                    if (j < t.n) ok = load(false, j);
-                    if (ok) ok = load(true, j - 1);
+            // in the order of the MMAs: K two key tiles ahead of V, across query tiles
+            QTiles<BK> qk(a, pair, npairs), qv = qk;
+            int jk = 0, jv = 0, ahead = 0;
+            bool ks = qk.advance(a), vs = qv.advance(a);
+            while (ok && vs) {
+                if (ks && ahead < 2) {
+                    if (!(ok = load(false, qk.t, jk))) break;
+                    ++ahead;
+                    if (++jk == qk.n) {
+                        jk = 0;
+                        ks = qk.advance(a);
+                    }
+                    continue;
+                }
+                if (!(ok = load(true, qv.t, jv))) break;
+                --ahead;
+                if (++jv == qv.n) {
+                    jv = 0;
+                    vs = qv.advance(a);
                 }
             }
             // no bulk copy may still be writing shared memory at the exit: the leader sees both CTAs' land
@@ -274,59 +298,85 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 for (uint32_t l = L > NSLOT ? L - NSLOT : 0; l < L; ++l)
                     while (!mbar_try_wait_cluster(full(l % NSLOT), (l / NSLOT) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
                     }
-                if (k > 0)
-                    while (!mbar_try_wait_cluster(q_full, (k - 1) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
-                    }
             }
+        }
+    } else if (warp == kWarpQ) {
+        // the query tiles: each as soon as the S before it are through with the buffer
+        if (lane == 0) {
+            const uint32_t lead = map_to_rank(bars, 0) - bars;
+            QTiles<BK> q(a, pair, npairs);
+            while (q.advance(a)) {
+                if (q.k > 0 && !wait(q_empty, (q.k - 1) & 1, g, 2)) break;
+                if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * 65536);
+                for (int c = 0; c < 4; ++c)
+                    tma_load_3d_pair(sb + OFF_Q + c * 16384, &map_q, c * 64, q.t.r0 + (int)rank * 128, q.t.b, q_full + lead);
+            }
+            const uint64_t t0 = globaltimer_ns();
+            if (rank == 0 && q.k > 0)
+                while (!mbar_try_wait_cluster(q_full, (q.k - 1) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
+                }
         }
     } else if (warp == kWarpMma) {
         if (rank == 0) {
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t id_s = idesc_bf16(256, BK, 0), id_o = idesc_bf16(256, D, 1);
-            uint32_t L = 0, gt = 0;                                  // slots used, key tiles before this query tile
-            bool ok = true;
-            for (int k = 0; ok && q_tile<BK>(a, pair, npairs, k, t); ++k) {
-                if (!(ok = wait_w(q_full, k & 1, g, 3))) break;
-                for (int j = 0; ok && j <= t.n; ++j) {
-                    if (j < t.n) {                                   // S_j
-                        const uint32_t s = L % NSLOT, buf = (gt + j) & 1;
-                        if (!(ok = wait_w(full(s), (L / NSLOT) & 1, g, 4))) break;
-                        ++L;
-                        tc_fence_after();
-                        if (elect_one()) {
+            // S runs two key tiles ahead of P V, across query tiles.  The queue of the tensor pipe is two MMAs deep: what
+            // is waited for right behind the P V MMAs costs nothing, so the next S's operands and the next V
+            // are; only the wait for the next P is not covered
+            QTiles<BK> qs(a, pair, npairs), qp = qs;
+            int js = 0;
+            uint32_t L = 0, gt = 0, gs = 0;                          // slots used; key tiles done, key tiles with S issued
+            bool more = qs.advance(a), ok = true;
+            auto wait_slot = [&](uint32_t l) { return wait_w(full(l % NSLOT), (l / NSLOT) & 1, g, 4); };
+            auto issue_s = [&]() {                                   // S of the next key tile, from the next slot
+                if (js == 0 && !wait_w(q_full, qs.k & 1, g, 3)) return false;
+                if (!wait_slot(L)) return false;
+                tc_fence_after();
+                const uint32_t s = L % NSLOT, buf = gs & 1;
+                ++L;
+                ++gs;
+                const bool last = ++js == qs.n;
+                if (elect_one()) {
 #pragma unroll
-                            for (int ks = 0; ks < D / 16; ++ks)
-                                mma_ss_pair(tm + TM_S + buf * BK, desc_k_sw128(sb + OFF_Q + (ks >> 2) * 16384 + (ks & 3) * 32),
-                                            desc_k_sw128(sb + OFF_SLOT + s * SLOT + (ks >> 2) * 8192 + (ks & 3) * 32), id_s,
-                                            ks > 0 ? 1u : 0u);
-                            mma_commit_pair(s_full(buf));
-                            mma_commit_pair(empty(s));
-                            if (j == t.n - 1) mma_commit_pair(q_empty);
-                        }
-                        __syncwarp();
-                    }
-                    if (j >= 1) {                                    // O += P_{j-1} V_{j-1}
-                        const uint32_t i = gt + j - 1, buf = i & 1, s = L % NSLOT;
-                        if (j == 1 && k > 0 && !(ok = wait_w(o_free, (k - 1) & 1, g, 5))) break;
-                        if (!(ok = wait_w(p_full(buf), (i >> 1) & 1, g, 6))) break;
-                        if (!(ok = wait_w(full(s), (L / NSLOT) & 1, g, 7))) break;
-                        ++L;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            // P of keys [16 ks, 16 ks + 16): the two halves of a row sit 64 columns apart
-#pragma unroll
-                            for (int ks = 0; ks < BK / 16; ++ks)
-                                mma_ts_pair(tm + TM_O, tm + TM_S + buf * BK + (ks >> 2) * 64 + (ks & 3) * 8,
-                                            desc_mn_sw128(sb + OFF_SLOT + s * SLOT + ks * 2048, 16384), id_o,
-                                            (j > 1 || ks > 0) ? 1u : 0u);
-                            mma_commit_pair(o_done(buf));
-                            mma_commit_pair(empty(s));
-                        }
-                        __syncwarp();
-                    }
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_ss_pair(tm + TM_S + buf * BK, desc_k_sw128(sb + OFF_Q + (ks >> 2) * 16384 + (ks & 3) * 32),
+                                    desc_k_sw128(sb + OFF_SLOT + s * SLOT + (ks >> 2) * 8192 + (ks & 3) * 32), id_s,
+                                    ks > 0 ? 1u : 0u);
+                    mma_commit_pair(s_full(buf));
+                    mma_commit_pair(empty(s));
+                    if (last) mma_commit_pair(q_empty);
                 }
-                gt += t.n;
-            }
+                __syncwarp();
+                if (last) {
+                    js = 0;
+                    more = qs.advance(a);
+                }
+                return true;
+            };
+            for (int i = 0; ok && more && i < 2; ++i) ok = issue_s();
+            while (ok && qp.advance(a))
+                for (int j = 0; j < qp.n; ++j, ++gt) {
+                    const uint32_t buf = gt & 1, s = L % NSLOT;
+                    if (gt == 0 && !(ok = wait_slot(L))) break;
+                    if (j == 0 && qp.k > 0 && !(ok = wait_w(o_free, (qp.k - 1) & 1, g, 5))) break;
+                    if (!(ok = wait_w(p_full(buf), (gt >> 1) & 1, g, 6))) break;
+                    ++L;
+                    tc_fence_after();
+                    if (elect_one()) {                               // O += P_j V_j
+                        // P of keys [16 ks, 16 ks + 16): the two halves of a row sit 64 columns apart
+#pragma unroll
+                        for (int ks = 0; ks < BK / 16; ++ks)
+                            mma_ts_pair(tm + TM_O, tm + TM_S + buf * BK + (ks >> 2) * 64 + (ks & 3) * 8,
+                                        desc_mn_sw128(sb + OFF_SLOT + s * SLOT + ks * 2048, 16384), id_o,
+                                        (j > 0 || ks > 0) ? 1u : 0u);
+                        mma_commit_pair(o_done(buf));
+                        mma_commit_pair(empty(s));
+                    }
+                    __syncwarp();
+                    const bool next = j + 1 < qp.n || qp.has;        // another V follows, behind the next K if there is one
+                    if (next && !(ok = wait_slot(more ? L + 1 : L))) break;
+                    if (more && !(ok = issue_s())) break;
+                }
             if (elect_one()) mma_commit_pair(mma_done);              // every MMA is over before TMEM is released
             __syncwarp();
         }
@@ -343,14 +393,50 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const uint32_t lead_p = map_to_rank(p_full(0), 0), lead_free = map_to_rank(o_free, 0);
         uint32_t gt = 0;
         bool ok = true, stop = false;
-        for (int k = 0; !stop && q_tile<BK>(a, pair, npairs, k, t); ++k) {
+        // out = O / l of the query tile before, its last key tile number `last`, done between the first P of the
+        // next query tile and the next: the tensor pipe has that P and two S ahead of it meanwhile
+        bool pending = false;
+        int p_b = 0, p_row = 0;
+        float p_m = 0.f, p_l = 0.f;
+        auto finish = [&](uint32_t last) {
+            ok = ok && wait_w(o_done(last & 1), (last >> 1) & 1, g, 10);
+            bar_or(false, kSoft);                         // xch has been read
+            xch[half * 128 + r] = p_l;
+            if (bar_or(!ok, kSoft)) return false;
+            const float l = xch[r] + xch[128 + r];        // the row's sum from its two threads
+            bar_or(false, kSoft);                         // xch is read before its next use
+            tc_fence_after();
+            const float inv = 1.0f / l;
+            __nv_bfloat16* orow = a.out + ((size_t)p_b * a.TH + p_row) * D + half * 128;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                float o[32];
+                tmem_ld32(tl + TM_O + half * 128 + c, o);
+                tmem_wait_ld();
+                if (p_row < a.TH) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        reinterpret_cast<uint4*>(orow + c)[e] =
+                            make_uint4(bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                       bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                }
+            }
+            if (half == 0 && p_row < a.TH) a.lse[(size_t)p_b * a.THp + p_row] = p_m + log2f(l);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(lead_free);
+            return true;
+        };
+        QTiles<BK> q(a, pair, npairs);
+        while (!stop && q.advance(a)) {
+            const QTile t = q.t;
             const int row0 = t.r0 + (int)rank * 128, row = row0 + r;
             const int tok = min(row, a.TH - 1) / a.H;
             const int lo_row = a.lo[(size_t)t.b * a.T + tok];
             // a tile inside every row's keys needs no mask: [lo of the CTA's last token, its first token]
             const int full_lo = a.lo[(size_t)t.b * a.T + min(row0 + 127, a.TH - 1) / a.H], full_hi = min(row0, a.TH - 1) / a.H;
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < t.n; ++j) {
+            for (int j = 0; j < q.n; ++j) {
                 const uint32_t i = gt + j, buf = i & 1;
                 ok = ok && wait_w(s_full(buf), (i >> 1) & 1, g, 8);
                 tc_fence_after();
@@ -416,36 +502,20 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(lead_p + 8 * buf);
-            }
-            if (stop) break;
-            // the row's sum from its two threads, then out = O / l
-            const uint32_t i = gt + t.n - 1;
-            ok = ok && wait_w(o_done(i & 1), (i >> 1) & 1, g, 10);
-            xch[half * 128 + r] = l;
-            if (bar_or(!ok, kSoft)) break;
-            l = xch[r] + xch[128 + r];
-            tc_fence_after();
-            const float inv = 1.0f / l;
-            __nv_bfloat16* orow = a.out + ((size_t)t.b * a.TH + row) * D + half * 128;
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                float o[32];
-                tmem_ld32(tl + TM_O + half * 128 + c, o);
-                tmem_wait_ld();
-                if (row < a.TH) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        reinterpret_cast<uint4*>(orow + c)[e] =
-                            make_uint4(bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                       bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                if (j == 0 && pending && !finish(gt - 1)) {
+                    stop = true;
+                    break;
                 }
             }
-            if (half == 0 && row < a.TH) a.lse[(size_t)t.b * a.THp + row] = m + log2f(l);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_pair(lead_free);
-            gt += t.n;
+            if (stop) break;
+            pending = true;
+            p_b = t.b;
+            p_row = row;
+            p_m = m;
+            p_l = l;
+            gt += q.n;
         }
+        if (!stop && pending) finish(gt - 1);
         tmem_wait_ld();
         tmem_wait_st();
     }
@@ -460,22 +530,25 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 }
 
 // ---------------------------------------------------------------- backward: dq ------------------------
-// A CTA pair takes 256 query rows again and walks their keys in tiles of 64:
-//   S = Q K^T,  dP = dO V^T   (M 256, N 64, K 256; all from shared memory)
-//   dQ += dS K                (M 256, N 256, K 64; dS in TMEM over its dP)
-// TMEM: dQ 256 columns, two buffers of 64 for S and two for dP.  A CTA loads 32 keys of every K and V tile and
-// 128 columns of every K tile (48 KB per 64 keys).  8 warps, thread = (row, 32 of the 64 keys):
-// P = 2^(c s - L) and dS = P (dP - delta) with the row's L and delta in registers.  The tensor pipe runs S
-// and dP of tile j + 1 while dS of tile j is formed.
+// A CTA pair takes 256 query rows again and walks their keys in tiles of 128:
+//   S = Q K^T,  dP = dO V^T   (M 256, N 128, K 256; all from shared memory)
+//   dQ += dS K                (M 256, N 256, K 128; dS in TMEM over its dP)
+// TMEM: dQ 256 columns, S 128, dP 128.  A CTA loads 64 keys of every K and V tile and 128 columns of every K tile,
+// each into a buffer of its own: S of tile j + 1, dQ of tile j, dP of tile j + 1 follow each other in the tensor
+// pipe, so each has the other two's time to arrive, and dS of tile j is formed under S of tile j + 1.
+// 8 warps, thread = (row, 64 of the 128 keys): P = 2^(c s - L), dS = P (dP - delta), the row's L and delta in
+// registers.  dq of a query tile is written after the first dS of the next.
+// (Key tiles of 64 with two buffers of S and dP: 1.5 times slower.  An MMA of N 64 reads 5 KB of shared memory a CTA
+// in the time of 32 cycles, one of N 128 6 KB in 64, and shared memory gives 128 bytes a cycle.)
 namespace bq {
-constexpr int BK = 64;
-constexpr uint32_t SLOT = 16384;
-constexpr int NSLOT = 6;
+constexpr int BK = 128;
+constexpr uint32_t SLOT = 32768;
+constexpr int NSLOT = 3, KS = 0, VS = 1, KD = 2;         // K by keys, V by keys, K by columns
 constexpr uint32_t OFF_Q = 0, OFF_DO = 65536, OFF_SLOT = 131072, OFF_BAR = OFF_SLOT + NSLOT * SLOT;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TM_DQ = 0, TM_S = 256, TM_DP = 384;
-constexpr int kThreads = 320, kWarpTma = 8, kWarpMma = 9;
+constexpr int kThreads = 352, kWarpTma = 8, kWarpMma = 9, kWarpQ = 10;
 }  // namespace bq
 
 __global__ void __launch_bounds__(bq::kThreads, 1)
@@ -488,14 +561,12 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const uint32_t sb = smem_u32(smem);
     const uint32_t bars = sb + OFF_BAR;
     const uint32_t q_full = bars, q_empty = bars + 8, do_full = bars + 16, do_empty = bars + 24, dq_done = bars + 32,
-                   dq_free = bars + 40, mma_done = bars + 48;
-    auto s_full = [&](uint32_t i) { return bars + 56 + 8 * i; };
-    auto dp_full = [&](uint32_t i) { return bars + 72 + 8 * i; };
-    auto ds_full = [&](uint32_t i) { return bars + 88 + 8 * i; };
-    auto full = [&](uint32_t s) { return bars + 104 + 8 * s; };
-    auto empty = [&](uint32_t s) { return bars + 104 + 8 * NSLOT + 8 * s; };
-    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 104 + 16 * NSLOT);
-    const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 112 + 16 * NSLOT), a.status, a.timeout_ns};
+                   dq_free = bars + 40, mma_done = bars + 48, s_full = bars + 56, s_free = bars + 64, dp_full = bars + 72,
+                   ds_full = bars + 80;
+    auto full = [&](uint32_t s) { return bars + 88 + 8 * s; };
+    auto empty = [&](uint32_t s) { return bars + 88 + 8 * NSLOT + 8 * s; };
+    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 88 + 16 * NSLOT);
+    const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 96 + 16 * NSLOT), a.status, a.timeout_ns};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
@@ -505,11 +576,10 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         mbar_init(q_empty, 1);
         mbar_init(do_full, 1);
         mbar_init(do_empty, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(s_full(i), 1);
-            mbar_init(dp_full(i), 1);
-            mbar_init(ds_full(i), 16);
-        }
+        mbar_init(s_full, 1);
+        mbar_init(s_free, 16);
+        mbar_init(dp_full, 1);
+        mbar_init(ds_full, 16);
         mbar_init(dq_done, 1);
         mbar_init(dq_free, 16);
         mbar_init(mma_done, 1);
@@ -529,116 +599,138 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
-    QTile t{};
 
-    // Slots in order, per query tile: Ks_0, Vs_0 and, for every j >= 1, Ks_j, Vs_j, Kd_{j-1}, and Kd_{n-1}: the order
-    // of the MMAs.
+    // Number i of the pair's key tiles uses each of the three buffers for the i-th time.
     if (warp == kWarpTma) {
         if (lane == 0) {
             const uint32_t lead = map_to_rank(bars, 0) - bars;
-            uint32_t L = 0;
-            int k = 0;
             bool ok = true;
-            // the next slot: 32 keys of tile j, all columns (nc = 4), or its 64 keys, 128 columns (nc = 2)
-            auto load = [&](const CUtensorMap* m, int j, int nc) {
-                const uint32_t s = L % NSLOT, u = L / NSLOT;
-                ++L;
-                if (u > 0 && !wait(empty(s), (u - 1) & 1, g, 1)) return false;
-                if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * SLOT);
-                const int col = nc == 4 ? 0 : (int)rank * 128, key = t.lo + j * BK + (nc == 4 ? (int)rank * 32 : 0);
-                for (int c = 0; c < nc; ++c)
-                    tma_load_3d_pair(sb + OFF_SLOT + s * SLOT + c * (SLOT / nc), m, col + c * 64, key, t.b, full(s) + lead);
+            uint32_t n_loads[NSLOT] = {};
+            auto load = [&](uint32_t slot, const CUtensorMap* m, const QTile& q, int j, uint32_t i) {
+                if (i > 0 && !wait(empty(slot), (i - 1) & 1, g, 1)) return false;
+                n_loads[slot] = i + 1;
+                if (rank == 0) mbar_arrive_expect_tx(full(slot), 2 * SLOT);
+                const int key0 = q.lo + j * BK;
+                if (slot == KD) {                                    // 128 keys, this CTA's 128 columns
+                    for (int c = 0; c < 2; ++c)
+                        tma_load_3d_pair(sb + OFF_SLOT + slot * SLOT + c * 16384, m, (int)rank * 128 + c * 64, key0, q.b, full(slot) + lead);
+                } else {                                             // this CTA's 64 keys, all columns
+                    for (int c = 0; c < 4; ++c)
+                        tma_load_3d_pair(sb + OFF_SLOT + slot * SLOT + c * 8192, m, c * 64, key0 + (int)rank * 64, q.b, full(slot) + lead);
+                }
                 return true;
             };
-            auto load_rows = [&](const CUtensorMap* m, uint32_t off, uint32_t bar, uint32_t freed) {
-                if (k > 0 && !wait(freed, (k - 1) & 1, g, 2)) return false;
-                if (rank == 0) mbar_arrive_expect_tx(bar, 2 * 65536);
-                for (int c = 0; c < 4; ++c)
-                    tma_load_3d_pair(sb + off + c * 16384, m, c * 64, t.r0 + (int)rank * 128, t.b, bar + lead);
-                return true;
-            };
-            for (; ok && q_tile<BK>(a, pair, npairs, k, t); ++k) {
-                ok = load(&map_ks, 0, 4) && load_rows(&map_q, OFF_Q, q_full, q_empty) && load(&map_vs, 0, 4) &&
-                     load_rows(&map_do, OFF_DO, do_full, do_empty);
-                for (int j = 1; ok && j <= t.n; ++j) {
-                    if (j < t.n) ok = load(&map_ks, j, 4) && load(&map_vs, j, 4);
-                    ok = ok && load(&map_kd, j - 1, 2);
+            // the order of the MMAs: K and V of the first tile, then K by keys, K by columns of the tile before, V
+            QTiles<BK> qs(a, pair, npairs), qd = qs;
+            int js = 0, jd = 0;
+            uint32_t i = 0;
+            bool more = qs.advance(a);
+            qd.advance(a);
+            while (ok && (more || i > 0)) {
+                if (more) ok = load(KS, &map_ks, qs.t, js, i);
+                if (ok && i > 0) {
+                    ok = load(KD, &map_kd, qd.t, jd, i - 1);
+                    if (++jd == qd.n) {
+                        jd = 0;
+                        qd.advance(a);
+                    }
+                }
+                if (!more) break;
+                ok = ok && load(VS, &map_vs, qs.t, js, i);
+                ++i;
+                if (++js == qs.n) {
+                    js = 0;
+                    more = qs.advance(a);
                 }
             }
             // no bulk copy may still be writing shared memory at the exit: the leader sees both CTAs' land
             if (rank == 0) {
                 const uint64_t t0 = globaltimer_ns();
-                for (uint32_t l = L > NSLOT ? L - NSLOT : 0; l < L; ++l)
-                    while (!mbar_try_wait_cluster(full(l % NSLOT), (l / NSLOT) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
-                    }
-                if (k > 0)
-                    while (!(mbar_try_wait_cluster(q_full, (k - 1) & 1) && mbar_try_wait_cluster(do_full, (k - 1) & 1)) &&
-                           globaltimer_ns() - t0 < a.timeout_ns) {
+#pragma unroll
+                for (uint32_t s = 0; s < NSLOT; ++s)
+                    while (n_loads[s] && !mbar_try_wait_cluster(full(s), (n_loads[s] - 1) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
                     }
             }
+        }
+    } else if (warp == kWarpQ) {
+        // Q and dO: each as soon as the MMAs before are through with its buffer
+        if (lane == 0) {
+            const uint32_t lead = map_to_rank(bars, 0) - bars;
+            QTiles<BK> q(a, pair, npairs);
+            bool ok = true;
+            auto load_rows = [&](const CUtensorMap* m, uint32_t off, uint32_t bar, uint32_t freed) {
+                if (q.k > 0 && !wait(freed, (q.k - 1) & 1, g, 2)) return false;
+                if (rank == 0) mbar_arrive_expect_tx(bar, 2 * 65536);
+                for (int c = 0; c < 4; ++c)
+                    tma_load_3d_pair(sb + off + c * 16384, m, c * 64, q.t.r0 + (int)rank * 128, q.t.b, bar + lead);
+                return true;
+            };
+            while (ok && q.advance(a))
+                ok = load_rows(&map_q, OFF_Q, q_full, q_empty) && load_rows(&map_do, OFF_DO, do_full, do_empty);
+            const uint64_t t0 = globaltimer_ns();
+            if (rank == 0 && ok && q.k > 0)
+                while (!(mbar_try_wait_cluster(q_full, (q.k - 1) & 1) && mbar_try_wait_cluster(do_full, (q.k - 1) & 1)) &&
+                       globaltimer_ns() - t0 < a.timeout_ns) {
+                }
         }
     } else if (warp == kWarpMma) {
         if (rank == 0) {
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t id_s = idesc_bf16(256, BK, 0), id_q = idesc_bf16(256, D, 1);
-            uint32_t L = 0, gt = 0;
-            bool ok = true;
-            auto ready = [&](uint32_t& s) {                          // the next slot's data
-                s = L % NSLOT;
-                const uint32_t u = L / NSLOT;
-                ++L;
-                return wait_w(full(s), u & 1, g, 3);
-            };
-            // 256 rows (at off_a) times the 64 keys of the next slot
-            auto issue = [&](uint32_t off_a, uint32_t d, uint32_t done, uint32_t rows_free, bool last) {
-                uint32_t s;
-                if (!ready(s)) return false;
+            QTiles<BK> qs(a, pair, npairs), qd = qs;                 // S and dP run one key tile ahead of dQ, across query tiles
+            int js = 0;
+            uint32_t i = 0;                                          // the key tile whose dQ is next
+            bool more = qs.advance(a), ok = true;
+            // 256 rows (at off_a) times the 128 keys in a slot; n: the key tile's number
+            auto issue = [&](uint32_t off_a, uint32_t d, uint32_t slot, uint32_t n, uint32_t done, uint32_t rows_free) {
+                if (!wait_w(full(slot), n & 1, g, 4)) return false;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
                         mma_ss_pair(tm + d, desc_k_sw128(sb + off_a + (ks >> 2) * 16384 + (ks & 3) * 32),
-                                    desc_k_sw128(sb + OFF_SLOT + s * SLOT + (ks >> 2) * 4096 + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
+                                    desc_k_sw128(sb + OFF_SLOT + slot * SLOT + (ks >> 2) * 8192 + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
                     mma_commit_pair(done);
-                    mma_commit_pair(empty(s));
-                    if (last) mma_commit_pair(rows_free);
+                    mma_commit_pair(empty(slot));
+                    if (js + 1 == qs.n) mma_commit_pair(rows_free);
                 }
                 __syncwarp();
                 return true;
             };
-            auto issue_s = [&](int j) {
-                const uint32_t buf = (gt + j) & 1;
-                return issue(OFF_Q, TM_S + buf * BK, s_full(buf), q_empty, j == t.n - 1);
+            auto issue_s = [&](uint32_t n) {
+                if (js == 0 && !wait_w(q_full, qs.k & 1, g, 3)) return false;
+                return issue(OFF_Q, TM_S, KS, n, s_full, q_empty);
             };
-            auto issue_dp = [&](int j) {
-                const uint32_t buf = (gt + j) & 1;
-                return issue(OFF_DO, TM_DP + buf * BK, dp_full(buf), do_empty, j == t.n - 1);
+            auto issue_dp = [&](uint32_t n) {
+                if (js == 0 && !wait_w(do_full, qs.k & 1, g, 5)) return false;
+                if (!issue(OFF_DO, TM_DP, VS, n, dp_full, do_empty)) return false;
+                if (++js == qs.n) {
+                    js = 0;
+                    more = qs.advance(a);
+                }
+                return true;
             };
-            for (int k = 0; ok && q_tile<BK>(a, pair, npairs, k, t); ++k) {
-                if (!(ok = wait_w(q_full, k & 1, g, 4) && issue_s(0))) break;
-                if (!(ok = wait_w(do_full, k & 1, g, 5) && issue_dp(0))) break;
-                for (int j = 0; ok && j < t.n; ++j) {
-                    const uint32_t i = gt + j, buf = i & 1;
-                    if (j + 1 < t.n && !(ok = issue_s(j + 1) && issue_dp(j + 1))) break;
-                    if (!(ok = wait_w(ds_full(buf), (i >> 1) & 1, g, 7))) break;
-                    if (j == 0 && k > 0 && !(ok = wait_w(dq_free, (k - 1) & 1, g, 8))) break;
-                    uint32_t s;
-                    if (!(ok = ready(s))) break;
+            if (more) ok = issue_s(0) && issue_dp(0);
+            while (ok && qd.advance(a))
+                for (int j = 0; j < qd.n; ++j, ++i) {
+                    const bool next = more;
+                    if (next && !(ok = wait_w(s_free, i & 1, g, 9) && issue_s(i + 1))) break;
+                    if (j == 0 && qd.k > 0 && !(ok = wait_w(dq_free, (qd.k - 1) & 1, g, 8))) break;
+                    if (!(ok = wait_w(full(KD), i & 1, g, 7) && wait_w(ds_full, i & 1, g, 6))) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        // dS of keys [16 ks, 16 ks + 16): the two halves of a row sit 32 columns apart
+                        // dS of keys [16 ks, 16 ks + 16): the two halves of a row sit 64 columns apart
 #pragma unroll
                         for (int ks = 0; ks < BK / 16; ++ks)
-                            mma_ts_pair(tm + TM_DQ, tm + TM_DP + buf * BK + (ks >> 1) * 32 + (ks & 1) * 8,
-                                        desc_mn_sw128(sb + OFF_SLOT + s * SLOT + ks * 2048, 8192), id_q,
+                            mma_ts_pair(tm + TM_DQ, tm + TM_DP + (ks >> 2) * 64 + (ks & 3) * 8,
+                                        desc_mn_sw128(sb + OFF_SLOT + KD * SLOT + ks * 2048, 16384), id_q,
                                         (j > 0 || ks > 0) ? 1u : 0u);
-                        mma_commit_pair(empty(s));
-                        if (j == t.n - 1) mma_commit_pair(dq_done);
+                        mma_commit_pair(empty(KD));
+                        if (j == qd.n - 1) mma_commit_pair(dq_done);
                     }
                     __syncwarp();
+                    if (next && !(ok = issue_dp(i + 1))) break;
                 }
-                gt += t.n;
-            }
             if (elect_one()) mma_commit_pair(mma_done);
             __syncwarp();
         }
@@ -653,58 +745,21 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t lead = map_to_rank(bars, 0) - bars;
         uint32_t gt = 0;
-        for (int k = 0; q_tile<BK>(a, pair, npairs, k, t); ++k) {
-            const int row0 = t.r0 + (int)rank * 128, row = row0 + r;
-            const bool live = row < a.TH;
-            const int tok = min(row, a.TH - 1) / a.H;
-            const int lo_row = live ? a.lo[(size_t)t.b * a.T + tok] : 0x7fffffff;   // a row past the end sees no key
-            const int full_lo = row0 + 127 < a.TH ? a.lo[(size_t)t.b * a.T + (row0 + 127) / a.H] : 0x7fffffff;
-            const int full_hi = min(row0, a.TH - 1) / a.H;
-            const float lse = live ? a.lse[(size_t)t.b * a.THp + row] : 0.f;
-            const float delta = live ? a.delta[(size_t)t.b * a.THp + row] : 0.f;
-            bool ok = true;
-            for (int j = 0; j < t.n; ++j) {
-                const uint32_t i = gt + j, buf = i & 1, par = (i >> 1) & 1;
-                if (!(ok = wait_w(s_full(buf), par, g, 10))) break;
-                tc_fence_after();
-                float s[32], dp[32];
-                tmem_ld32(tl + TM_S + buf * BK + half * 32, s);
-                tmem_wait_ld();
-                const int key0 = t.lo + j * BK;
-                const bool whole = key0 >= full_lo && key0 + BK - 1 <= full_hi;
-                const int c_lo = lo_row - (key0 + half * 32), c_hi = tok - (key0 + half * 32);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    s[c] = ex2_approx(fmaf(s[c], a.scale_log2, -lse));
-                    if (!whole) s[c] = (c >= c_lo && c <= c_hi) ? s[c] : 0.f;
-                }
-                if (!(ok = wait_w(dp_full(buf), par, g, 11))) break;
-                tc_fence_after();
-                tmem_ld32(tl + TM_DP + buf * BK + half * 32, dp);
-                tmem_wait_ld();
-                uint32_t v[16];
-#pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    v[c] = bf16x2(s[2 * c] * (dp[2 * c] - delta), s[2 * c + 1] * (dp[2 * c + 1] - delta));
-                tmem_st16(tl + TM_DP + buf * BK + half * 32, v);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(ds_full(buf) + lead);
-            }
-            if (!ok || !wait_w(dq_done, k & 1, g, 12)) break;
-            gt += t.n;
+        // dq of query tile k - 1, after the first dS of tile k
+        int p_b = 0, p_row = 0;
+        auto finish = [&](int kp) {
+            if (!wait_w(dq_done, kp & 1, g, 12)) return false;
             tc_fence_after();
             // turn back: columns [64 half, +64) and their partners 128 further
-            __nv_bfloat16* orow = a.dq + ((size_t)t.b * a.TH + row) * D + half * 64;
-            const float4* cs = reinterpret_cast<const float4*>(a.cs + (size_t)tok * (D / 2) + half * 64);
+            __nv_bfloat16* orow = a.dq + ((size_t)p_b * a.TH + p_row) * D + half * 64;
+            const float4* cs = reinterpret_cast<const float4*>(a.cs + (size_t)(min(p_row, a.TH - 1) / a.H) * (D / 2) + half * 64);
 #pragma unroll 1
             for (int c = 0; c < 64; c += 16) {
                 float x1[16], x2[16];
                 tmem_ld16(tl + TM_DQ + half * 64 + c, x1);
                 tmem_ld16(tl + TM_DQ + 128 + half * 64 + c, x2);
                 tmem_wait_ld();
-                if (live) {
+                if (p_row < a.TH) {
                     uint32_t o1[8], o2[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -723,7 +778,64 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_pair(dq_free + lead);
+            return true;
+        };
+        bool ok = true;
+        QTiles<BK> q(a, pair, npairs);
+        while (ok && q.advance(a)) {
+            const QTile t = q.t;
+            const int row0 = t.r0 + (int)rank * 128, row = row0 + r;
+            const bool live = row < a.TH;
+            const int tok = min(row, a.TH - 1) / a.H;
+            const int lo_row = live ? a.lo[(size_t)t.b * a.T + tok] : 0x7fffffff;   // a row past the end sees no key
+            const int full_lo = row0 + 127 < a.TH ? a.lo[(size_t)t.b * a.T + (row0 + 127) / a.H] : 0x7fffffff;
+            const int full_hi = min(row0, a.TH - 1) / a.H;
+            const float lse = live ? a.lse[(size_t)t.b * a.THp + row] : 0.f;
+            const float delta = live ? a.delta[(size_t)t.b * a.THp + row] : 0.f;
+            for (int j = 0; j < q.n; ++j) {
+                const uint32_t par = (gt + j) & 1;
+                if (!(ok = wait_w(s_full, par, g, 10))) break;
+                tc_fence_after();
+                float s[64];
+                tmem_ld32(tl + TM_S + half * 64, s);
+                tmem_ld32(tl + TM_S + half * 64 + 32, s + 32);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(s_free + lead);
+                const int key0 = t.lo + j * BK;
+                const bool whole = key0 >= full_lo && key0 + BK - 1 <= full_hi;
+#pragma unroll
+                for (int c = 0; c < 64; ++c) s[c] = ex2_approx(fmaf(s[c], a.scale_log2, -lse));
+                if (!whole) {
+                    const int c_lo = lo_row - (key0 + half * 64), c_hi = tok - (key0 + half * 64);
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) s[c] = (c >= c_lo && c <= c_hi) ? s[c] : 0.f;
+                }
+                if (!(ok = wait_w(dp_full, par, g, 11))) break;
+                tc_fence_after();
+                float dp[32];
+                uint32_t v[32];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    tmem_ld32(tl + TM_DP + half * 64 + 32 * e, dp);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        v[16 * e + c] = bf16x2(s[32 * e + 2 * c] * (dp[2 * c] - delta), s[32 * e + 2 * c + 1] * (dp[2 * c + 1] - delta));
+                }
+                tmem_st32(tl + TM_DP + half * 64, v);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(ds_full + lead);
+                if (j == 0 && q.k > 0 && !(ok = finish(q.k - 1))) break;
+            }
+            p_b = t.b;
+            p_row = row;
+            gt += q.n;
         }
+        if (ok && q.k > 0) finish(q.k - 1);
         tmem_wait_ld();
         tmem_wait_st();
     }
@@ -908,6 +1020,7 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const uint32_t id_s = idesc_bf16(128, BR, 0), id_a = idesc_bf16(128, D, 1);
         uint32_t L = 0, gi = 0, ns = 0;
         bool ok = true;
+        auto wait_slot = [&](uint32_t l) { return wait_w(full(l % NSLOT), (l / NSLOT) & 1, g, 3); };
         for (; ok && segs.next(a, sg); ++ns) {
             if (!(ok = wait_w(a_tmem, ns & 1, g, 2))) break;
             tc_fence_after();
@@ -917,38 +1030,43 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             }
             __syncwarp();
             L += 2;
-            for (int j = 0; ok && j <= sg.n; ++j) {
-                if (j < sg.n) {
-                    const uint32_t s = L % NSLOT, buf = (gi + j) & 1;
-                    if (!(ok = wait_w(full(s), (L / NSLOT) & 1, g, 3))) break;
-                    ++L;
-                    tc_fence_after();
-                    if (elect_one()) {
+            auto issue_s = [&](int j) {                              // S^T_j from the next slot
+                const uint32_t s = L % NSLOT, buf = (gi + j) & 1;
+                ++L;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            mma_ts(tm + TM_S + buf * BR, tm + TM_A + ks * 8,
-                                   desc_k_sw128(sb + s * SLOT + (ks >> 2) * 8192 + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
-                        mma_commit(s_full(buf));
-                        mma_commit(empty(s));
-                    }
-                    __syncwarp();
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_ts(tm + TM_S + buf * BR, tm + TM_A + ks * 8,
+                               desc_k_sw128(sb + s * SLOT + (ks >> 2) * 8192 + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
+                    mma_commit(s_full(buf));
+                    mma_commit(empty(s));
                 }
-                if (j >= 1) {
-                    const uint32_t s = L % NSLOT, i = gi + j - 1, buf = i & 1;
-                    if (!(ok = wait_w(full(s), (L / NSLOT) & 1, g, 12))) break;
-                    if (!(ok = wait_w(p_full(buf), (i >> 1) & 1, g, 4))) break;
-                    ++L;
-                    tc_fence_after();
-                    if (elect_one()) {
+                __syncwarp();
+            };
+            for (int j = 0; ok && j < min(2, sg.n); ++j)
+                if ((ok = wait_slot(L))) issue_s(j);
+            if (!ok || !(ok = wait_slot(L))) break;                  // Y_0
+            // The queue of the tensor pipe is two MMAs deep: what is waited for behind the second product's MMAs costs
+            // nothing, so the next operands are; only the wait for the next P^T is not covered
+            for (int j = 0; j < sg.n; ++j) {
+                const uint32_t i = gi + j, buf = i & 1, s = L % NSLOT;
+                if (!(ok = wait_w(p_full(buf), (i >> 1) & 1, g, 4))) break;
+                ++L;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                        for (int ks = 0; ks < BR / 16; ++ks)
-                            mma_ts(tm + TM_ACC, tm + TM_S + buf * BR + ks * 8, desc_mn_sw128(sb + s * SLOT + ks * 2048, 8192), id_a,
-                                   (j > 1 || ks > 0) ? 1u : 0u);
-                        mma_commit(empty(s));
-                        if (j == sg.n) mma_commit(acc_done);
-                    }
-                    __syncwarp();
+                    for (int ks = 0; ks < BR / 16; ++ks)
+                        mma_ts(tm + TM_ACC, tm + TM_S + buf * BR + ks * 8,
+                               desc_mn_sw128(sb + s * SLOT + ks * 2048, 8192), id_a, (j > 0 || ks > 0) ? 1u : 0u);
+                    mma_commit(empty(s));
+                    if (j == sg.n - 1) mma_commit(acc_done);
                 }
+                __syncwarp();
+                const bool more = j + 2 < sg.n;                      // X_{j+2}, then Y_{j+1}
+                if (more && !(ok = wait_slot(L))) break;
+                if (j + 1 < sg.n && !(ok = wait_slot(more ? L + 1 : L))) break;
+                if (more) issue_s(j + 2);
             }
             gi += sg.n;
         }
@@ -1348,17 +1466,17 @@ cudaError_t launch_mqa_backward(const rglru_mqa_dims* d, const void* v, const vo
     a.dk = static_cast<__nv_bfloat16*>(dk);
     a.dv = static_cast<__nv_bfloat16*>(dv);
     const int* last = reinterpret_cast<const int*>(p + l.last);
-    CUtensorMap q128, do128, k32, v32, k64, q64, do64, k128, v128;
+    CUtensorMap q128, do128, q64, do64, k64, v64, k128, v128;
     if (!map_rows(&q128, p + l.q_rot, a.TH, B, 128) || !map_rows(&do128, dout, a.TH, B, 128) ||
-        !map_rows(&k32, p + l.k_rot, T, B, 32) || !map_rows(&v32, v, T, B, 32) || !map_rows(&k64, p + l.k_rot, T, B, 64) ||
         !map_rows(&q64, p + l.q_rot, a.TH, B, 64) || !map_rows(&do64, dout, a.TH, B, 64) ||
+        !map_rows(&k64, p + l.k_rot, T, B, 64) || !map_rows(&v64, v, T, B, 64) ||
         !map_rows(&k128, p + l.k_rot, T, B, 128) || !map_rows(&v128, v, T, B, 128))
         return cudaErrorInvalidValue;
     const long long rows = (long long)B * a.TH;
     mqa_delta_kernel<<<(unsigned)((rows + 31) / 32 + 1), 1024, 0, s>>>(a, static_cast<const __nv_bfloat16*>(dout), last,
                                                                        const_cast<long long*>(a.cum));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_pairs(mqa_dq_kernel, std::min(pq, B * a.ntr), bq::kThreads, bq::SMEM_BYTES, s, q128, do128, k32, v32, k64, a);
+    e = launch_pairs(mqa_dq_kernel, std::min(pq, B * a.ntr), bq::kThreads, bq::SMEM_BYTES, s, q128, do128, k64, v64, k128, a);
     if (e != cudaSuccess) return e;
     e = launch_pairs(mqa_dkv_kernel, pk, bk::kThreads, bk::SMEM_BYTES, s, q64, do64, k128, v128, last, a);
     if (e != cudaSuccess) return e;
