@@ -16,6 +16,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "angles.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "pair.cuh"
@@ -56,25 +57,6 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t c) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
     return __half22float2(*reinterpret_cast<__half2*>(&h));
-}
-
-// ---- angles ------------------------------------------------------------------------------------------
-// base^(-2j/d) = 2^(-j log2(base) / 128) with log2(base) in two parts, the first short enough that
-// its product with j is exact: within 2 units of the last place of the power itself, at a fifth of
-// the fp64 operations of pow.
-struct Base {
-    double hi, lo;                     // log2(base)
-};
-__device__ __forceinline__ void cos_sin(Base base, int j, double p, double& c, double& s) {
-    const double x = exp2(base.hi * (-j / 128.0));
-    sincos(p * fma(x, base.lo * (-j / 128.0) * 0.69314718055994530942, x), &s, &c);
-}
-inline Base log2_base(float base) {
-    const long double l = log2l((long double)base);
-    Base b;
-    b.hi = (double)(float)l;           // 24 bits
-    b.lo = (double)(l - (long double)b.hi);
-    return b;
 }
 
 // ---- one slot by one warp ------------------------------------------------------------------------------
@@ -122,7 +104,7 @@ __device__ __forceinline__ void widen(const float (&x)[8], double (&y)[8]) {
 // are most of the arithmetic), then a warp per key or value.  The last min(len, w) tokens of a row
 // go into their slots.
 constexpr int kWriteRows = 8;
-__global__ void __launch_bounds__(128) mqa_cache8_write_kernel(int B, int T, int w, int pos0, Base base, const int* lengths,
+__global__ void __launch_bounds__(128) mqa_cache8_write_kernel(int B, int T, int w, int pos0, RopeBase base, const int* lengths,
                                                                const __nv_bfloat16* k, const __nv_bfloat16* v,
                                                                uint8_t* codes, float* scales) {
     __shared__ double2 cs[D / 2];
@@ -136,7 +118,7 @@ __global__ void __launch_bounds__(128) mqa_cache8_write_kernel(int B, int T, int
     }
     if (!any) return;
     const long long p = (long long)pos0 + t;
-    cos_sin(base, threadIdx.x, (double)p, cs[threadIdx.x].x, cs[threadIdx.x].y);
+    rope_cos_sin(base, threadIdx.x, (double)p, cs[threadIdx.x].x, cs[threadIdx.x].y);
     __syncthreads();
     const int slot = (int)(p % w);
     for (int i = warp; i < 2 * nb; i += 4) {
@@ -180,7 +162,7 @@ __global__ void __launch_bounds__(256) mqa_cache8_read_kernel(long long slots, i
 // x1 = e4m3(16 (q~ 2^-e - x0)), ...: a part is off by at most 2^-4 of itself, so |r| <= 2^-12 |q~| (or
 // 2^-18 448 2^e where x2 is below e4m3's normal numbers), less than bf16 would leave.
 constexpr int kQParts = 3, kQRows = kQParts * kMaxH;
-__global__ void __launch_bounds__(256) mqa_decode8_turn_kernel(int H, int w, Base base, const int* pos,
+__global__ void __launch_bounds__(256) mqa_decode8_turn_kernel(int H, int w, RopeBase base, const int* pos,
                                                                const __nv_bfloat16* q, const __nv_bfloat16* k,
                                                                const __nv_bfloat16* v, uint8_t* qp, float* qs,
                                                                unsigned* done, uint8_t* codes, float* scales,
@@ -196,7 +178,7 @@ __global__ void __launch_bounds__(256) mqa_decode8_turn_kernel(int H, int w, Bas
         return;
     }
     float x[8];
-    if (threadIdx.x < D / 2) cos_sin(base, threadIdx.x, (double)p, cs[threadIdx.x].x, cs[threadIdx.x].y);
+    if (threadIdx.x < D / 2) rope_cos_sin(base, threadIdx.x, (double)p, cs[threadIdx.x].x, cs[threadIdx.x].y);
     __syncthreads();
     const int slot = p % w;
     for (int i = warp; i < H + 2; i += 8) {
@@ -322,8 +304,8 @@ struct DecSeg {
 };
 __device__ __forceinline__ int owner(long long x, long long total, int G) {
     int c = (int)(x * G / total);
-    while (total * (c + 1) / G <= x) ++c;
-    while (total * c / G > x) --c;
+    while (c + 1 < G && total * (c + 1) / G <= x) ++c;
+    while (c > 0 && total * c / G > x) --c;
     return c;
 }
 __device__ __forceinline__ bool next_seg(const DecArgs& a, Walk& k, DecSeg& s) {
@@ -334,7 +316,7 @@ __device__ __forceinline__ bool next_seg(const DecArgs& a, Walk& k, DecSeg& s) {
         tiles = (n + kTile - 1) / kTile;
         if (k.pos < k.row_beg + tiles) break;
         k.row_beg += tiles;
-        ++k.row;
+        if (++k.row >= a.B) return false;
     }
     s.b = k.row;
     s.n = n;
@@ -838,7 +820,7 @@ cudaError_t launch_mqa_cache8_write(const rglru_mqa_dims* d, const void* k, cons
     // without lengths only the last min(T, w) tokens are written; with them any token may be
     const int tokens = lengths ? d->seq_len : std::min(d->seq_len, d->window);
     mqa_cache8_write_kernel<<<dim3(tokens, (d->batch + kWriteRows - 1) / kWriteRows), 128, 0, s>>>(
-        d->batch, d->seq_len, d->window, pos0, log2_base(d->rope_base), lengths, static_cast<const __nv_bfloat16*>(k),
+        d->batch, d->seq_len, d->window, pos0, rope_base(d->rope_base), lengths, static_cast<const __nv_bfloat16*>(k),
         static_cast<const __nv_bfloat16*>(v), static_cast<uint8_t*>(codes), scales);
     return cudaGetLastError();
 }
@@ -871,7 +853,7 @@ cudaError_t launch_mqa_decode8(const rglru_mqa_dims* d, const void* q, const voi
     a.status = static_cast<DeviceStatus*>(ws);
     a.timeout_ns = 1000000000ull;
     mqa_decode8_turn_kernel<<<B, 256, 0, s>>>(
-        d->q_heads, w, log2_base(d->rope_base), pos, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+        d->q_heads, w, rope_base(d->rope_base), pos, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
         static_cast<const __nv_bfloat16*>(v), p + l.qp, reinterpret_cast<float*>(p + l.qs), a.done, static_cast<uint8_t*>(codes),
         scales, a.out);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -20,6 +20,7 @@
 
 #include <mutex>
 
+#include "angles.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "pair.cuh"
@@ -35,96 +36,134 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxClusters = 74;       // 2-CTA clusters of 148 SMs
 
 // ---------------------------------------------------------------- rotary embedding, documents ----
-// cosine and sine of position pos0 + t, pair j, angle and reduction in fp64: [T][d/2]
-__global__ void __launch_bounds__(D / 2) mqa_angles_kernel(int pos0, float base, float2* cs) {
-    const int j = threadIdx.x, t = blockIdx.x;
-    const double ang = ((double)pos0 + t) * pow((double)base, -2.0 * j / D);
-    double s, c;
-    sincos(ang, &s, &c);
-    cs[(size_t)t * (D / 2) + j] = make_float2((float)c, (float)s);
+constexpr int kScanThreads = 1024, kScanPer = 8, kScanChunk = kScanThreads * kScanPer;
+
+// The maximum (or minimum) of v over the threads of the block before this one, start for the first, and over all.
+template <bool kMax>
+__device__ __forceinline__ int better(int a, int b) {
+    return kMax ? max(a, b) : min(a, b);
+}
+template <bool kMax>
+__device__ __forceinline__ int scan_before(int v, int start, int* warp_v, int& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = better<kMax>(v, u);
+    }
+    if (lane == 31) warp_v[warp] = v;
+    __syncthreads();
+    int w = warp_v[lane];                                // kScanThreads / 32 = 32 warps
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w = better<kMax>(w, u);
+    }
+    all = __shfl_sync(0xffffffffu, w, 31);
+    const int warps_before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    int before = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) before = start;
+    if (warp > 0) before = better<kMax>(before, warps_before);
+    __syncthreads();
+    return before;
 }
 
-// Per row: the first key of every token, lo = max(0, t - w + 1, start of its document), and the last
-// token that sees it, last = min(T - 1, t + w - 1, end of its document): a running maximum forwards and a
-// running minimum backwards over the tokens that start a document.
-constexpr int kScanThreads = 1024, kScanPer = 8, kScanChunk = kScanThreads * kScanPer;
-__global__ void __launch_bounds__(kScanThreads) mqa_documents_kernel(int T, int w, const uint8_t* reset, int* lo, int* last) {
+// Blocks [0, B): a row's first key of every token, lo = max(0, t - w + 1, start of its document), and the last token
+// that sees it, last = min(T - 1, t + w - 1, end of its document): a running maximum forwards and a running
+// minimum backwards over the tokens that start a document.  The other blocks: cosine and sine of position
+// pos0 + t, pair j, [T][d/2], angle and reduction in fp64.
+__global__ void __launch_bounds__(kScanThreads) mqa_prepare_kernel(int B, int T, int w, const uint8_t* reset, int* lo, int* last,
+                                                                   int pos0, RopeBase base, float2* cs) {
+    if (blockIdx.x >= (unsigned)B) {
+        const int t = (blockIdx.x - B) * (kScanThreads / (D / 2)) + threadIdx.x / (D / 2), j = threadIdx.x % (D / 2);
+        if (t >= T) return;
+        double s, c;
+        rope_cos_sin(base, j, (double)pos0 + t, c, s);
+        cs[(size_t)t * (D / 2) + j] = make_float2((float)c, (float)s);
+        return;
+    }
     __shared__ int warp_v[32];
-    const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b = blockIdx.x;
     const uint8_t* rs = reset ? reset + (size_t)b * T : nullptr;
     lo += (size_t)b * T;
     last += (size_t)b * T;
     const int chunks = (T + kScanChunk - 1) / kScanChunk;
-    int carry = 0;
+    int carry = 0, all;
     for (int c = 0; c < chunks; ++c) {
         const int t0 = c * kScanChunk + threadIdx.x * kScanPer;
         int v[kScanPer], run = 0;
 #pragma unroll
-        for (int e = 0; e < kScanPer; ++e) v[e] = t0 + e < T && rs && rs[t0 + e] ? t0 + e : 0;
-#pragma unroll
-        for (int e = 0; e < kScanPer; ++e) v[e] = run = max(run, v[e]);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run = max(run, u);
+        for (int e = 0; e < kScanPer; ++e) {
+            v[e] = t0 + e < T && rs && rs[t0 + e] ? t0 + e : 0;
+            run = max(run, v[e]);
         }
-        if (lane == 31) warp_v[warp] = run;
-        int before = __shfl_up_sync(0xffffffffu, run, 1);
-        if (lane == 0) before = 0;
-        __syncthreads();
-        int base = max(before, carry);
-        for (int i = 0; i < 32; ++i) {
-            if (i < warp) base = max(base, warp_v[i]);
-            carry = max(carry, warp_v[i]);
-        }
+        run = max(carry, scan_before<true>(run, 0, warp_v, all));
 #pragma unroll
-        for (int e = 0; e < kScanPer; ++e)
-            if (t0 + e < T) lo[t0 + e] = max(max(base, v[e]), t0 + e - w + 1);
-        __syncthreads();
+        for (int e = 0; e < kScanPer; ++e) {
+            run = max(run, v[e]);
+            if (t0 + e < T) lo[t0 + e] = max(run, t0 + e - w + 1);
+        }
+        carry = max(carry, all);
     }
     carry = T;                          // the first document start after the tokens seen so far, going back
     for (int c = chunks - 1; c >= 0; --c) {
-        const int t0 = c * kScanChunk + threadIdx.x * kScanPer;
-        int v[kScanPer], run = T;       // v[e]: the first start after t0 + e, inside this thread's tokens
+        // thread 0 has the chunk's last tokens
+        const int t1 = c * kScanChunk + (kScanThreads - (int)threadIdx.x) * kScanPer - 1;
+        int v[kScanPer], run = T;
 #pragma unroll
-        for (int e = kScanPer - 1; e >= 0; --e) {
-            v[e] = run;
-            if (t0 + e < T && rs && rs[t0 + e]) run = t0 + e;
+        for (int e = 0; e < kScanPer; ++e) {
+            v[e] = t1 - e < T && rs && rs[t1 - e] ? t1 - e : T;
+            run = min(run, v[e]);
         }
+        run = min(carry, scan_before<false>(run, T, warp_v, all));
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_down_sync(0xffffffffu, run, o);
-            if (lane + o < 32) run = min(run, u);
+        for (int e = 0; e < kScanPer; ++e) {
+            const int t = t1 - e;
+            if (t < T) last[t] = w - 1 < run - 1 - t ? t + w - 1 : run - 1;
+            run = min(run, v[e]);
         }
-        if (lane == 0) warp_v[warp] = run;
-        int after = __shfl_down_sync(0xffffffffu, run, 1);
-        if (lane == 31) after = T;
-        __syncthreads();
-        int base = min(after, carry);
-        for (int i = 0; i < 32; ++i) {
-            if (i > warp) base = min(base, warp_v[i]);
-            carry = min(carry, warp_v[i]);
-        }
-#pragma unroll
-        for (int e = 0; e < kScanPer; ++e)
-            if (t0 + e < T) last[t0 + e] = (int)min((long long)min(min(base, v[e]), T) - 1, (long long)t0 + e + w - 1);
-        __syncthreads();
+        carry = min(carry, all);
     }
 }
 
-// thread = (row b, token t, pair j) over the H query heads and the key
-__global__ void __launch_bounds__(D / 2) mqa_turn_kernel(int T, int H, const float2* cs, const __nv_bfloat16* q,
-                                                         const __nv_bfloat16* k, __nv_bfloat16* q_rot,
-                                                         __nv_bfloat16* k_rot) {
-    const int j = threadIdx.x, t = blockIdx.x, b = blockIdx.y;
-    const float2 a = cs[(size_t)t * (D / 2) + j];
-    const size_t tok = (size_t)b * T + t;
-    for (int h = 0; h <= H; ++h) {
-        const __nv_bfloat16* src = h < H ? q + (tok * H + h) * D : k + tok * D;
-        __nv_bfloat16* dst = h < H ? q_rot + (tok * H + h) * D : k_rot + tok * D;
-        const float x1 = __bfloat162float(src[j]), x2 = __bfloat162float(src[j + D / 2]);
-        dst[j] = __float2bfloat16_rn(x1 * a.x - x2 * a.y);
-        dst[j + D / 2] = __float2bfloat16_rn(x2 * a.x + x1 * a.y);
+// 16 threads a token, 8 pairs each, over its H query heads and its key: bound by HBM (q and k in and out), so
+// the rows of a few heads are in flight together
+constexpr int kTurnRows = 4;
+__global__ void __launch_bounds__(256) mqa_turn_kernel(long long tokens, int T, int H, const float2* cs, const __nv_bfloat16* q,
+                                                       const __nv_bfloat16* k, __nv_bfloat16* q_rot, __nv_bfloat16* k_rot) {
+    const long long tok = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int c = threadIdx.x & 15;
+    if (tok >= tokens) return;
+    float4 a[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] = __ldg(reinterpret_cast<const float4*>(cs + (size_t)(tok % T) * (D / 2) + 8 * c) + e);
+    for (int h0 = 0; h0 <= H; h0 += kTurnRows) {
+        uint4 x[kTurnRows], y[kTurnRows];
+#pragma unroll
+        for (int i = 0; i < kTurnRows; ++i) {
+            const int h = h0 + i;
+            if (h > H) break;
+            const uint4* src = reinterpret_cast<const uint4*>(h < H ? q + (tok * H + h) * D : k + tok * D);
+            x[i] = __ldg(src + c);
+            y[i] = __ldg(src + 16 + c);
+        }
+#pragma unroll
+        for (int i = 0; i < kTurnRows; ++i) {
+            const int h = h0 + i;
+            if (h > H) break;
+            const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, ys[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+            uint32_t o1[4], o2[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x0 = __uint_as_float(xs[e] << 16), x1 = __uint_as_float(xs[e] & 0xffff0000u);
+                const float y0 = __uint_as_float(ys[e] << 16), y1 = __uint_as_float(ys[e] & 0xffff0000u);
+                o1[e] = bf16x2(x0 * a[e].x - y0 * a[e].y, x1 * a[e].z - y1 * a[e].w);
+                o2[e] = bf16x2(y0 * a[e].x + x0 * a[e].y, y1 * a[e].z + x1 * a[e].w);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(h < H ? q_rot + (tok * H + h) * D : k_rot + tok * D);
+            dst[c] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+            dst[16 + c] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+        }
     }
 }
 
@@ -320,17 +359,14 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         if (rank == 0) {
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t id_s = idesc_bf16(256, BK, 0), id_o = idesc_bf16(256, D, 1);
-            // S runs two key tiles ahead of P V, across query tiles.  The queue of the tensor pipe is two MMAs deep: what
-            // is waited for right behind the P V MMAs costs nothing, so the next S's operands and the next V
-            // are; only the wait for the next P is not covered
+            // S runs two key tiles ahead of P V, across query tiles
             QTiles<BK> qs(a, pair, npairs), qp = qs;
             int js = 0;
             uint32_t L = 0, gt = 0, gs = 0;                          // slots used; key tiles done, key tiles with S issued
             bool more = qs.advance(a), ok = true;
             auto wait_slot = [&](uint32_t l) { return wait_w(full(l % NSLOT), (l / NSLOT) & 1, g, 4); };
-            auto issue_s = [&]() {                                   // S of the next key tile, from the next slot
+            auto issue_s = [&]() {                                   // S of the next key tile, from the next slot (which is there)
                 if (js == 0 && !wait_w(q_full, qs.k & 1, g, 3)) return false;
-                if (!wait_slot(L)) return false;
                 tc_fence_after();
                 const uint32_t s = L % NSLOT, buf = gs & 1;
                 ++L;
@@ -353,13 +389,12 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 }
                 return true;
             };
-            for (int i = 0; ok && more && i < 2; ++i) ok = issue_s();
+            for (int i = 0; ok && more && i < 2; ++i) ok = wait_slot(L) && issue_s();
             while (ok && qp.advance(a))
                 for (int j = 0; j < qp.n; ++j, ++gt) {
-                    const uint32_t buf = gt & 1, s = L % NSLOT;
-                    if (gt == 0 && !(ok = wait_slot(L))) break;
+                    const uint32_t buf = gt & 1, s = L % NSLOT, lk = more ? L + 1 : L;   // the next K behind this V
                     if (j == 0 && qp.k > 0 && !(ok = wait_w(o_free, (qp.k - 1) & 1, g, 5))) break;
-                    if (!(ok = wait_w(p_full(buf), (gt >> 1) & 1, g, 6))) break;
+                    if (!(ok = wait_w(p_full(buf), (gt >> 1) & 1, full(s), (L / NSLOT) & 1, full(lk % NSLOT), (lk / NSLOT) & 1, g, 6))) break;
                     ++L;
                     tc_fence_after();
                     if (elect_one()) {                               // O += P_j V_j
@@ -373,8 +408,6 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         mma_commit_pair(empty(s));
                     }
                     __syncwarp();
-                    const bool next = j + 1 < qp.n || qp.has;        // another V follows, behind the next K if there is one
-                    if (next && !(ok = wait_slot(more ? L + 1 : L))) break;
                     if (more && !(ok = issue_s())) break;
                 }
             if (elect_one()) mma_commit_pair(mma_done);              // every MMA is over before TMEM is released
@@ -681,9 +714,8 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             int js = 0;
             uint32_t i = 0;                                          // the key tile whose dQ is next
             bool more = qs.advance(a), ok = true;
-            // 256 rows (at off_a) times the 128 keys in a slot; n: the key tile's number
-            auto issue = [&](uint32_t off_a, uint32_t d, uint32_t slot, uint32_t n, uint32_t done, uint32_t rows_free) {
-                if (!wait_w(full(slot), n & 1, g, 4)) return false;
+            // 256 rows (at off_a) times the 128 keys in a slot (which are there)
+            auto issue = [&](uint32_t off_a, uint32_t d, uint32_t slot, uint32_t done, uint32_t rows_free) {
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -695,28 +727,28 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     if (js + 1 == qs.n) mma_commit_pair(rows_free);
                 }
                 __syncwarp();
+            };
+            auto issue_s = [&]() {
+                if (js == 0 && !wait_w(q_full, qs.k & 1, g, 3)) return false;
+                issue(OFF_Q, TM_S, KS, s_full, q_empty);
                 return true;
             };
-            auto issue_s = [&](uint32_t n) {
-                if (js == 0 && !wait_w(q_full, qs.k & 1, g, 3)) return false;
-                return issue(OFF_Q, TM_S, KS, n, s_full, q_empty);
-            };
-            auto issue_dp = [&](uint32_t n) {
+            auto issue_dp = [&]() {
                 if (js == 0 && !wait_w(do_full, qs.k & 1, g, 5)) return false;
-                if (!issue(OFF_DO, TM_DP, VS, n, dp_full, do_empty)) return false;
+                issue(OFF_DO, TM_DP, VS, dp_full, do_empty);
                 if (++js == qs.n) {
                     js = 0;
                     more = qs.advance(a);
                 }
                 return true;
             };
-            if (more) ok = issue_s(0) && issue_dp(0);
+            if (more) ok = wait_w(full(KS), 0, full(VS), 0, g, 4) && issue_s() && issue_dp();
             while (ok && qd.advance(a))
                 for (int j = 0; j < qd.n; ++j, ++i) {
                     const bool next = more;
-                    if (next && !(ok = wait_w(s_free, i & 1, g, 9) && issue_s(i + 1))) break;
+                    if (next && !(ok = wait_w(s_free, i & 1, full(KS), (i + 1) & 1, g, 9) && issue_s())) break;
                     if (j == 0 && qd.k > 0 && !(ok = wait_w(dq_free, (qd.k - 1) & 1, g, 8))) break;
-                    if (!(ok = wait_w(full(KD), i & 1, g, 7) && wait_w(ds_full, i & 1, g, 6))) break;
+                    if (!(ok = wait_w(ds_full, i & 1, full(KD), i & 1, g, 6))) break;
                     tc_fence_after();
                     if (elect_one()) {
                         // dS of keys [16 ks, 16 ks + 16): the two halves of a row sit 64 columns apart
@@ -729,7 +761,7 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         if (j == qd.n - 1) mma_commit_pair(dq_done);
                     }
                     __syncwarp();
-                    if (next && !(ok = issue_dp(i + 1))) break;
+                    if (next && !(ok = wait_w(full(VS), (i + 1) & 1, g, 7) && issue_dp())) break;
                 }
             if (elect_one()) mma_commit_pair(mma_done);
             __syncwarp();
@@ -903,7 +935,7 @@ struct Segs {
         j = lo;
     }
     __device__ __forceinline__ bool next(const Args& a, Seg& s) {
-        if (pos >= end) return false;
+        if (pos >= end || j >= a.B * a.nkt) return false;
         const long long c0 = cum[j], c1 = cum[j + 1];
         s.j = j;
         s.b = j / a.nkt;
@@ -1046,12 +1078,11 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             };
             for (int j = 0; ok && j < min(2, sg.n); ++j)
                 if ((ok = wait_slot(L))) issue_s(j);
-            if (!ok || !(ok = wait_slot(L))) break;                  // Y_0
-            // The queue of the tensor pipe is two MMAs deep: what is waited for behind the second product's MMAs costs
-            // nothing, so the next operands are; only the wait for the next P^T is not covered
-            for (int j = 0; j < sg.n; ++j) {
+            for (int j = 0; ok && j < sg.n; ++j) {
                 const uint32_t i = gi + j, buf = i & 1, s = L % NSLOT;
-                if (!(ok = wait_w(p_full(buf), (i >> 1) & 1, g, 4))) break;
+                const bool more = j + 2 < sg.n;
+                const uint32_t lx = more ? L + 1 : L;                // X_{j+2} behind Y_j
+                if (!(ok = wait_w(p_full(buf), (i >> 1) & 1, full(s), (L / NSLOT) & 1, full(lx % NSLOT), (lx / NSLOT) & 1, g, 4))) break;
                 ++L;
                 tc_fence_after();
                 if (elect_one()) {
@@ -1063,9 +1094,6 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     if (j == sg.n - 1) mma_commit(acc_done);
                 }
                 __syncwarp();
-                const bool more = j + 2 < sg.n;                      // X_{j+2}, then Y_{j+1}
-                if (more && !(ok = wait_slot(L))) break;
-                if (j + 1 < sg.n && !(ok = wait_slot(more ? L + 1 : L))) break;
                 if (more) issue_s(j + 2);
             }
             gi += sg.n;
@@ -1221,8 +1249,8 @@ __global__ void __launch_bounds__(bk::BKEY) mqa_dkv_sum_kernel(const Args a, int
     G = pieces(total, G);
     auto cluster_of = [&](long long x) {
         int c = (int)(x * G / total);
-        while (piece(total, c + 1, G) <= x) ++c;
-        while (piece(total, c, G) > x) --c;
+        while (c + 1 < G && piece(total, c + 1, G) <= x) ++c;
+        while (c > 0 && piece(total, c, G) > x) --c;
         return c;
     };
     const int c0 = cluster_of(x0), c1 = cluster_of(x1);
@@ -1262,7 +1290,8 @@ __global__ void __launch_bounds__(bk::BKEY) mqa_dkv_sum_kernel(const Args a, int
 }
 
 // ---------------------------------------------------------------- backward: delta, the dk / dv line ----
-// delta = dO . out per query row (a warp a row); the last block adds up the row tiles of the key tiles
+// delta = dO . out per query row (a warp takes kDeltaRows rows, their loads in flight together: bound by HBM); the last block adds up the row tiles of the key tiles
+constexpr int kDeltaRows = 4;
 __global__ void __launch_bounds__(1024) mqa_delta_kernel(const Args a, const __nv_bfloat16* dout, const int* last_t,
                                                          long long* cum) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1296,19 +1325,29 @@ __global__ void __launch_bounds__(1024) mqa_delta_kernel(const Args a, const __n
         }
         return;
     }
-    const long long row = (long long)blockIdx.x * 32 + warp;
-    if (row >= (long long)a.B * a.TH) return;
-    const uint4 x = reinterpret_cast<const uint4*>(dout + row * D)[lane], y = reinterpret_cast<const uint4*>(a.out + row * D)[lane];
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-    float s = 0.f;
+    const long long row0 = ((long long)blockIdx.x * 32 + warp) * kDeltaRows, rows = (long long)a.B * a.TH;
+    uint4 x[kDeltaRows], y[kDeltaRows];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
-        s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
+    for (int i = 0; i < kDeltaRows; ++i) {
+        if (row0 + i >= rows) break;
+        x[i] = reinterpret_cast<const uint4*>(dout + (row0 + i) * D)[lane];
+        y[i] = reinterpret_cast<const uint4*>(a.out + (row0 + i) * D)[lane];
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) a.delta[row / a.TH * a.THp + row % a.TH] = s;
+    for (int i = 0; i < kDeltaRows; ++i) {
+        const long long row = row0 + i;
+        if (row >= rows) break;
+        const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, ys[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
+            s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) a.delta[row / a.TH * a.THp + row % a.TH] = s;
+    }
 }
 
 // What the forward keeps: lse, first keys and last queries, angles, the rotated queries and keys.
@@ -1439,13 +1478,12 @@ cudaError_t launch_mqa_forward(const rglru_mqa_dims* d, const void* q, const voi
     CUtensorMap mq, mk, mv;
     if (!map_rows(&mq, p + l.q_rot, a.TH, B, 128) || !map_rows(&mk, p + l.k_rot, T, B, 64) || !map_rows(&mv, v, T, B, 128))
         return cudaErrorInvalidValue;
-    mqa_angles_kernel<<<T, D / 2, 0, s>>>(pos0, d->rope_base, reinterpret_cast<float2*>(p + l.cs));
-    mqa_documents_kernel<<<B, kScanThreads, 0, s>>>(T, d->window, reset, reinterpret_cast<int*>(p + l.lo),
-                                                    reinterpret_cast<int*>(p + l.last));
-    mqa_turn_kernel<<<dim3(T, B), D / 2, 0, s>>>(T, H, a.cs, static_cast<const __nv_bfloat16*>(q),
-                                                 static_cast<const __nv_bfloat16*>(k),
-                                                 reinterpret_cast<__nv_bfloat16*>(p + l.q_rot),
-                                                 reinterpret_cast<__nv_bfloat16*>(p + l.k_rot));
+    mqa_prepare_kernel<<<B + (T + 7) / 8, kScanThreads, 0, s>>>(B, T, d->window, reset, reinterpret_cast<int*>(p + l.lo),
+                                                                reinterpret_cast<int*>(p + l.last), pos0, rope_base(d->rope_base),
+                                                                reinterpret_cast<float2*>(p + l.cs));
+    mqa_turn_kernel<<<(unsigned)(((long long)B * T + 15) / 16), 256, 0, s>>>(
+        (long long)B * T, T, H, a.cs, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+        reinterpret_cast<__nv_bfloat16*>(p + l.q_rot), reinterpret_cast<__nv_bfloat16*>(p + l.k_rot));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return launch_pairs(mqa_forward_kernel, std::min(pairs, B * a.ntr), fw::kThreads, fw::SMEM_BYTES, s, mq, mk, mv, a);
 }
@@ -1473,7 +1511,7 @@ cudaError_t launch_mqa_backward(const rglru_mqa_dims* d, const void* v, const vo
         !map_rows(&k128, p + l.k_rot, T, B, 128) || !map_rows(&v128, v, T, B, 128))
         return cudaErrorInvalidValue;
     const long long rows = (long long)B * a.TH;
-    mqa_delta_kernel<<<(unsigned)((rows + 31) / 32 + 1), 1024, 0, s>>>(a, static_cast<const __nv_bfloat16*>(dout), last,
+    mqa_delta_kernel<<<(unsigned)((rows + 32 * kDeltaRows - 1) / (32 * kDeltaRows) + 1), 1024, 0, s>>>(a, static_cast<const __nv_bfloat16*>(dout), last,
                                                                        const_cast<long long*>(a.cum));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_pairs(mqa_dq_kernel, std::min(pq, B * a.ntr), bq::kThreads, bq::SMEM_BYTES, s, q128, do128, k64, v64, k128, a);

@@ -123,6 +123,20 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Guard&
 __device__ __forceinline__ bool wait_w(uint32_t bar, uint32_t parity, const Guard& g, unsigned where) {
     return __all_sync(0xffffffffu, wait(bar, parity, g, where));
 }
+// The whole warp follows two or three waits, asked one behind the other before any answer is looked at: an answer
+// takes 80 cycles and more, in which an MMA warp that asks one by one leaves the tensor pipe (whose queue is two
+// MMAs deep) idle.
+__device__ __forceinline__ bool wait_w(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, const Guard& g, unsigned where) {
+    const bool r0 = mbar_try_wait(b0, p0), r1 = mbar_try_wait(b1, p1);
+    if (__all_sync(0xffffffffu, r0 & r1)) return true;
+    return __all_sync(0xffffffffu, wait(b0, p0, g, where) && wait(b1, p1, g, where + 16));
+}
+__device__ __forceinline__ bool wait_w(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2,
+                                       const Guard& g, unsigned where) {
+    const bool r0 = mbar_try_wait(b0, p0), r1 = mbar_try_wait(b1, p1), r2 = mbar_try_wait(b2, p2);
+    if (__all_sync(0xffffffffu, r0 & r1 & r2)) return true;
+    return __all_sync(0xffffffffu, wait(b0, p0, g, where) && wait(b1, p1, g, where + 16) && wait(b2, p2, g, where + 32));
+}
 // named barrier 1 over `threads` threads, returning the OR of v over them
 __device__ __forceinline__ bool bar_or(bool v, int threads) {
     uint32_t r;
