@@ -36,6 +36,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxClusters = 74;       // 2-CTA clusters of 148 SMs
 
 // ---------------------------------------------------------------- rotary embedding, documents ----
+constexpr int kAngleStep = 8, kAngleTokens = 64;         // tokens a block of 1024 threads has at a time, and in all
 constexpr int kScanThreads = 1024, kScanPer = 8, kScanChunk = kScanThreads * kScanPer;
 
 // The maximum (or minimum) of v over the threads of the block before this one, start for the first, and over all.
@@ -74,12 +75,23 @@ __device__ __forceinline__ int scan_before(int v, int start, int* warp_v, int& a
 // pos0 + t, pair j, [T][d/2], angle and reduction in fp64.
 __global__ void __launch_bounds__(kScanThreads) mqa_prepare_kernel(int B, int T, int w, const uint8_t* reset, int* lo, int* last,
                                                                    int pos0, RopeBase base, float2* cs) {
+    pdl_launch();
+    pdl_wait();
     if (blockIdx.x >= (unsigned)B) {
-        const int t = (blockIdx.x - B) * (kScanThreads / (D / 2)) + threadIdx.x / (D / 2), j = threadIdx.x % (D / 2);
+        int t = (blockIdx.x - B) * kAngleTokens + threadIdx.x / (D / 2);
+        const int j = threadIdx.x % (D / 2);
         if (t >= T) return;
-        double s, c;
+        // every kAngleStep-th token by an angle addition (a dozen units of fp64's last place at most)
+        double c, s, dc, ds;
         rope_cos_sin(base, j, (double)pos0 + t, c, s);
-        cs[(size_t)t * (D / 2) + j] = make_float2((float)c, (float)s);
+        rope_cos_sin(base, j, (double)kAngleStep, dc, ds);
+#pragma unroll 1
+        for (int i = 0; i < kAngleTokens / kAngleStep && t < T; ++i, t += kAngleStep) {
+            cs[(size_t)t * (D / 2) + j] = make_float2((float)c, (float)s);
+            const double x = c * dc - s * ds;
+            s = s * dc + c * ds;
+            c = x;
+        }
         return;
     }
     __shared__ int warp_v[32];
@@ -93,8 +105,10 @@ __global__ void __launch_bounds__(kScanThreads) mqa_prepare_kernel(int B, int T,
         const int t0 = c * kScanChunk + threadIdx.x * kScanPer;
         int v[kScanPer], run = 0;
 #pragma unroll
+        for (int e = 0; e < kScanPer; ++e) v[e] = rs ? rs[min(t0 + e, T - 1)] : 0;      // loads together
+#pragma unroll
         for (int e = 0; e < kScanPer; ++e) {
-            v[e] = t0 + e < T && rs && rs[t0 + e] ? t0 + e : 0;
+            v[e] = t0 + e < T && v[e] ? t0 + e : 0;
             run = max(run, v[e]);
         }
         run = max(carry, scan_before<true>(run, 0, warp_v, all));
@@ -111,8 +125,10 @@ __global__ void __launch_bounds__(kScanThreads) mqa_prepare_kernel(int B, int T,
         const int t1 = c * kScanChunk + (kScanThreads - (int)threadIdx.x) * kScanPer - 1;
         int v[kScanPer], run = T;
 #pragma unroll
+        for (int e = 0; e < kScanPer; ++e) v[e] = rs ? rs[min(t1 - e, T - 1)] : 0;
+#pragma unroll
         for (int e = 0; e < kScanPer; ++e) {
-            v[e] = t1 - e < T && rs && rs[t1 - e] ? t1 - e : T;
+            v[e] = t1 - e < T && v[e] ? t1 - e : T;
             run = min(run, v[e]);
         }
         run = min(carry, scan_before<false>(run, T, warp_v, all));
@@ -126,17 +142,54 @@ __global__ void __launch_bounds__(kScanThreads) mqa_prepare_kernel(int B, int T,
     }
 }
 
-// 16 threads a token, 8 pairs each, over its H query heads and its key: bound by HBM (q and k in and out), so
-// the rows of a few heads are in flight together
-constexpr int kTurnRows = 4;
-__global__ void __launch_bounds__(256) mqa_turn_kernel(long long tokens, int T, int H, const float2* cs, const __nv_bfloat16* q,
-                                                       const __nv_bfloat16* k, __nv_bfloat16* q_rot, __nv_bfloat16* k_rot) {
+// Blocks but the last: 16 threads a token, 8 pairs each, over its H query heads and its key: bound by HBM (q and k in
+// and out), so the rows of a few heads are in flight together.  The last block: the line of (key tile, row
+// tile) products that the backward cuts into pieces: cum[j] = the row tiles of the key tiles before j, a
+// key tile's rows being those from its first key's token to the last token that sees its last key.
+constexpr int kTurnRows = 4, kTurnThreads = 256, kKeyTile = 128, kRowTile = 64;
+__global__ void __launch_bounds__(kTurnThreads) mqa_turn_kernel(long long tokens, int T, int H, const float2* cs,
+                                                                const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                                                __nv_bfloat16* q_rot, __nv_bfloat16* k_rot, const int* last_t,
+                                                                long long* cum) {
+    pdl_launch();
+    pdl_wait();
+    if (blockIdx.x == gridDim.x - 1) {
+        __shared__ long long warp_v[kTurnThreads / 32];
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nkt = (T + kKeyTile - 1) / kKeyTile;
+        const long long nk = tokens / T * nkt;
+        long long carry = 0;
+        if (threadIdx.x == 0) cum[0] = 0;
+        for (long long j0 = 0; j0 < nk; j0 += kTurnThreads) {
+            const long long j = j0 + threadIdx.x;
+            long long v = 0;
+            if (j < nk) {
+                const int key0 = (int)(j % nkt) * kKeyTile, key1 = min(key0 + kKeyTile, T) - 1;
+                v = ((long long)(last_t[j / nkt * T + key1] + 1 - key0) * H + kRowTile - 1) / kRowTile;
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (lane == 31) warp_v[warp] = v;
+            __syncthreads();
+            long long before = carry;
+#pragma unroll
+            for (int i = 0; i < kTurnThreads / 32; ++i) {
+                if (i < warp) before += warp_v[i];
+                carry += warp_v[i];
+            }
+            if (j < nk) cum[j + 1] = before + v;
+            __syncthreads();
+        }
+        return;
+    }
     const long long tok = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
     const int c = threadIdx.x & 15;
     if (tok >= tokens) return;
     float4 a[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a[e] = __ldg(reinterpret_cast<const float4*>(cs + (size_t)(tok % T) * (D / 2) + 8 * c) + e);
+    for (int e = 0; e < 4; ++e) a[e] = reinterpret_cast<const float4*>(cs + (size_t)(tok % T) * (D / 2) + 8 * c)[e];
     for (int h0 = 0; h0 <= H; h0 += kTurnRows) {
         uint4 x[kTurnRows], y[kTurnRows];
 #pragma unroll
@@ -144,8 +197,8 @@ __global__ void __launch_bounds__(256) mqa_turn_kernel(long long tokens, int T, 
             const int h = h0 + i;
             if (h > H) break;
             const uint4* src = reinterpret_cast<const uint4*>(h < H ? q + (tok * H + h) * D : k + tok * D);
-            x[i] = __ldg(src + c);
-            y[i] = __ldg(src + 16 + c);
+            x[i] = src[c];
+            y[i] = src[16 + c];
         }
 #pragma unroll
         for (int i = 0; i < kTurnRows; ++i) {
@@ -287,6 +340,8 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
+    pdl_launch();
+    pdl_wait();
 
     if (warp == kWarpTma) {
         if (lane == 0) {
@@ -632,6 +687,8 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
+    pdl_launch();
+    pdl_wait();
 
     // Number i of the pair's key tiles uses each of the three buffers for the i-th time.
     if (warp == kWarpTma) {
@@ -788,6 +845,9 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 #pragma unroll 1
             for (int c = 0; c < 64; c += 16) {
                 float x1[16], x2[16];
+                float4 fs[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) fs[e] = cs[c / 2 + e];   // (cos, sin) of two pairs
                 tmem_ld16(tl + TM_DQ + half * 64 + c, x1);
                 tmem_ld16(tl + TM_DQ + 128 + half * 64 + c, x2);
                 tmem_wait_ld();
@@ -795,7 +855,7 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     uint32_t o1[8], o2[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float4 f = cs[c / 2 + e];              // (cos, sin) of two pairs
+                        const float4 f = fs[e];
                         const float y0 = x1[2 * e] * a.scale, y1 = x1[2 * e + 1] * a.scale;
                         const float z0 = x2[2 * e] * a.scale, z1 = x2[2 * e + 1] * a.scale;
                         o1[e] = bf16x2(y0 * f.x + z0 * f.y, y1 * f.z + z1 * f.w);
@@ -894,7 +954,7 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 // documents; a piece of a key tile leaves its sums in fp32 as part number (cluster + key tile), and
 // mqa_dkv_sum_kernel adds the parts of a key tile in order: the same bits at every run.
 namespace bk {
-constexpr int BR = 64, BKEY = 128;
+constexpr int BR = kRowTile, BKEY = kKeyTile;
 constexpr uint32_t SLOT = 32768;
 constexpr int NSLOT = 6, NVEC = 4;
 constexpr uint32_t OFF_P = NSLOT * SLOT, OFF_VEC = OFF_P + 2 * 16384, OFF_BAR = OFF_VEC + NVEC * 256;
@@ -1002,6 +1062,8 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
+    pdl_launch();
+    pdl_wait();
     Segs segs(a, cl, G);
     Seg sg{};
 
@@ -1240,11 +1302,15 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     }
 }
 
-// The sum of a key tile's parts in the clusters' order; dk is scaled and turned back.  Block = (key tile,
-// 32 columns: 16 of the first half with their partners for dk), thread = key; z = 0: dv, 1: dk.
-__global__ void __launch_bounds__(bk::BKEY) mqa_dkv_sum_kernel(const Args a, int G) {
+// The sum of a key tile's parts in the clusters' order; dk is scaled and turned back.  Thread = (key, 4 columns of the
+// first half and their partners of the second); block = 32 keys x 32 columns twice; z = 0: dv, 1: dk.
+__global__ void __launch_bounds__(256) mqa_dkv_sum_kernel(const Args a, int G) {
     using namespace bk;
-    const int j = blockIdx.x, z = blockIdx.z, r = threadIdx.x;
+    pdl_launch();
+    const int j = blockIdx.x, z = blockIdx.z, r = (blockIdx.y & 3) * 32 + (threadIdx.x >> 3);
+    const int grp = (blockIdx.y >> 2) * 8 + (threadIdx.x & 7);           // columns [4 grp, +4) and 128 further
+    const int b = j / a.nkt, key = (j % a.nkt) * BKEY + r;
+    pdl_wait();
     const long long total = a.cum[a.B * a.nkt], x0 = a.cum[j], x1 = a.cum[j + 1] - 1;
     G = pieces(total, G);
     auto cluster_of = [&](long long x) {
@@ -1254,78 +1320,36 @@ __global__ void __launch_bounds__(bk::BKEY) mqa_dkv_sum_kernel(const Args a, int
         return c;
     };
     const int c0 = cluster_of(x0), c1 = cluster_of(x1);
-    const int b = j / a.nkt, key = (j % a.nkt) * BKEY + r;
-    const int col1 = z == 0 ? blockIdx.y * 32 : blockIdx.y * 16, col2 = z == 0 ? col1 + 16 : col1 + 128;
-    float x[16] = {}, y[16] = {};
-    for (int c = c0; c <= c1; ++c) {
-        const float4* part = reinterpret_cast<const float4*>(a.part + ((size_t)(c + j) * 2 + z) * PART_FLOATS);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 u = part[(col1 / 4 + e) * BKEY + r], v = part[(col2 / 4 + e) * BKEY + r];
-            x[4 * e] += u.x; x[4 * e + 1] += u.y; x[4 * e + 2] += u.z; x[4 * e + 3] += u.w;
-            y[4 * e] += v.x; y[4 * e + 1] += v.y; y[4 * e + 2] += v.z; y[4 * e + 3] += v.w;
-        }
-    }
     if (key >= a.T) return;
+    const float4* cs = reinterpret_cast<const float4*>(a.cs + (size_t)key * (D / 2) + 4 * grp);
+    const float4 f0 = cs[0], f1 = cs[1];
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+        const float4* part = reinterpret_cast<const float4*>(a.part + ((size_t)(c + j) * 2 + z) * PART_FLOATS) + r;
+        const float4 u = part[grp * BKEY], v = part[(grp + 32) * BKEY];
+        x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+        y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+    }
     if (z == 1) {
-        const float2* cs = a.cs + (size_t)key * (D / 2) + col1;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const float2 f = cs[e];
-            const float u = x[e] * a.scale, v = y[e] * a.scale;
-            x[e] = u * f.x + v * f.y;
-            y[e] = v * f.x - u * f.y;
-        }
+        const float4 u = make_float4(x.x * a.scale, x.y * a.scale, x.z * a.scale, x.w * a.scale);
+        const float4 v = make_float4(y.x * a.scale, y.y * a.scale, y.z * a.scale, y.w * a.scale);
+        x = make_float4(u.x * f0.x + v.x * f0.y, u.y * f0.z + v.y * f0.w, u.z * f1.x + v.z * f1.y, u.w * f1.z + v.w * f1.w);
+        y = make_float4(v.x * f0.x - u.x * f0.y, v.y * f0.z - u.y * f0.w, v.z * f1.x - u.z * f1.y, v.w * f1.z - u.w * f1.w);
     }
-    __nv_bfloat16* o = (z == 0 ? a.dv : a.dk) + ((size_t)b * a.T + key) * D;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        reinterpret_cast<uint4*>(o + col1)[e] =
-            make_uint4(pr::bf16x2(x[8 * e], x[8 * e + 1]), pr::bf16x2(x[8 * e + 2], x[8 * e + 3]),
-                       pr::bf16x2(x[8 * e + 4], x[8 * e + 5]), pr::bf16x2(x[8 * e + 6], x[8 * e + 7]));
-        reinterpret_cast<uint4*>(o + col2)[e] =
-            make_uint4(pr::bf16x2(y[8 * e], y[8 * e + 1]), pr::bf16x2(y[8 * e + 2], y[8 * e + 3]),
-                       pr::bf16x2(y[8 * e + 4], y[8 * e + 5]), pr::bf16x2(y[8 * e + 6], y[8 * e + 7]));
-    }
+    __nv_bfloat16* o = (z == 0 ? a.dv : a.dk) + ((size_t)b * a.T + key) * D + 4 * grp;
+    *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2(x.x, x.y), bf16x2(x.z, x.w));
+    *reinterpret_cast<uint2*>(o + 128) = make_uint2(bf16x2(y.x, y.y), bf16x2(y.z, y.w));
 }
 
-// ---------------------------------------------------------------- backward: delta, the dk / dv line ----
-// delta = dO . out per query row (a warp takes kDeltaRows rows, their loads in flight together: bound by HBM); the last block adds up the row tiles of the key tiles
-constexpr int kDeltaRows = 4;
-__global__ void __launch_bounds__(1024) mqa_delta_kernel(const Args a, const __nv_bfloat16* dout, const int* last_t,
-                                                         long long* cum) {
+// ---------------------------------------------------------------- backward: delta ------------------------
+// delta = dO . out per query row (a warp takes kDeltaRows rows, their loads in flight together: bound by HBM)
+constexpr int kDeltaRows = 4, kDeltaWarps = 8;
+__global__ void __launch_bounds__(32 * kDeltaWarps) mqa_delta_kernel(const Args a, const __nv_bfloat16* dout) {
+    pdl_launch();
+    pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (blockIdx.x == gridDim.x - 1) {
-        __shared__ long long warp_v[32];
-        const int nk = a.B * a.nkt;
-        long long carry = 0;
-        if (threadIdx.x == 0) cum[0] = 0;
-        for (int j0 = 0; j0 < nk; j0 += 1024) {
-            const int j = j0 + threadIdx.x;
-            long long v = 0;
-            if (j < nk) {
-                // rows [key0 H, (last + 1) H): up to the last token that the tile's last key is seen by
-                const int b = j / a.nkt, key0 = (j % a.nkt) * bk::BKEY, key1 = min(key0 + bk::BKEY, a.T) - 1;
-                v = ((long long)(last_t[(size_t)b * a.T + key1] + 1 - key0) * a.H + bk::BR - 1) / bk::BR;
-            }
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
-            }
-            if (lane == 31) warp_v[warp] = v;
-            __syncthreads();
-            long long base = carry;
-            for (int i = 0; i < 32; ++i) {
-                if (i < warp) base += warp_v[i];
-                carry += warp_v[i];
-            }
-            if (j < nk) cum[j + 1] = base + v;
-            __syncthreads();
-        }
-        return;
-    }
-    const long long row0 = ((long long)blockIdx.x * 32 + warp) * kDeltaRows, rows = (long long)a.B * a.TH;
+    const long long row0 = ((long long)blockIdx.x * kDeltaWarps + warp) * kDeltaRows, rows = (long long)a.B * a.TH;
     uint4 x[kDeltaRows], y[kDeltaRows];
 #pragma unroll
     for (int i = 0; i < kDeltaRows; ++i) {
@@ -1350,12 +1374,13 @@ __global__ void __launch_bounds__(1024) mqa_delta_kernel(const Args a, const __n
     }
 }
 
-// What the forward keeps: lse, first keys and last queries, angles, the rotated queries and keys.
+// What the forward keeps: lse, first keys and last queries, the backward's line, angles, the rotated queries and keys.
 struct SaveLayout {
-    size_t lse, lo, last, cs, q_rot, k_rot, total;
+    size_t lse, lo, last, cum, cs, q_rot, k_rot, total;
 };
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 inline size_t row_pitch(const rglru_mqa_dims* d) { return ((size_t)d->seq_len * d->q_heads + 63) & ~size_t(63); }
+inline int key_tiles(const rglru_mqa_dims* d) { return (d->seq_len + kKeyTile - 1) / kKeyTile; }
 inline SaveLayout save_layout(const rglru_mqa_dims* d) {
     const size_t tok = (size_t)d->batch * d->seq_len;
     SaveLayout l{};
@@ -1363,22 +1388,21 @@ inline SaveLayout save_layout(const rglru_mqa_dims* d) {
     l.lse = o; o = up256(o + d->batch * row_pitch(d) * 4);
     l.lo = o; o = up256(o + tok * 4);
     l.last = o; o = up256(o + tok * 4);
+    l.cum = o; o = up256(o + ((size_t)d->batch * key_tiles(d) + 1) * 8);
     l.cs = o; o = up256(o + (size_t)d->seq_len * (D / 2) * sizeof(float2));
     l.q_rot = o; o = up256(o + tok * d->q_heads * D * 2);
     l.k_rot = o; o = up256(o + tok * D * 2);
     l.total = o;
     return l;
 }
-inline int key_tiles(const rglru_mqa_dims* d) { return (d->seq_len + bk::BKEY - 1) / bk::BKEY; }
 struct WsLayout {
-    size_t delta, cum, part, total;
+    size_t delta, part, total;
 };
 inline WsLayout ws_layout(const rglru_mqa_dims* d) {
     const size_t nk = (size_t)d->batch * key_tiles(d);
     WsLayout l{};
     size_t o = 256;                    // the status word
     l.delta = o; o = up256(o + d->batch * row_pitch(d) * 4);
-    l.cum = o; o = up256(o + (nk + 1) * 8);
     l.part = o; o = up256(o + (nk + kMaxClusters) * 2 * bk::PART_FLOATS * 4);
     l.total = o;
     return l;
@@ -1398,7 +1422,7 @@ inline Args make_args(const rglru_mqa_dims* d, void* save, void* ws) {
     a.lo = reinterpret_cast<const int*>(p + l.lo);
     a.lse = reinterpret_cast<float*>(p + l.lse);
     a.delta = reinterpret_cast<float*>(w + wl.delta);
-    a.cum = reinterpret_cast<const long long*>(w + wl.cum);
+    a.cum = reinterpret_cast<const long long*>(p + l.cum);
     a.part = reinterpret_cast<float*>(w + wl.part);
     a.status = static_cast<DeviceStatus*>(ws);
     a.timeout_ns = 1000000000ull;
@@ -1442,20 +1466,23 @@ cudaError_t resident_pairs(K kern, int threads, uint32_t smem, int which, int* p
     return cudaSuccess;
 }
 
+// a launch behind the kernel before it on the stream (programmatic dependent), in clusters of `cluster` CTAs
 template <typename... KArgs, typename... Given>
-cudaError_t launch_pairs(void (*kern)(KArgs...), int pairs, int threads, uint32_t smem, cudaStream_t s, const Given&... given) {
+cudaError_t launch(void (*kern)(KArgs...), dim3 grid, int threads, uint32_t smem, int cluster, cudaStream_t s, const Given&... given) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2u * (unsigned)pairs);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, given...);
 }
 
@@ -1478,14 +1505,17 @@ cudaError_t launch_mqa_forward(const rglru_mqa_dims* d, const void* q, const voi
     CUtensorMap mq, mk, mv;
     if (!map_rows(&mq, p + l.q_rot, a.TH, B, 128) || !map_rows(&mk, p + l.k_rot, T, B, 64) || !map_rows(&mv, v, T, B, 128))
         return cudaErrorInvalidValue;
-    mqa_prepare_kernel<<<B + (T + 7) / 8, kScanThreads, 0, s>>>(B, T, d->window, reset, reinterpret_cast<int*>(p + l.lo),
-                                                                reinterpret_cast<int*>(p + l.last), pos0, rope_base(d->rope_base),
-                                                                reinterpret_cast<float2*>(p + l.cs));
-    mqa_turn_kernel<<<(unsigned)(((long long)B * T + 15) / 16), 256, 0, s>>>(
-        (long long)B * T, T, H, a.cs, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-        reinterpret_cast<__nv_bfloat16*>(p + l.q_rot), reinterpret_cast<__nv_bfloat16*>(p + l.k_rot));
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_pairs(mqa_forward_kernel, std::min(pairs, B * a.ntr), fw::kThreads, fw::SMEM_BYTES, s, mq, mk, mv, a);
+    const long long tokens = (long long)B * T;
+    e = launch(mqa_prepare_kernel, dim3(B + (T + kAngleTokens - 1) / kAngleTokens), kScanThreads, 0, 1, s, B, T, d->window, reset,
+               reinterpret_cast<int*>(p + l.lo), reinterpret_cast<int*>(p + l.last), pos0, rope_base(d->rope_base),
+               reinterpret_cast<float2*>(p + l.cs));
+    if (e != cudaSuccess) return e;
+    e = launch(mqa_turn_kernel, dim3((unsigned)((tokens + 15) / 16 + 1)), kTurnThreads, 0, 1, s, tokens, T, H, a.cs,
+               static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+               reinterpret_cast<__nv_bfloat16*>(p + l.q_rot), reinterpret_cast<__nv_bfloat16*>(p + l.k_rot),
+               reinterpret_cast<const int*>(p + l.last), reinterpret_cast<long long*>(p + l.cum));
+    if (e != cudaSuccess) return e;
+    return launch(mqa_forward_kernel, dim3(2 * std::min(pairs, B * a.ntr)), fw::kThreads, fw::SMEM_BYTES, 2, s, mq, mk, mv, a);
 }
 
 cudaError_t launch_mqa_backward(const rglru_mqa_dims* d, const void* v, const void* out, const void* dout,
@@ -1511,15 +1541,15 @@ cudaError_t launch_mqa_backward(const rglru_mqa_dims* d, const void* v, const vo
         !map_rows(&k128, p + l.k_rot, T, B, 128) || !map_rows(&v128, v, T, B, 128))
         return cudaErrorInvalidValue;
     const long long rows = (long long)B * a.TH;
-    mqa_delta_kernel<<<(unsigned)((rows + 32 * kDeltaRows - 1) / (32 * kDeltaRows) + 1), 1024, 0, s>>>(a, static_cast<const __nv_bfloat16*>(dout), last,
-                                                                       const_cast<long long*>(a.cum));
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_pairs(mqa_dq_kernel, std::min(pq, B * a.ntr), bq::kThreads, bq::SMEM_BYTES, s, q128, do128, k64, v64, k128, a);
+    constexpr int per = kDeltaWarps * kDeltaRows;
+    e = launch(mqa_delta_kernel, dim3((unsigned)((rows + per - 1) / per)), 32 * kDeltaWarps, 0, 1, s, a,
+               static_cast<const __nv_bfloat16*>(dout));
     if (e != cudaSuccess) return e;
-    e = launch_pairs(mqa_dkv_kernel, pk, bk::kThreads, bk::SMEM_BYTES, s, q64, do64, k128, v128, last, a);
+    e = launch(mqa_dq_kernel, dim3(2 * std::min(pq, B * a.ntr)), bq::kThreads, bq::SMEM_BYTES, 2, s, q128, do128, k64, v64, k128, a);
     if (e != cudaSuccess) return e;
-    mqa_dkv_sum_kernel<<<dim3(B * a.nkt, 8, 2), bk::BKEY, 0, s>>>(a, pk);
-    return cudaGetLastError();
+    e = launch(mqa_dkv_kernel, dim3(2 * pk), bk::kThreads, bk::SMEM_BYTES, 2, s, q64, do64, k128, v128, last, a);
+    if (e != cudaSuccess) return e;
+    return launch(mqa_dkv_sum_kernel, dim3(B * a.nkt, 16, 2), 256, 0, 1, s, a, pk);
 }
 
 }  // namespace rglru

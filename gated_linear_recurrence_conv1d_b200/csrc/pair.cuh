@@ -96,6 +96,12 @@ __device__ __forceinline__ void st_async_v4(uint32_t dst_cluster, uint32_t a, ui
                  : "memory");
 }
 
+// Programmatic dependent launch: the kernel behind this one may be launched from now on (its set-up overlaps this
+// kernel); and the kernels before this one are complete and their writes visible.  Every CTA of every
+// kernel of a chain waits, so that "the kernel before" stands for all of them.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Bounded waits: a wait that expires latches TIMEOUT (site, CTA) and makes every later wait of the CTA fail.
 struct Guard {
     volatile int* abort;               // shared memory, one per CTA
