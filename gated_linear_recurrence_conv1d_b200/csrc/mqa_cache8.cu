@@ -6,7 +6,9 @@
 //     scale = max(amax |x|, 448 * 2^-126) / 448,   code = e4m3(x / scale),   value = code * scale
 // (448 is e4m3's largest value; the floor keeps the scale of a zero slot a normal number).  The key is
 // rotated, and the quotient taken, in fp64 and rounded once to fp32 before the code: a code then does
-// not depend on the rounding of a sine or a product next to a border between two codes.
+// not depend on the rounding of a sine or a product next to a border between two codes.  (The quotient is the
+// product with the fp64 reciprocal, off by 2^-52: after the rounding to fp32 a quotient that is exactly
+// on a border, which has 5 bits, is on it again.)
 #include <algorithm>
 
 #include <cuda.h>
@@ -61,10 +63,14 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t c) {
 
 // ---- one slot by one warp ------------------------------------------------------------------------------
 // lane l holds the pairs j = 4 l .. 4 l + 3: elements j and j + 128
-__device__ __forceinline__ double max_nan(double a, double b) { return (a != a || b != b) ? a + b : fmax(a, b); }
-__device__ __forceinline__ void load_pairs(const __nv_bfloat16* p, int lane, float (&x)[8]) {
-    const uint2 u = reinterpret_cast<const uint2*>(p)[lane], v = reinterpret_cast<const uint2*>(p + D / 2)[lane];
-    const uint32_t w[4] = {u.x, u.y, v.x, v.y};
+struct Pairs {
+    uint2 a, b;                        // bf16
+};
+__device__ __forceinline__ Pairs load_pairs(const __nv_bfloat16* p, int lane) {
+    return Pairs{reinterpret_cast<const uint2*>(p)[lane], reinterpret_cast<const uint2*>(p + D / 2)[lane]};
+}
+__device__ __forceinline__ void unpack(const Pairs& p, float (&x)[8]) {
+    const uint32_t w[4] = {p.a.x, p.a.y, p.b.x, p.b.y};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         x[2 * e] = __uint_as_float(w[e] << 16);
@@ -72,16 +78,17 @@ __device__ __forceinline__ void load_pairs(const __nv_bfloat16* p, int lane, flo
     }
 }
 __device__ __forceinline__ void quantise_slot(const double (&x)[8], int lane, uint8_t* codes, float* scale) {
-    double m = 0.0;
+    // the largest |x| by its bits: a NaN is larger than infinity, so the slot is NaN as a whole
+    long long m = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max_nan(m, fabs(x[e]));          // a NaN stays: the slot is NaN as a whole
+    for (int e = 0; e < 8; ++e) m = max(m, __double_as_longlong(fabs(x[e])));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m < kFloor) m = kFloor;
-    const float s = (float)(m / 448.0);
+    for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float s = (float)(__longlong_as_double(max(m, __double_as_longlong(kFloor))) / 448.0);
+    const double r = 1.0 / (double)s;
     float q[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = (float)(x[e] / (double)s);
+    for (int e = 0; e < 8; ++e) q[e] = (float)(x[e] * r);
     reinterpret_cast<uint32_t*>(codes)[lane] = e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16;
     reinterpret_cast<uint32_t*>(codes + D / 2)[lane] = e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16;
     if (lane == 0) *scale = s;
@@ -100,60 +107,76 @@ __device__ __forceinline__ void widen(const float (&x)[8], double (&y)[8]) {
 }
 
 // ---------------------------------------------------------------- write -------------------------------
-// Block = (token, up to kRows batch rows): the angles of the token's position once for all of them (they
-// are most of the arithmetic), then a warp per key or value.  The last min(len, w) tokens of a row
-// go into their slots.
+// Block = (token, up to kWriteRows batch rows): the angles of the token's position once for all of them (they are
+// half of the arithmetic), while the rows' keys and values are on their way; a warp per row.  The last min(len, w)
+// tokens of a row go into their slots.
 constexpr int kWriteRows = 8;
-__global__ void __launch_bounds__(128) mqa_cache8_write_kernel(int B, int T, int w, int pos0, RopeBase base, const int* lengths,
-                                                               const __nv_bfloat16* k, const __nv_bfloat16* v,
-                                                               uint8_t* codes, float* scales) {
+__global__ void __launch_bounds__(32 * kWriteRows) mqa_cache8_write_kernel(int B, int T, int w, int pos0, RopeBase base,
+                                                                           const int* lengths, const __nv_bfloat16* k,
+                                                                           const __nv_bfloat16* v, uint8_t* codes, float* scales) {
     __shared__ double2 cs[D / 2];
-    const int t = blockIdx.x + (lengths ? 0 : max(0, T - w)), b0 = blockIdx.y * kWriteRows;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nb = min(kWriteRows, B - b0);
-    bool any = !lengths;
-    for (int i = 0; i < nb && !any; ++i) {
-        const int len = min(lengths[b0 + i], T);
-        any = t < len && t >= len - w;
+    const int t = blockIdx.x + (lengths ? 0 : max(0, T - w));
+    const int lane = threadIdx.x & 31, b = blockIdx.y * kWriteRows + (threadIdx.x >> 5);
+    bool mine = b < B;
+    if (mine && lengths) {
+        const int len = min(lengths[b], T);
+        mine = t < len && t >= len - w;
     }
-    if (!any) return;
+    if (!__syncthreads_or(mine)) return;
+    Pairs pk{}, pv{};
+    if (mine) {
+        pk = load_pairs(k + ((size_t)b * T + t) * D, lane);
+        pv = load_pairs(v + ((size_t)b * T + t) * D, lane);
+    }
     const long long p = (long long)pos0 + t;
-    rope_cos_sin(base, threadIdx.x, (double)p, cs[threadIdx.x].x, cs[threadIdx.x].y);
+    if (threadIdx.x < D / 2) rope_cos_sin(base, threadIdx.x, (double)p, cs[threadIdx.x].x, cs[threadIdx.x].y);
     __syncthreads();
-    const int slot = (int)(p % w);
-    for (int i = warp; i < 2 * nb; i += 4) {
-        const int b = b0 + (i >> 1), val = i & 1;
-        if (lengths) {
-            const int len = min(lengths[b], T);
-            if (t >= len || t < len - w) continue;
-        }
-        float x[8];
-        double y[8];
-        load_pairs((val ? v : k) + ((size_t)b * T + t) * D, lane, x);
-        if (val) widen(x, y); else turn64(x, cs, lane, y);
-        const size_t s = ((size_t)b * 2 + val) * w + slot;
-        quantise_slot(y, lane, codes + s * D, scales + s);
-    }
+    if (!mine) return;
+    const size_t s = (size_t)b * 2 * w + (int)(p % w);
+    float x[8];
+    double y[8];
+    unpack(pk, x);
+    turn64(x, cs, lane, y);
+    quantise_slot(y, lane, codes + s * D, scales + s);
+    unpack(pv, x);
+    widen(x, y);
+    quantise_slot(y, lane, codes + (s + w) * D, scales + s + w);
 }
 
 // ---------------------------------------------------------------- read ---------------------------------
-// A warp per slot and lane = 8 elements
+// 16 lanes a slot, 16 codes each, kReadSlots slots a half warp, their loads in flight together: bound by HBM
+constexpr int kReadSlots = 4, kReadBlock = 16 * kReadSlots;          // slots of a block of 256 threads
 __global__ void __launch_bounds__(256) mqa_cache8_read_kernel(long long slots, int w, const int* pos,
                                                               const uint8_t* codes, const float* scales,
                                                               __nv_bfloat16* cache) {
-    const long long s = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (s >= slots) return;
-    if (pos && s % w > pos[s / (2 * (long long)w)]) return;
-    const uint2 c = *reinterpret_cast<const uint2*>(codes + s * D + 8 * lane);
-    const float f = scales[s];
-    uint32_t o[4];
+    const long long s0 = (long long)blockIdx.x * kReadBlock + (threadIdx.x >> 4);
+    const int c = threadIdx.x & 15;
+    uint4 u[kReadSlots];
+    float f[kReadSlots];
+    bool have[kReadSlots];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 x = e4m3x2_values(((e < 2 ? c.x : c.y) >> (16 * (e & 1))) & 0xffffu);
-        o[e] = bf16x2(f * x.x, f * x.y);
+    for (int i = 0; i < kReadSlots; ++i) {
+        const long long s = s0 + 16 * i;
+        have[i] = s < slots && (!pos || s % w <= pos[s / (2 * (long long)w)]);
+        if (have[i]) {
+            u[i] = reinterpret_cast<const uint4*>(codes + s * D)[c];
+            f[i] = scales[s];
+        }
     }
-    *reinterpret_cast<uint4*>(cache + s * D + 8 * lane) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+    for (int i = 0; i < kReadSlots; ++i) {
+        if (!have[i]) continue;
+        const uint32_t q[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float2 x = e4m3x2_values((q[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+            o[e] = bf16x2(f[i] * x.x, f[i] * x.y);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(cache + (s0 + 16 * i) * D) + 2 * c;
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
 }
 
 // ---------------------------------------------------------------- decode: queries and the new slot -----
@@ -185,13 +208,13 @@ __global__ void __launch_bounds__(256) mqa_decode8_turn_kernel(int H, int w, Rop
         if (i >= H) {
             const int val = i - H;
             double y[8];
-            load_pairs((val ? v : k) + (size_t)b * D, lane, x);
+            unpack(load_pairs((val ? v : k) + (size_t)b * D, lane), x);
             if (val) widen(x, y); else turn64(x, cs, lane, y);
             const size_t s = ((size_t)b * 2 + val) * w + slot;
             quantise_slot(y, lane, codes + s * D, scales + s);
             continue;
         }
-        load_pairs(q + ((size_t)b * H + i) * D, lane, x);
+        unpack(load_pairs(q + ((size_t)b * H + i) * D, lane), x);
         float y[8], m = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -819,7 +842,7 @@ cudaError_t launch_mqa_cache8_write(const rglru_mqa_dims* d, const void* k, cons
     using namespace c8;
     // without lengths only the last min(T, w) tokens are written; with them any token may be
     const int tokens = lengths ? d->seq_len : std::min(d->seq_len, d->window);
-    mqa_cache8_write_kernel<<<dim3(tokens, (d->batch + kWriteRows - 1) / kWriteRows), 128, 0, s>>>(
+    mqa_cache8_write_kernel<<<dim3(tokens, (d->batch + kWriteRows - 1) / kWriteRows), 32 * kWriteRows, 0, s>>>(
         d->batch, d->seq_len, d->window, pos0, rope_base(d->rope_base), lengths, static_cast<const __nv_bfloat16*>(k),
         static_cast<const __nv_bfloat16*>(v), static_cast<uint8_t*>(codes), scales);
     return cudaGetLastError();
@@ -876,7 +899,7 @@ cudaError_t launch_mqa_cache8_read(const rglru_mqa_dims* d, const void* codes, c
                                    void* cache, cudaStream_t s) {
     using namespace c8;
     const long long slots = 2LL * d->batch * d->window;
-    mqa_cache8_read_kernel<<<(unsigned)((slots + 7) / 8), 256, 0, s>>>(slots, d->window, pos,
+    mqa_cache8_read_kernel<<<(unsigned)((slots + kReadBlock - 1) / kReadBlock), 256, 0, s>>>(slots, d->window, pos,
                                                                        static_cast<const uint8_t*>(codes), scales,
                                                                        static_cast<__nv_bfloat16*>(cache));
     return cudaGetLastError();
