@@ -77,7 +77,12 @@ __device__ __forceinline__ void unpack(const Pairs& p, float (&x)[8]) {
         x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void quantise_slot(const double (&x)[8], int lane, uint8_t* codes, float* scale) {
+// this lane's codes: 4 of the first half, 4 of the second; every lane has the scale
+struct SlotCodes {
+    uint32_t a, b;
+    float scale;
+};
+__device__ __forceinline__ SlotCodes quantise_slot(const double (&x)[8]) {
     // the largest |x| by its bits: a NaN is larger than infinity, so the slot is NaN as a whole
     long long m = 0;
 #pragma unroll
@@ -89,9 +94,12 @@ __device__ __forceinline__ void quantise_slot(const double (&x)[8], int lane, ui
     float q[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) q[e] = (float)(x[e] * r);
-    reinterpret_cast<uint32_t*>(codes)[lane] = e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16;
-    reinterpret_cast<uint32_t*>(codes + D / 2)[lane] = e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16;
-    if (lane == 0) *scale = s;
+    return SlotCodes{e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16, e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16, s};
+}
+__device__ __forceinline__ void store_slot(const SlotCodes& c, int lane, uint8_t* codes, float* scale) {
+    reinterpret_cast<uint32_t*>(codes)[lane] = c.a;
+    reinterpret_cast<uint32_t*>(codes + D / 2)[lane] = c.b;
+    if (lane == 0) *scale = c.scale;
 }
 __device__ __forceinline__ void turn64(const float (&x)[8], const double2* cs, int lane, double (&y)[8]) {
 #pragma unroll
@@ -137,10 +145,10 @@ __global__ void __launch_bounds__(32 * kWriteRows) mqa_cache8_write_kernel(int B
     double y[8];
     unpack(pk, x);
     turn64(x, cs, lane, y);
-    quantise_slot(y, lane, codes + s * D, scales + s);
+    store_slot(quantise_slot(y), lane, codes + s * D, scales + s);
     unpack(pv, x);
     widen(x, y);
-    quantise_slot(y, lane, codes + (s + w) * D, scales + s + w);
+    store_slot(quantise_slot(y), lane, codes + (s + w) * D, scales + s + w);
 }
 
 // ---------------------------------------------------------------- read ---------------------------------
@@ -179,82 +187,8 @@ __global__ void __launch_bounds__(256) mqa_cache8_read_kernel(long long slots, i
     }
 }
 
-// ---------------------------------------------------------------- decode: queries and the new slot -----
-// Queries enter the score MMA as e4m3 too, in three parts: with 2^e the power of two that brings the head's
-// largest rotated element into (224, 448],  q~ = 2^e (x0 + x1 / 16 + x2 / 256) + r, x0 = e4m3(q~ 2^-e),
-// x1 = e4m3(16 (q~ 2^-e - x0)), ...: a part is off by at most 2^-4 of itself, so |r| <= 2^-12 |q~| (or
-// 2^-18 448 2^e where x2 is below e4m3's normal numbers), less than bf16 would leave.
-constexpr int kQParts = 3, kQRows = kQParts * kMaxH;
-__global__ void __launch_bounds__(256) mqa_decode8_turn_kernel(int H, int w, RopeBase base, const int* pos,
-                                                               const __nv_bfloat16* q, const __nv_bfloat16* k,
-                                                               const __nv_bfloat16* v, uint8_t* qp, float* qs,
-                                                               unsigned* done, uint8_t* codes, float* scales,
-                                                               __nv_bfloat16* out) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ double2 cs[D / 2];
-    const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int p = pos[b];
-    if (threadIdx.x < 2) done[2 * b + threadIdx.x] = 0;
-    if (p < 0) {                                     // a row without a token
-        for (int e = threadIdx.x; e < H * D / 8; e += 256)
-            reinterpret_cast<uint4*>(out + (size_t)b * H * D)[e] = make_uint4(0, 0, 0, 0);
-        return;
-    }
-    float x[8];
-    if (threadIdx.x < D / 2) rope_cos_sin(base, threadIdx.x, (double)p, cs[threadIdx.x].x, cs[threadIdx.x].y);
-    __syncthreads();
-    const int slot = p % w;
-    for (int i = warp; i < H + 2; i += 8) {
-        if (i >= H) {
-            const int val = i - H;
-            double y[8];
-            unpack(load_pairs((val ? v : k) + (size_t)b * D, lane), x);
-            if (val) widen(x, y); else turn64(x, cs, lane, y);
-            const size_t s = ((size_t)b * 2 + val) * w + slot;
-            quantise_slot(y, lane, codes + s * D, scales + s);
-            continue;
-        }
-        unpack(load_pairs(q + ((size_t)b * H + i) * D, lane), x);
-        float y[8], m = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float c = (float)cs[4 * lane + e].x, s = (float)cs[4 * lane + e].y;
-            y[e] = x[e] * c - x[4 + e] * s;
-            y[4 + e] = x[4 + e] * c + x[e] * s;
-            m = fmaxf(m, fmaxf(fabsf(y[e]), fabsf(y[4 + e])));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        // m / 448 rounded up to a power of two (at least 2^-100, so that its reciprocal is finite)
-        const float r448 = fminf(fmaxf(m, 448.0f * 7.9e-31f), 3.0e38f) * (1.0f / 448.0f);
-        int e2 = (__float_as_int(r448) >> 23) - 127;
-        if (__float_as_int(r448) & 0x7fffff) ++e2;
-        const float up = __int_as_float((e2 + 127) << 23), down = __int_as_float((127 - e2) << 23);
-        if (lane == 0) qs[b * kMaxH + head_row(i)] = m < INFINITY ? up : __int_as_float(0x7fffffff);   // an infinity: NaN
-        uint32_t c[kQParts][2] = {};
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            float u = y[e] * down, z = y[e + 1] * down;
-#pragma unroll
-            for (int part = 0; part < kQParts; ++part) {
-                const uint32_t cc = e4m3x2(u, z);
-                const float2 f = e4m3x2_values(cc);
-                c[part][e >> 2] |= cc << (8 * (e & 2));
-                u = (u - f.x) * 16.0f;
-                z = (z - f.y) * 16.0f;
-            }
-        }
-#pragma unroll
-        for (int part = 0; part < kQParts; ++part) {
-            uint8_t* row = qp + ((size_t)b * kQRows + part * kMaxH + head_row(i)) * D;
-            reinterpret_cast<uint32_t*>(row)[lane] = c[part][0];
-            reinterpret_cast<uint32_t*>(row + D / 2)[lane] = c[part][1];
-        }
-    }
-}
-
 // ---------------------------------------------------------------- decode: attention --------------------
-// The slots of a row are cut into tiles of 128 and the tiles of all rows laid out as one line, of which every
+// One kernel.  The slots of a row are cut into tiles of 128 and the tiles of all rows laid out as one line, of which every
 // CTA takes an equal piece (a "segment" is a piece of one row): the rings' bytes are spread evenly
 // over the SMs whatever the rows' lengths.  Per tile
 //   S^T = K Qp^T   (M 128 slots, N 48 = 16 heads x 3 parts, K 256; e4m3, fp32 sums)
@@ -268,17 +202,30 @@ __global__ void __launch_bounds__(256) mqa_decode8_turn_kernel(int H, int w, Rop
 // moves it is rescaled there (each group has its own vref and its own columns of S, W and O, so the groups
 // never meet).  A row inside one segment is written at once; else the segments leave (m, sum, O) and the
 // one that finishes last adds them up in order.
+// At the beginning of a segment (the first tiles are on their way meanwhile, and after the first segment the last
+// products of the segment before run) the softmax warps rotate the row's queries and write their parts as the B
+// operand: with 2^e the power of two that brings the head's largest element into (224, 448],
+// q~ = 2^e (x0 + x1 / 16 + x2 / 256) + r, x0 = e4m3(q~ 2^-e), x1 = e4m3(16 (q~ 2^-e - x0)), ...: a part is off by at most
+// 2^-4 of itself, so |r| <= 2^-12 |q~| (or 2^-18 448 2^e where x2 is below e4m3's normal numbers), less than
+// bf16 would leave.  The segment that holds the row's new slot also rotates and quantises the new key and value, writes them
+// to the ring and hands them to the MMA warp, which puts them into the tiles that it has (they may have been
+// loaded before the ring was written).
 // The step reads every code once: bound by HBM.
 constexpr uint32_t TILE_BYTES = kTile * D;            // 32768: 2 boxes of [128 slots x 128 B]
 constexpr int kNBuf = 5;
+constexpr int kMaxCtas = 148;
+constexpr int kQParts = 3, kQRows = kQParts * kMaxH;
 constexpr uint32_t Q_BYTES = kQRows * D;              // 12288: 2 boxes of [48 x 128 B]
 constexpr int kWParts = 3, kWRows = kWParts * kMaxH;
 constexpr uint32_t W_BYTES = kWRows * kTile;          // 6144: [48 x 128 slots]
-constexpr uint32_t OFF_Q = kNBuf * TILE_BYTES, OFF_W = OFF_Q + 2 * Q_BYTES, OFF_QS = OFF_W + 2 * W_BYTES;
 constexpr uint32_t RED_BYTES = 256;                   // of a group: [4 warps][8 heads], [4] scales
-constexpr uint32_t OFF_RED = OFF_QS + 2 * 64, OFF_MRG = OFF_RED + 2 * RED_BYTES;
-constexpr int kMrgParts = 64;                         // parts whose factors a merge holds at a time
-constexpr uint32_t OFF_BAR = OFF_MRG + 2 * (kMrgParts + 2) * 8 * 4;
+constexpr uint32_t STG_BYTES = 2 * D + 16;            // the new slot: key and value codes, their scales
+constexpr uint32_t OFF_Q = kNBuf * TILE_BYTES, OFF_W = OFF_Q + Q_BYTES, OFF_CS = OFF_W + 2 * W_BYTES;
+constexpr uint32_t IN_BYTES = (kMaxH + 2) * D * 2;     // a segment's queries, new key and value
+constexpr uint32_t OFF_IN = OFF_CS + D / 2 * 16, OFF_STG = OFF_IN + 2 * IN_BYTES;
+constexpr uint32_t OFF_QS = OFF_STG + 2 * STG_BYTES, OFF_RED = OFF_QS + 64, OFF_MRG = OFF_RED + 2 * RED_BYTES;
+constexpr uint32_t MRG_BYTES = kMaxCtas * kHg * 4;    // of a group: a factor per part and head
+constexpr uint32_t OFF_BAR = OFF_MRG + 2 * MRG_BYTES;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TM_S = 0, TM_O = 128, TMEM_COLS = 256;     // S: two buffers, 64 apart; O: two halves, 64 apart
@@ -289,10 +236,12 @@ constexpr float kAlpha = 4096.0f;                     // weights are held as alp
 struct DecArgs {
     int B, H, w;
     float scale_log2;
+    RopeBase base;
     const int* pos;
-    const float* scales;               // [B][2][w]
-    const float* qs;                   // [B][16], by head_row
-    unsigned* done;                    // [B][2 groups]
+    const __nv_bfloat16 *q, *k, *v;
+    uint8_t* codes;                    // [B][2][w][d]
+    float* scales;                     // [B][2][w]
+    unsigned* done;                    // [B][2 groups]: the segments of the row that have left their parts; 0 between calls
     float* part;                       // [B + CTAs][part_pitch]: m [16], sum [16] by head_row, O [H][d]
     __nv_bfloat16* out;
     DeviceStatus* status;
@@ -318,25 +267,24 @@ __device__ __forceinline__ int slots_of(const DecArgs& a, int b) {
     const int p = a.pos[b];
     return p < 0 ? 0 : min(p, a.w - 1) + 1;
 }
+// Tiles of all rows: batch * window <= 2^29, so at most 2^22 + 2^16, and 148 times that fits 32 bits.
 struct Walk {
-    long long pos, end, total, row_beg;  // on the line; row_beg: where the current row begins
-    int G, row;
+    unsigned pos, end, total, row_beg;   // on the line; row_beg: where the current row begins
+    unsigned G;
+    int row;
 };
 struct DecSeg {
     int b, t0, nt, n, c0, c1;            // row, its first tile here, tiles here, slots of the row, the row's CTAs
 };
-__device__ __forceinline__ int owner(long long x, long long total, int G) {
-    int c = (int)(x * G / total);
-    while (c + 1 < G && total * (c + 1) / G <= x) ++c;
-    while (c > 0 && total * c / G > x) --c;
-    return c;
-}
+// the CTA whose piece [total c / G, total (c + 1) / G) holds x: the last c with total c < (x + 1) G
+__device__ __forceinline__ int owner(unsigned x, unsigned total, unsigned G) { return (int)(((x + 1) * G - 1) / total); }
 __device__ __forceinline__ bool next_seg(const DecArgs& a, Walk& k, DecSeg& s) {
     if (k.pos >= k.end) return false;
-    int n, tiles;
+    int n;
+    unsigned tiles;
     for (;;) {                           // rows without tokens have no tiles
         n = slots_of(a, k.row);
-        tiles = (n + kTile - 1) / kTile;
+        tiles = (unsigned)(n + kTile - 1) / kTile;
         if (k.pos < k.row_beg + tiles) break;
         k.row_beg += tiles;
         if (++k.row >= a.B) return false;
@@ -345,18 +293,15 @@ __device__ __forceinline__ bool next_seg(const DecArgs& a, Walk& k, DecSeg& s) {
     s.n = n;
     s.t0 = (int)(k.pos - k.row_beg);
     s.nt = (int)(min(k.end, k.row_beg + tiles) - k.pos);
-    if (s.nt == tiles) {
-        s.c0 = s.c1 = blockIdx.x;
-    } else {
-        s.c0 = owner(k.row_beg, k.total, k.G);
-        s.c1 = owner(k.row_beg + tiles - 1, k.total, k.G);
-    }
+    const bool whole = s.nt == (int)tiles;
+    s.c0 = whole ? (int)blockIdx.x : owner(k.row_beg, k.total, k.G);
+    s.c1 = whole ? (int)blockIdx.x : owner(k.row_beg + tiles - 1, k.total, k.G);
     k.pos += s.nt;
     return true;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kv, const DecArgs a) {
+mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
@@ -366,11 +311,12 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     auto s_full = [&](uint32_t i) { return bars + 16 * kNBuf + 8 * i; };
     auto w_full = [&](uint32_t i) { return bars + 16 * kNBuf + 16 + 8 * i; };
     auto o_done = [&](uint32_t i) { return bars + 16 * kNBuf + 32 + 8 * i; };
-    const uint32_t o_free = bars + 16 * kNBuf + 48, mma_done = o_free + 8;
-    auto q_free = [&](uint32_t i) { return bars + 16 * kNBuf + 64 + 8 * i; };
-    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 16 * kNBuf + 80);
-    const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 16 * kNBuf + 96), a.status, a.timeout_ns};
-    long long* scan = reinterpret_cast<long long*>(smem);            // before the first load: per-warp sums
+    const uint32_t o_free = bars + 16 * kNBuf + 48, mma_done = o_free + 8, q_ready = o_free + 16;
+    auto in_full = [&](uint32_t i) { return bars + 16 * kNBuf + 72 + 8 * i; };
+    auto in_free = [&](uint32_t i) { return bars + 16 * kNBuf + 88 + 8 * i; };
+    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 16 * kNBuf + 104);
+    const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 16 * kNBuf + 112), a.status, a.timeout_ns};
+    unsigned* scan = reinterpret_cast<unsigned*>(smem);            // before the first load: per-warp sums
     Walk* walk_s = reinterpret_cast<Walk*>(smem + OFF_W);            // before the first weights
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -383,9 +329,11 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             mbar_init(s_full(i), 1);
             mbar_init(w_full(i), 8);
             mbar_init(o_done(i), 1);
-            mbar_init(q_free(i), 8);
+            mbar_init(in_full(i), 1);
+            mbar_init(in_free(i), 8);
         }
         mbar_init(o_free, 8);
+        mbar_init(q_ready, 8);
         mbar_init(mma_done, 1);
         *g.abort = 0;
         fence_barrier_init();
@@ -394,20 +342,22 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         tmem_alloc(smem_u32((const void*)tmem_s), TMEM_COLS);
         tmem_relinquish();
     }
+    pdl_launch();
+    pdl_wait();
     // this CTA's piece of the line of tiles: every thread counts the tiles of a run of rows
     {
         const int per = (a.B + kThreads - 1) / kThreads, r0 = min(a.B, (int)threadIdx.x * per), r1 = min(a.B, r0 + per);
-        long long mine = 0;
+        unsigned mine = 0;
         for (int b = r0; b < r1; ++b) mine += (slots_of(a, b) + kTile - 1) / kTile;
-        long long sum = mine;                                        // through this thread, in the warp
+        unsigned sum = mine;                                        // through this thread, in the warp
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, sum, o);
+            const unsigned u = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += u;
         }
         if (lane == 31) scan[warp] = sum;
         __syncthreads();
-        long long before = sum - mine, total = 0;
+        unsigned before = sum - mine, total = 0;
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) {
             if (i < warp) before += scan[i];
@@ -415,11 +365,11 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         }
         Walk k;
         k.total = total;
-        k.G = (int)min((long long)gridDim.x, total);
+        k.G = min(gridDim.x, total);
         k.pos = k.end = 0;
         k.row = 0;
         k.row_beg = 0;
-        const bool some = (int)blockIdx.x < k.G;
+        const bool some = blockIdx.x < k.G;
         if (some) {
             k.pos = total * blockIdx.x / k.G;
             k.end = total * (blockIdx.x + 1) / k.G;
@@ -441,43 +391,31 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     if (warp == kWarpTma) {
         if (lane == 0) {
             uint32_t L = 0, ns = 0;
-            bool ok = true, waited = false;
-            uint32_t q_bar = 0;                                      // a barrier that still expects the first queries
-            auto load_q = [&](uint32_t bar) {
-                for (int c = 0; c < 2; ++c)
-                    tma_load_2d(sb + OFF_Q + (ns & 1) * Q_BYTES + c * (Q_BYTES / 2), &map_q, c * 128, sg.b * kQRows, bar);
-                bulk_load(sb + OFF_QS + (ns & 1) * 64, a.qs + sg.b * kMaxH, 64, bar);
-            };
-            // the kernel before this one writes the queries and the new slots: what does not hold them is
-            // loaded before it is waited for
-            auto previous = [&]() {
-                if (waited) return;
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-                waited = true;
-                if (q_bar) load_q(q_bar);
-            };
+            bool ok = true;
             for (; ok && next_seg(a, k, sg); ++ns) {
-                const int slot = a.pos[sg.b] % a.w;
+                // the segment's inputs before its tiles, which would queue in front of them for microseconds
+                const uint32_t e = ns & 1, row_bytes = (uint32_t)a.H * D * 2, in = sb + OFF_IN + e * IN_BYTES;
+                if (ns > 1 && !(ok = wait(in_free(e), ((ns >> 1) - 1) & 1, g, 11))) break;
+                mbar_arrive_expect_tx(in_full(e), row_bytes + 2 * D * 2);
+                bulk_load(in, a.q + (size_t)sg.b * a.H * D, row_bytes, in_full(e));
+                bulk_load(in + kMaxH * D * 2, a.k + (size_t)sg.b * D, D * 2, in_full(e));
+                bulk_load(in + kMaxH * D * 2 + D * 2, a.v + (size_t)sg.b * D, D * 2, in_full(e));
                 for (int t = 0; ok && t < sg.nt; ++t)
                     for (int kv = 0; kv < 2; ++kv, ++L) {
                         const uint32_t s = L % kNBuf, u = L / kNBuf;
-                        const bool q = t == 0 && kv == 0;
-                        const int row = (sg.t0 + t) * kTile;
-                        if (u > 0 || (q && ns > 0) || (slot >= row && slot < row + kTile)) previous();
                         if (u > 0 && !(ok = wait(empty(s), (u - 1) & 1, g, 1))) break;
-                        if (q && ns > 1 && !(ok = wait(q_free(ns & 1), ((ns >> 1) - 1) & 1, g, 10))) break;
-                        mbar_arrive_expect_tx(full(s), TILE_BYTES + (q ? Q_BYTES + 64 : 0));
+                        mbar_arrive_expect_tx(full(s), TILE_BYTES);
                         for (int c = 0; c < 2; ++c)
-                            tma_load_2d(sb + s * TILE_BYTES + c * 16384, &map_kv, c * 128, (2 * sg.b + kv) * a.w + row, full(s));
-                        if (q) {
-                            if (waited) load_q(full(s)); else q_bar = full(s);
-                        }
+                            tma_load_2d(sb + s * TILE_BYTES + c * 16384, &map_kv, c * 128, (2 * sg.b + kv) * a.w + (sg.t0 + t) * kTile,
+                                        full(s));
                     }
-                previous();
             }
             const uint64_t t0 = globaltimer_ns();
             for (uint32_t l = L > kNBuf ? L - kNBuf : 0; l < L; ++l)
                 while (!mbar_try_wait(full(l % kNBuf), (l / kNBuf) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
+                }
+            for (uint32_t l = ns > 2 ? ns - 2 : 0; l < ns; ++l)
+                while (!mbar_try_wait(in_full(l & 1), (l >> 1) & 1) && globaltimer_ns() - t0 < a.timeout_ns) {
                 }
         }
     } else if (warp == kWarpMma) {
@@ -485,17 +423,29 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const uint32_t id_s = idesc_fp8(kQRows, 0, 0), id_o = idesc_fp8(kWRows, 1, 1);
         uint32_t gt = 0, ns = 0;
         bool ok = true;
+        // the new key's (half 0) or value's (1) codes over row `slot` of the tile in buffer s
+        auto put_new = [&](uint32_t s, int slot, int half) {
+            if (lane < 16) {
+                const uint4 c = *reinterpret_cast<const uint4*>(smem + OFF_STG + (ns & 1) * STG_BYTES + half * D + lane * 16);
+                *reinterpret_cast<uint4*>(smem + s * TILE_BYTES + (lane >> 3) * 16384 + slot * 128 + (((lane & 7) ^ (slot & 7)) << 4)) = c;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
         for (; ok && next_seg(a, k, sg); ++ns) {
+            if (!(ok = wait_w(q_ready, ns & 1, g, 10))) break;
+            const int slot = a.pos[sg.b] % a.w - sg.t0 * kTile;       // the new slot, from the segment's first
             for (int t = 0; ok && t <= sg.nt; ++t) {
                 if (t < sg.nt) {
                     const uint32_t i = gt + t, l = 2 * i, s = l % kNBuf, buf = i & 1;
                     if (!(ok = wait_w(full(s), (l / kNBuf) & 1, g, 2))) break;
+                    if (slot >= t * kTile && slot < (t + 1) * kTile) put_new(s, slot - t * kTile, 0);
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < D / 32; ++ks)
                             mma_fp8(tm + TM_S + buf * 64, desc_k_sw128(sb + s * TILE_BYTES + (ks >> 2) * 16384 + (ks & 3) * 32),
-                                     desc_k_sw128(sb + OFF_Q + (ns & 1) * Q_BYTES + (ks >> 2) * (Q_BYTES / 2) + (ks & 3) * 32), id_s,
+                                     desc_k_sw128(sb + OFF_Q + (ks >> 2) * (Q_BYTES / 2) + (ks & 3) * 32), id_s,
                                      ks > 0 ? 1u : 0u);
                         mma_commit(s_full(buf));
                         mma_commit(empty(s));
@@ -507,6 +457,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     if (t == 1 && ns > 0 && !(ok = wait_w(o_free, (ns - 1) & 1, g, 3))) break;
                     if (!(ok = wait_w(full(s), (l / kNBuf) & 1, g, 4))) break;
                     if (!(ok = wait_w(w_full(buf), (i >> 1) & 1, g, 5))) break;
+                    if (slot >= (t - 1) * kTile && slot < t * kTile) put_new(s, slot - (t - 1) * kTile, 1);
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
@@ -548,12 +499,105 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 : "memory");
             return o != 0;
         };
-        asm volatile("griddepcontrol.wait;" ::: "memory");           // the new slot's scales, the rows' counters
+        auto both_or = [&](bool v) {                                 // the OR of v over both groups
+            uint32_t o;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.u32 q, %1, 0;\n\t"
+                "barrier.red.or.pred p, 3, 256, q;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(o)
+                : "r"((uint32_t)v)
+                : "memory");
+            return o != 0;
+        };
+        // rows without a token
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+            if (a.pos[b] < 0)
+                for (int e = threadIdx.x; e < a.H * D / 8; e += 256)
+                    reinterpret_cast<uint4*>(a.out + (size_t)b * a.H * D)[e] = make_uint4(0, 0, 0, 0);
+        // a segment's queries, and its new slot if it holds it, into shared memory (and the ring)
+        auto begin = [&](const DecSeg& x, uint32_t n) {
+            double2* cs = reinterpret_cast<double2*>(smem + OFF_CS);
+            uint8_t* stg = smem + OFF_STG + (n & 1) * STG_BYTES;
+            const int p = a.pos[x.b], slot = p % a.w, wi = threadIdx.x >> 5;
+            const bool fresh = slot >= x.t0 * kTile && slot < (x.t0 + x.nt) * kTile;
+            if (threadIdx.x < D / 2) rope_cos_sin(a.base, threadIdx.x, (double)p, cs[threadIdx.x].x, cs[threadIdx.x].y);
+            const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(smem + OFF_IN + (n & 1) * IN_BYTES);
+            const bool here = wait_w(in_full(n & 1), (n >> 1) & 1, g, 12);
+            if (both_or(!here)) return false;             // the angles are there too
+            for (int i = wi; i < a.H + (fresh ? 2 : 0); i += 8) {
+                float y[8], z[8];
+                if (i >= a.H) {
+                    const int half = i - a.H;
+                    unpack(load_pairs(in + (kMaxH + half) * D, lane), z);
+                    double d[8];
+                    if (half) widen(z, d); else turn64(z, cs, lane, d);
+                    const SlotCodes c = quantise_slot(d);
+                    const size_t at = ((size_t)x.b * 2 + half) * a.w + slot;
+                    store_slot(c, lane, a.codes + at * D, a.scales + at);
+                    store_slot(c, lane, stg + half * D, reinterpret_cast<float*>(stg + 2 * D) + half);
+                    continue;
+                }
+                unpack(load_pairs(in + i * D, lane), z);
+                float mq = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float c = (float)cs[4 * lane + e].x, s = (float)cs[4 * lane + e].y;
+                    y[e] = z[e] * c - z[4 + e] * s;
+                    y[4 + e] = z[4 + e] * c + z[e] * s;
+                    mq = fmaxf(mq, fmaxf(fabsf(y[e]), fabsf(y[4 + e])));
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, o));
+                // mq / 448 rounded up to a power of two (at least 2^-100, so that its reciprocal is finite)
+                const float r448 = fminf(fmaxf(mq, 448.0f * 7.9e-31f), 3.0e38f) * (1.0f / 448.0f);
+                int e2 = (__float_as_int(r448) >> 23) - 127;
+                if (__float_as_int(r448) & 0x7fffff) ++e2;
+                const float up = __int_as_float((e2 + 127) << 23), down = __int_as_float((127 - e2) << 23);
+                if (lane == 0)                            // a query with an infinity: NaN
+                    reinterpret_cast<float*>(smem + OFF_QS)[head_row(i)] = mq < INFINITY ? up : __int_as_float(0x7fffffff);
+                uint32_t c[kQParts][2] = {};
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    float u = y[e] * down, v = y[e + 1] * down;
+#pragma unroll
+                    for (int part = 0; part < kQParts; ++part) {
+                        const uint32_t cc = e4m3x2(u, v);
+                        const float2 f = e4m3x2_values(cc);
+                        c[part][e >> 2] |= cc << (8 * (e & 2));
+                        u = (u - f.x) * 16.0f;
+                        v = (v - f.y) * 16.0f;
+                    }
+                }
+                // row part * 16 + head_row of the two [48 x 128 bytes] blocks, 16-byte chunks swizzled by the row
+#pragma unroll
+                for (int part = 0; part < kQParts; ++part) {
+                    const int row = part * kMaxH + head_row(i);
+                    uint8_t* dst = smem + OFF_Q + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
+                    *reinterpret_cast<uint32_t*>(dst) = c[part][0];
+                    *reinterpret_cast<uint32_t*>(dst + Q_BYTES / 2) = c[part][1];
+                }
+            }
+            fence_proxy_async_smem();
+            asm volatile("bar.sync 3, 256;" ::: "memory");            // the scales and codes are there for every warp
+            if (lane == 0) {
+                mbar_arrive(in_free(n & 1));
+                mbar_arrive(q_ready);
+            }
+            return true;
+        };
         uint32_t gt = 0, ns = 0;
         bool ok = true, stop = false;
-        for (; !stop && next_seg(a, k, sg); ++ns) {
+        DecSeg nx{};
+        bool more = next_seg(a, k, nx);
+        if (more && !begin(nx, 0)) more = false;
+        for (; more; ++ns) {
+            sg = nx;
             const float *sk = a.scales + (size_t)sg.b * 2 * a.w, *sv = sk + a.w;
-            const float* qs = reinterpret_cast<const float*>(smem + OFF_QS + (ns & 1) * 64) + grp * kHg;
+            const float* qs = reinterpret_cast<const float*>(smem + OFF_QS) + grp * kHg;
+            const float* fresh = reinterpret_cast<const float*>(smem + OFF_STG + (ns & 1) * STG_BYTES + 2 * D);
+            const int slot = a.pos[sg.b] % a.w;
             float m[kHg], l[kHg], vref = 0.f;
 #pragma unroll
             for (int h = 0; h < kHg; ++h) {
@@ -562,10 +606,11 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             }
             int x = sg.t0 * kTile + r;
             float k_next = x < sg.n ? sk[x] : 0.f, v_next = x < sg.n ? sv[x] : 0.f;
-            for (int t = 0; t < sg.nt; ++t) {
+            for (int t = 0; !stop && t < sg.nt; ++t) {
                 const uint32_t i = gt + t, buf = i & 1;
                 const bool valid = x < sg.n;
-                const float ks = k_next * a.scale_log2, vs = v_next;
+                const bool is_new = x == slot;            // the ring's own scale of it may be read before it is written
+                const float ks = (is_new ? fresh[0] : k_next) * a.scale_log2, vs = is_new ? fresh[1] : v_next;
                 x += kTile;                               // the next tile's scales while this one is worked on
                 k_next = x < sg.n ? sk[x] : 0.f;
                 v_next = x < sg.n ? sv[x] : 0.f;
@@ -684,8 +729,11 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive(w_full(buf));
             }
-            if (stop) break;
-            if (lane == 0) mbar_arrive(q_free(ns & 1));   // this segment's queries and their scales are done with
+            // the groups leave together (a failed wait of one of them): they meet in begin()
+            if (both_or(stop || !ok)) break;
+            // the next segment's queries, under this one's last products
+            more = next_seg(a, k, nx);
+            if (more && !begin(nx, ns + 1)) break;
             const uint32_t last = gt + sg.nt - 1;
             gt += sg.nt;
             // sums over the slots: lanes, then warps
@@ -696,7 +744,10 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 if (lane == 0) red[(warp & 3) * kHg + h] = l[h];
             }
             ok = ok && wait_w(o_done(last & 1), (last >> 1) & 1, g, 9);
-            if (grp_or(!ok)) break;
+            if (grp_or(!ok)) {
+                stop = true;
+                continue;
+            }
             tc_fence_after();
             float o[2][kHg];
 #pragma unroll
@@ -741,69 +792,56 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 }
             __threadfence();
             grp_or(false);
+            // how many of the row's segments were done before; the last one's increment wraps the counter to 0
             unsigned n = 0;
-            if (r == 0) n = atomicAdd(a.done + 2 * sg.b + grp, 1u);
+            if (r == 0) n = atomicInc(a.done + 2 * sg.b + grp, (unsigned)(sg.c1 - sg.c0));
             if (!grp_or(r == 0 && n == (unsigned)(sg.c1 - sg.c0))) continue;
-            // the last of the row's segments: their parts in order, kMrgParts at a time.  The factors
-            // 2^(m_c - max) / sum first (thread = part x head), then thread = 4 columns of a head
+            // the last of the row's segments adds up their parts in order, with factors 2^(m_c - max) / sum: thread =
+            // (head, every 16th part) for those, (4 columns, every other head) for the sums
             __threadfence();
             const float* p0 = a.part + (size_t)(sg.c0 + sg.b) * pitch;
             const int np = sg.c1 - sg.c0 + 1;
-            float* fac = reinterpret_cast<float*>(smem + OFF_MRG) + grp * (kMrgParts + 2) * 8;
-            float *mx_s = fac + kMrgParts * 8, *inv_s = mx_s + 8;
+            float* fac = reinterpret_cast<float*>(smem + OFF_MRG + grp * MRG_BYTES);
             {
-                const int h = r & 7, c0 = r >> 3;          // 16 parts side by side
+                const int h = r >> 4, at = grp * kHg + (h < nh ? h : 0);
                 float mx = -INFINITY, ls = 0.f;
-                if (h < nh)
-                    for (int c = c0; c < np; c += 16) {
-                        const float mc = __ldcg(p0 + (size_t)c * pitch + grp * kHg + h);
-                        const float lc = __ldcg(p0 + (size_t)c * pitch + kMaxH + grp * kHg + h);
-                        const float mn = fmaxf(mx, mc);
-                        ls = mx == -INFINITY ? lc : fmaf(ls, ex2_approx(mx - mn), lc * ex2_approx(mc - mn));
-                        mx = mn;
-                    }
-                fac[r] = mx;
-                fac[128 + r] = ls;
-                grp_or(false);
-                if (r < 8) {
-                    float mm = -INFINITY, s = 0.f;
-                    for (int c = 0; c < 16; ++c) mm = fmaxf(mm, fac[c * 8 + r]);
-                    for (int c = 0; c < 16; ++c)
-                        if (fac[c * 8 + r] != -INFINITY) s = fmaf(fac[128 + c * 8 + r], ex2_approx(fac[c * 8 + r] - mm), s);
-                    mx_s[r] = mm;
-                    inv_s[r] = 1.0f / s;
+                for (int c = r & 15; c < np; c += 16) {
+                    const float mc = __ldcg(p0 + (size_t)c * pitch + at), lc = __ldcg(p0 + (size_t)c * pitch + kMaxH + at);
+                    fac[c * kHg + h] = mc;
+                    const float mn = fmaxf(mx, mc);
+                    ls = mx == -INFINITY ? lc : fmaf(ls, ex2_approx(mx - mn), lc * ex2_approx(mc - mn));
+                    mx = mn;
                 }
-                grp_or(false);
-            }
-            float4 y[4] = {};                              // heads 2 j + (r >> 6) of the group, columns 4 (r & 63) ...
-            for (int cb = 0; cb < np; cb += kMrgParts) {
-                const int nc = min(kMrgParts, np - cb);
-                for (int e = r; e < nc * 8; e += 128)
-                    if ((e & 7) < nh)
-                        fac[e] = ex2_approx(__ldcg(p0 + (size_t)(cb + (e >> 3)) * pitch + grp * kHg + (e & 7)) - mx_s[e & 7]) * inv_s[e & 7];
-                grp_or(false);
-#pragma unroll 4
-                for (int c = 0; c < nc; ++c) {
-                    const float4* pc = reinterpret_cast<const float4*>(p0 + (size_t)(cb + c) * pitch + 2 * kMaxH) + (r & 63);
+                float all = mx;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int h = 2 * j + (r >> 6);
-                        if (h < nh) {
-                            const float4 z = __ldcg(pc + (2 * h + grp) * (D / 4));
-                            const float f = fac[c * 8 + h];
-                            y[j] = make_float4(fmaf(z.x, f, y[j].x), fmaf(z.y, f, y[j].y), fmaf(z.z, f, y[j].z), fmaf(z.w, f, y[j].w));
-                        }
-                    }
-                }
-                grp_or(false);
+                for (int o = 8; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+                ls = mx == -INFINITY ? 0.f : ls * ex2_approx(mx - all);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+                const float inv = 1.0f / ls;
+                for (int c = r & 15; c < np; c += 16) fac[c * kHg + h] = ex2_approx(fac[c * kHg + h] - all) * inv;
             }
+            grp_or(false);
+            float4 y[4] = {};                              // heads 2 j + (r >> 6) of the group, columns 4 (r & 63) ...
+            const float4* pc = reinterpret_cast<const float4*>(p0 + 2 * kMaxH) + (r & 63);
+            const int h0 = r >> 6;
+#pragma unroll 4
+            for (int c = 0; c < np && nh > 0; ++c, pc += pitch / 4)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int h = min(2 * j + h0, nh - 1);  // past the group's heads: loaded, not written
+                    const float4 z = __ldcg(pc + (2 * h + grp) * (D / 4));
+                    const float f = fac[c * kHg + h];
+                    y[j] = make_float4(fmaf(z.x, f, y[j].x), fmaf(z.y, f, y[j].y), fmaf(z.z, f, y[j].z), fmaf(z.w, f, y[j].w));
+                }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int h = 2 * j + (r >> 6);
+                const int h = 2 * j + h0;
                 if (h < nh)
                     reinterpret_cast<uint2*>(a.out + ((size_t)sg.b * a.H + 2 * h + grp) * D)[r & 63] =
                         make_uint2(bf16x2(y[j].x, y[j].y), bf16x2(y[j].z, y[j].w));
             }
+            grp_or(false);                                // the factors are read before the next use
         }
         tmem_wait_ld();
         tmem_wait_st();
@@ -817,17 +855,14 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 }
 
 struct DecLayout {
-    size_t done, qs, qp, part, total;
+    size_t done, part, total;
 };
-constexpr int kMaxCtas = 148;
 inline DecLayout dec_layout(const rglru_mqa_dims* d) {
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     const size_t B = (size_t)d->batch;
     DecLayout l{};
     size_t o = 256;                    // the status word
-    l.done = o; o = up(o + B * 8);
-    l.qs = o; o = up(o + B * kMaxH * 4);
-    l.qp = o; o = up(o + B * kQRows * D);
+    l.done = o; o = up(o + 65535 * 8);   // for any batch, so that calls of any dims find their counters at 0
     l.part = o; o = up(o + (B + kMaxCtas) * part_pitch(d->q_heads) * 4);
     l.total = o;
     return l;
@@ -854,11 +889,9 @@ cudaError_t launch_mqa_decode8(const rglru_mqa_dims* d, const void* q, const voi
     const DecLayout l = dec_layout(d);
     uint8_t* p = static_cast<uint8_t*>(ws);
     const int B = d->batch, w = d->window;
-    // the queries' parts as [B 48 rows][256 bytes] (box 128 x 48), the ring as [B 2 w slots][256 bytes] (box 128 x 128)
-    CUtensorMap mq, mkv;
-    if (!tc::make_map_2d_sw128_elem(&mq, p + l.qp, 1, D, (uint64_t)B * kQRows, D, 128, kQRows) ||
-        !tc::make_map_2d_sw128_elem(&mkv, codes, 1, D, (uint64_t)B * 2 * w, D, 128, kTile))
-        return cudaErrorInvalidValue;
+    // the ring as [B 2 w slots][256 bytes] (box 128 x 128)
+    CUtensorMap mkv;
+    if (!tc::make_map_2d_sw128_elem(&mkv, codes, 1, D, (uint64_t)B * 2 * w, D, 128, kTile)) return cudaErrorInvalidValue;
     cudaError_t e = set_smem_once(mqa_decode8_kernel, (int)SMEM_BYTES);
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
@@ -868,19 +901,17 @@ cudaError_t launch_mqa_decode8(const rglru_mqa_dims* d, const void* q, const voi
     a.B = B; a.H = d->q_heads; a.w = w;
     a.scale_log2 = d->scale * 1.4426950408889634f;
     a.pos = pos;
+    a.base = rope_base(d->rope_base);
+    a.q = static_cast<const __nv_bfloat16*>(q); a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.codes = static_cast<uint8_t*>(codes);
     a.scales = scales;
-    a.qs = reinterpret_cast<const float*>(p + l.qs);
     a.done = reinterpret_cast<unsigned*>(p + l.done);
     a.part = reinterpret_cast<float*>(p + l.part);
     a.out = static_cast<__nv_bfloat16*>(out);
     a.status = static_cast<DeviceStatus*>(ws);
     a.timeout_ns = 1000000000ull;
-    mqa_decode8_turn_kernel<<<B, 256, 0, s>>>(
-        d->q_heads, w, rope_base(d->rope_base), pos, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-        static_cast<const __nv_bfloat16*>(v), p + l.qp, reinterpret_cast<float*>(p + l.qs), a.done, static_cast<uint8_t*>(codes),
-        scales, a.out);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // the attention's launch, set-up and first tiles overlap the kernel before it
+    // launched behind the kernel before it on the stream, its set-up under that kernel's end
     const long long tiles = (long long)B * ((w + kTile - 1) / kTile);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -892,7 +923,7 @@ cudaError_t launch_mqa_decode8(const rglru_mqa_dims* d, const void* q, const voi
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mqa_decode8_kernel, mq, mkv, a);
+    return cudaLaunchKernelEx(&cfg, mqa_decode8_kernel, mkv, a);
 }
 
 cudaError_t launch_mqa_cache8_read(const rglru_mqa_dims* d, const void* codes, const float* scales, const int* pos,
