@@ -360,31 +360,33 @@ def mqa_decode(dims: MqaDims, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     _check(rc, "rglru_mqa_decode")
 
 
-def _expect(where: str, *wanted):
-    """wanted: (name, tensor or None, shape, dtypes).  The C ABI sees addresses only, so a tensor of another
-    shape, type or device than the dims say is refused here."""
-    device = None
-    for name, t, shape, dtypes in wanted:
-        if t is None:
-            continue
-        if not t.is_cuda or (device is not None and t.device != device):
-            raise ValueError(f"{where}: {name} must be a CUDA tensor on the same device as the others, got {t.device}")
-        device = t.device
-        if t.dtype not in dtypes:
-            raise ValueError(f"{where}: {name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if device is not None and device.index != torch.cuda.current_device():
-        raise ValueError(f"{where}: the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-
-
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 _CODES, _BYTES = (torch.float8_e4m3fn, torch.uint8), (torch.uint8,)
 
 
-def _expect_buffer(where: str, name: str, t: torch.Tensor, like: torch.Tensor):
-    if not t.is_cuda or t.device != like.device or t.dtype != torch.uint8:
-        raise ValueError(f"{where}: {name} must be a uint8 CUDA tensor on {like.device}")
+def _addresses(where: str, *wanted):
+    """wanted: (name, tensor or None, shape or None, dtypes) -> the tensors' addresses (None for none).  The C ABI sees
+    addresses only, so a tensor of another shape, type or device than the dims say is refused here."""
+    device, out = None, []
+    for name, t, shape, dtypes in wanted:
+        if t is None:
+            out.append(None)
+            continue
+        if not t.is_cuda or (device is not None and t.get_device() != device):
+            raise ValueError(f"{where}: {name} must be a CUDA tensor on the same device as the others, got {t.device}")
+        if device is None:
+            device = t.get_device()
+            if device != torch._C._cuda_getDevice():
+                raise ValueError(f"{where}: {name} is on {t.device}, the current device is "
+                                 f"cuda:{torch._C._cuda_getDevice()}")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{where}: {name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{where}: {name} must have shape {shape}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+        out.append(t.data_ptr())
+    return out
 
 
 def mqa_save_size(dims: MqaDims) -> int:
@@ -402,13 +404,14 @@ def mqa_forward(dims: MqaDims, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     (mqa_save_size bytes) keeps what mqa_backward needs."""
     B, T, H, d = dims.batch, dims.seq_len, dims.q_heads, dims.head_dim
     where = "rglru_mqa_forward"
-    _expect(where, ("q", q, (B, T, H, d), _BF16), ("k", k, (B, T, d), _BF16), ("v", v, (B, T, d), _BF16),
-            ("out", out, (B, T, H, d), _BF16), ("reset", reset, (B, T), _BYTES))
-    _expect_buffer(where, "save", save, q)
-    _expect_buffer(where, "workspace", workspace, q)
-    rc = load().rglru_mqa_forward(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(reset), int(pos0), _ptr(out),
-                                  _ptr(save), save.numel(), _ptr(workspace), workspace.numel(), _stream(stream))
-    _check(rc, where)
+    q_, k_, v_, out_, reset_, save_, ws_ = _addresses(
+        where, ("q", q, (B, T, H, d), _BF16), ("k", k, (B, T, d), _BF16), ("v", v, (B, T, d), _BF16),
+        ("out", out, (B, T, H, d), _BF16), ("reset", reset, (B, T), _BYTES), ("save", save, None, _BYTES),
+        ("workspace", workspace, None, _BYTES))
+    rc = load().rglru_mqa_forward(ctypes.byref(dims), q_, k_, v_, reset_, int(pos0), out_, save_, save.numel(), ws_,
+                                  workspace.numel(), _stream(stream))
+    if rc:
+        _check(rc, where)
 
 
 def mqa_backward(dims: MqaDims, v: torch.Tensor, out: torch.Tensor, dout: torch.Tensor, save: torch.Tensor,
@@ -416,13 +419,14 @@ def mqa_backward(dims: MqaDims, v: torch.Tensor, out: torch.Tensor, dout: torch.
     """rglru_mqa_backward: out, dout [B, T, H, d], v [B, T, d] -> dq [B, T, H, d], dk, dv [B, T, d]."""
     B, T, H, d = dims.batch, dims.seq_len, dims.q_heads, dims.head_dim
     where = "rglru_mqa_backward"
-    _expect(where, ("v", v, (B, T, d), _BF16), ("out", out, (B, T, H, d), _BF16), ("dout", dout, (B, T, H, d), _BF16),
-            ("dq", dq, (B, T, H, d), _BF16), ("dk", dk, (B, T, d), _BF16), ("dv", dv, (B, T, d), _BF16))
-    _expect_buffer(where, "save", save, v)
-    _expect_buffer(where, "workspace", workspace, v)
-    rc = load().rglru_mqa_backward(ctypes.byref(dims), _ptr(v), _ptr(out), _ptr(dout), _ptr(save), save.numel(),
-                                   _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(), _stream(stream))
-    _check(rc, where)
+    v_, out_, dout_, dq_, dk_, dv_, save_, ws_ = _addresses(
+        where, ("v", v, (B, T, d), _BF16), ("out", out, (B, T, H, d), _BF16), ("dout", dout, (B, T, H, d), _BF16),
+        ("dq", dq, (B, T, H, d), _BF16), ("dk", dk, (B, T, d), _BF16), ("dv", dv, (B, T, d), _BF16),
+        ("save", save, None, _BYTES), ("workspace", workspace, None, _BYTES))
+    rc = load().rglru_mqa_backward(ctypes.byref(dims), v_, out_, dout_, save_, save.numel(), dq_, dk_, dv_, ws_,
+                                   workspace.numel(), _stream(stream))
+    if rc:
+        _check(rc, where)
 
 
 def mqa_cache8_write(dims: MqaDims, k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
@@ -431,11 +435,12 @@ def mqa_cache8_write(dims: MqaDims, k: torch.Tensor, v: torch.Tensor, codes: tor
     its bytes), scales [B, 2, w] fp32."""
     B, T, w, d = dims.batch, dims.seq_len, dims.window, dims.head_dim
     where = "rglru_mqa_cache8_write"
-    _expect(where, ("k", k, (B, T, d), _BF16), ("v", v, (B, T, d), _BF16), ("codes", codes, (B, 2, w, d), _CODES),
-            ("scales", scales, (B, 2, w), _F32), ("lengths", lengths, (B,), _I32))
-    rc = load().rglru_mqa_cache8_write(ctypes.byref(dims), _ptr(k), _ptr(v), _ptr(lengths), int(pos0), _ptr(codes),
-                                       _ptr(scales), _stream(stream))
-    _check(rc, where)
+    k_, v_, codes_, scales_, lengths_ = _addresses(
+        where, ("k", k, (B, T, d), _BF16), ("v", v, (B, T, d), _BF16), ("codes", codes, (B, 2, w, d), _CODES),
+        ("scales", scales, (B, 2, w), _F32), ("lengths", lengths, (B,), _I32))
+    rc = load().rglru_mqa_cache8_write(ctypes.byref(dims), k_, v_, lengths_, int(pos0), codes_, scales_, _stream(stream))
+    if rc:
+        _check(rc, where)
 
 
 def mqa_decode8_workspace_size(dims: MqaDims) -> int:
@@ -448,12 +453,14 @@ def mqa_decode8(dims: MqaDims, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     [B, 2, w, d], scales [B, 2, w]) receives the new slot."""
     B, H, w, d = dims.batch, dims.q_heads, dims.window, dims.head_dim
     where = "rglru_mqa_decode8"
-    _expect(where, ("q", q, (B, H, d), _BF16), ("k", k, (B, d), _BF16), ("v", v, (B, d), _BF16), ("pos", pos, (B,), _I32),
-            ("codes", codes, (B, 2, w, d), _CODES), ("scales", scales, (B, 2, w), _F32), ("out", out, (B, H, d), _BF16))
-    _expect_buffer(where, "workspace", workspace, q)
-    rc = load().rglru_mqa_decode8(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(pos), _ptr(codes), _ptr(scales),
-                                  _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
-    _check(rc, where)
+    q_, k_, v_, pos_, codes_, scales_, out_, ws_ = _addresses(
+        where, ("q", q, (B, H, d), _BF16), ("k", k, (B, d), _BF16), ("v", v, (B, d), _BF16), ("pos", pos, (B,), _I32),
+        ("codes", codes, (B, 2, w, d), _CODES), ("scales", scales, (B, 2, w), _F32), ("out", out, (B, H, d), _BF16),
+        ("workspace", workspace, None, _BYTES))
+    rc = load().rglru_mqa_decode8(ctypes.byref(dims), q_, k_, v_, pos_, codes_, scales_, out_, ws_, workspace.numel(),
+                                  _stream(stream))
+    if rc:
+        _check(rc, where)
 
 
 def mqa_cache8_read(dims: MqaDims, codes: torch.Tensor, scales: torch.Tensor, cache: torch.Tensor,
@@ -461,11 +468,12 @@ def mqa_cache8_read(dims: MqaDims, codes: torch.Tensor, scales: torch.Tensor, ca
     """rglru_mqa_cache8_read: the 8-bit ring as the bf16 ring cache [B, 2, w, d]; pos [B] int32 or None."""
     B, w, d = dims.batch, dims.window, dims.head_dim
     where = "rglru_mqa_cache8_read"
-    _expect(where, ("codes", codes, (B, 2, w, d), _CODES), ("scales", scales, (B, 2, w), _F32),
-            ("cache", cache, (B, 2, w, d), _BF16), ("pos", pos, (B,), _I32))
-    rc = load().rglru_mqa_cache8_read(ctypes.byref(dims), _ptr(codes), _ptr(scales), _ptr(pos), _ptr(cache),
-                                      _stream(stream))
-    _check(rc, where)
+    codes_, scales_, cache_, pos_ = _addresses(
+        where, ("codes", codes, (B, 2, w, d), _CODES), ("scales", scales, (B, 2, w), _F32),
+        ("cache", cache, (B, 2, w, d), _BF16), ("pos", pos, (B,), _I32))
+    rc = load().rglru_mqa_cache8_read(ctypes.byref(dims), codes_, scales_, pos_, cache_, _stream(stream))
+    if rc:
+        _check(rc, where)
 
 
 def backward_workspace_size(dims: Dims) -> int:

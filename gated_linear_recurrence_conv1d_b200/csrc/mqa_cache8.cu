@@ -32,9 +32,10 @@ using namespace pr;
 constexpr int D = 256;
 constexpr int kMaxH = 16;
 constexpr int kTile = 128;             // slots per tile (the MMA's M)
-constexpr int kHg = kMaxH / 2;         // heads of a group of warps
-// rows of the queries' and weights' operands, columns of S and O: the even heads, then the odd ones
-__host__ __device__ constexpr int head_row(int h) { return (h & 1) * kHg + (h >> 1); }
+constexpr int kGroups = 4;             // groups of 4 warps: group g has the heads h = g mod 4
+constexpr int kHg = kMaxH / kGroups;
+// rows of the queries' and weights' operands, columns of S and O: the heads of group 0, then those of group 1, ...
+__host__ __device__ constexpr int head_row(int h) { return (h % kGroups) * kHg + h / kGroups; }
 constexpr double kFloor = 448.0 * 1.1754943508222875e-38;
 
 // ---- e4m3 ------------------------------------------------------------------------------------------
@@ -188,20 +189,21 @@ __global__ void __launch_bounds__(256) mqa_cache8_read_kernel(long long slots, i
 }
 
 // ---------------------------------------------------------------- decode: attention --------------------
-// One kernel.  The slots of a row are cut into tiles of 128 and the tiles of all rows laid out as one line, of which every
+// The slots of a row are cut into tiles of 128 and the tiles of all rows laid out as one line, of which every
 // CTA takes an equal piece (a "segment" is a piece of one row): the rings' bytes are spread evenly
 // over the SMs whatever the rows' lengths.  Per tile
 //   S^T = K Qp^T   (M 128 slots, N 48 = 16 heads x 3 parts, K 256; e4m3, fp32 sums)
 //   O^T += V^T Wp^T (M 128 columns twice, N 48 = 16 heads x 3 parts, K 128 slots)
-// straight from the codes in shared memory (V^T is the value tile read MN-major).  Two groups of 4 warps, one for
-// the even and one for the odd heads, thread = slot: s = (S0 + S1 / 16 + S2 / 256) 2^e c scale_k, p = 2^(s - m) with a reference maximum m per head that moves
+// straight from the codes in shared memory (V^T is the value tile read MN-major).  Four groups of 4 warps, each
+// with every fourth head, thread = slot: s = (S0 + S1 / 16 + S2 / 256) 2^e c scale_k, p = 2^(s - m) with a reference maximum m per head that moves
 // when a score passes it by more than 8 times, and the weight p scale_v, normalised by a power of two
 // vref >= the value scales seen so far, as three e5m2 parts: off by at most 2^-9 of itself, half of what bf16
 // would leave, down to weights of 2^-29 (e4m3 parts end at 2^-16, which shows where one slot has nearly all
 // the weight and a small value).  p adds to the thread's own sum in fp32.  O stays in TMEM for the whole segment; when m or vref
-// moves it is rescaled there (each group has its own vref and its own columns of S, W and O, so the groups
-// never meet).  A row inside one segment is written at once; else the segments leave (m, sum, O) and the
-// one that finishes last adds them up in order.
+// moves it is rescaled there (each group has its own vref and its own columns of S, W and O, so within a
+// segment the groups never meet).  A row inside one segment is written at once; else the segments leave (m, sum, O) and
+// mqa_decode8_merge_kernel adds them up in order.  (The segment that finishes last doing that here, by a counter of the
+// row, took longer at the end of the kernel, and its registers spilled the softmax's.)
 // At the beginning of a segment (the first tiles are on their way meanwhile, and after the first segment the last
 // products of the segment before run) the softmax warps rotate the row's queries and write their parts as the B
 // operand: with 2^e the power of two that brings the head's largest element into (224, 448],
@@ -218,18 +220,18 @@ constexpr int kQParts = 3, kQRows = kQParts * kMaxH;
 constexpr uint32_t Q_BYTES = kQRows * D;              // 12288: 2 boxes of [48 x 128 B]
 constexpr int kWParts = 3, kWRows = kWParts * kMaxH;
 constexpr uint32_t W_BYTES = kWRows * kTile;          // 6144: [48 x 128 slots]
-constexpr uint32_t RED_BYTES = 256;                   // of a group: [4 warps][8 heads], [4] scales
+constexpr uint32_t RED_BYTES = 128;                   // of a group: [4 warps][kHg], [4] scales, [kHg] maxima
 constexpr uint32_t STG_BYTES = 2 * D + 16;            // the new slot: key and value codes, their scales
 constexpr uint32_t OFF_Q = kNBuf * TILE_BYTES, OFF_W = OFF_Q + Q_BYTES, OFF_CS = OFF_W + 2 * W_BYTES;
 constexpr uint32_t IN_BYTES = (kMaxH + 2) * D * 2;     // a segment's queries, new key and value
 constexpr uint32_t OFF_IN = OFF_CS + D / 2 * 16, OFF_STG = OFF_IN + 2 * IN_BYTES;
-constexpr uint32_t OFF_QS = OFF_STG + 2 * STG_BYTES, OFF_RED = OFF_QS + 64, OFF_MRG = OFF_RED + 2 * RED_BYTES;
-constexpr uint32_t MRG_BYTES = kMaxCtas * kHg * 4;    // of a group: a factor per part and head
-constexpr uint32_t OFF_BAR = OFF_MRG + 2 * MRG_BYTES;
+constexpr uint32_t OFF_QS = OFF_STG + 2 * STG_BYTES, OFF_RED = OFF_QS + 64;
+constexpr uint32_t OFF_BAR = OFF_RED + kGroups * RED_BYTES;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TM_S = 0, TM_O = 128, TMEM_COLS = 256;     // S: two buffers, 64 apart; O: two halves, 64 apart
-constexpr int kThreads = 320, kWarpTma = 8, kWarpMma = 9;
+constexpr int kSoftWarps = 4 * kGroups, kSoft = 32 * kSoftWarps, kWarpTma = kSoftWarps, kWarpMma = kSoftWarps + 1;
+constexpr int kThreads = kSoft + 64;
 
 constexpr float kAlpha = 4096.0f;                     // weights are held as alpha p: p <= 8 keeps them below 57344
 
@@ -241,7 +243,7 @@ struct DecArgs {
     const __nv_bfloat16 *q, *k, *v;
     uint8_t* codes;                    // [B][2][w][d]
     float* scales;                     // [B][2][w]
-    unsigned* done;                    // [B][2 groups]: the segments of the row that have left their parts; 0 between calls
+    int2* meta;                        // [B] the first and the last CTA of a row
     float* part;                       // [B + CTAs][part_pitch]: m [16], sum [16] by head_row, O [H][d]
     __nv_bfloat16* out;
     DeviceStatus* status;
@@ -327,13 +329,13 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 1);
-            mbar_init(w_full(i), 8);
+            mbar_init(w_full(i), kSoftWarps);
             mbar_init(o_done(i), 1);
             mbar_init(in_full(i), 1);
-            mbar_init(in_free(i), 8);
+            mbar_init(in_free(i), kSoftWarps);
         }
-        mbar_init(o_free, 8);
-        mbar_init(q_ready, 8);
+        mbar_init(o_free, kSoftWarps);
+        mbar_init(q_ready, kSoftWarps);
         mbar_init(mma_done, 1);
         *g.abort = 0;
         fence_barrier_init();
@@ -484,7 +486,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
         __syncwarp();
     } else {
         const int grp = warp >> 2, r = threadIdx.x & 127;            // group; slot of a tile, then column
-        const int nh = (a.H + 1 - grp) >> 1;                         // this group's heads: 2 i + grp, i < nh
+        const int nh = (a.H + kGroups - 1 - grp) / kGroups;          // this group's heads: kGroups i + grp, i < nh
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + grp * kHg;
         float* red = reinterpret_cast<float*>(smem + OFF_RED + grp * RED_BYTES);
         auto grp_or = [&](bool v) {                                  // the OR of v over the group's 128 threads
@@ -504,18 +506,13 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
             asm volatile(
                 "{\n\t.reg .pred p, q;\n\t"
                 "setp.ne.u32 q, %1, 0;\n\t"
-                "barrier.red.or.pred p, 3, 256, q;\n\t"
+                "barrier.red.or.pred p, 5, 512, q;\n\t"
                 "selp.u32 %0, 1, 0, p;\n\t}"
                 : "=r"(o)
                 : "r"((uint32_t)v)
                 : "memory");
             return o != 0;
         };
-        // rows without a token
-        for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-            if (a.pos[b] < 0)
-                for (int e = threadIdx.x; e < a.H * D / 8; e += 256)
-                    reinterpret_cast<uint4*>(a.out + (size_t)b * a.H * D)[e] = make_uint4(0, 0, 0, 0);
         // a segment's queries, and its new slot if it holds it, into shared memory (and the ring)
         auto begin = [&](const DecSeg& x, uint32_t n) {
             double2* cs = reinterpret_cast<double2*>(smem + OFF_CS);
@@ -526,7 +523,8 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
             const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(smem + OFF_IN + (n & 1) * IN_BYTES);
             const bool here = wait_w(in_full(n & 1), (n >> 1) & 1, g, 12);
             if (both_or(!here)) return false;             // the angles are there too
-            for (int i = wi; i < a.H + (fresh ? 2 : 0); i += 8) {
+#pragma unroll 1
+            for (int i = wi; i < a.H + (fresh ? 2 : 0); i += kSoftWarps) {
                 float y[8], z[8];
                 if (i >= a.H) {
                     const int half = i - a.H;
@@ -580,25 +578,78 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 }
             }
             fence_proxy_async_smem();
-            asm volatile("bar.sync 3, 256;" ::: "memory");            // the scales and codes are there for every warp
+            asm volatile("bar.sync 5, 512;" ::: "memory");            // the scales and codes are there for every warp
             if (lane == 0) {
                 mbar_arrive(in_free(n & 1));
                 mbar_arrive(q_ready);
             }
             return true;
         };
+        float vref = 0.f;
+        // a segment's output, its last tile number `last`: the row's, or a part of it
+        auto finish = [&](const DecSeg& x, uint32_t last) {
+            if (grp_or(!wait_w(o_done(last & 1), (last >> 1) & 1, g, 9))) return false;
+            tc_fence_after();
+            float o[2][kHg], l[kHg];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                float y1[kHg], y2[kHg];
+                tmem_ld4(tl + TM_O + hh * 64, o[hh]);
+                tmem_ld4(tl + TM_O + hh * 64 + 16, y1);
+                tmem_ld4(tl + TM_O + hh * 64 + 32, y2);
+                tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < kHg; ++h)
+                    o[hh][h] = fmaf(y2[h], 1.0f / 64.0f, fmaf(y1[h], 1.0f / 8.0f, o[hh][h])) * (vref * (1.0f / kAlpha));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+#pragma unroll
+            for (int h = 0; h < kHg; ++h) l[h] = (red[h] + red[kHg + h]) + (red[2 * kHg + h] + red[3 * kHg + h]);
+            if (x.t0 == 0 && r == 0 && grp == 0) a.meta[x.b] = make_int2(x.c0, x.c1);
+            if (x.c0 == x.c1) {
+#pragma unroll
+                for (int h = 0; h < kHg; ++h)
+                    if (h < nh) {
+                        const float inv = 1.0f / l[h];
+                        __nv_bfloat16* row = a.out + ((size_t)x.b * a.H + kGroups * h + grp) * D + r;
+                        row[0] = __float2bfloat16_rn(o[0][h] * inv);
+                        row[128] = __float2bfloat16_rn(o[1][h] * inv);
+                    }
+                grp_or(false);                            // red is read before the next use
+                return true;
+            }
+            const int pitch = part_pitch(a.H);
+            float* part = a.part + (size_t)(blockIdx.x + x.b) * pitch;
+#pragma unroll
+            for (int h = 0; h < kHg; ++h)
+                if (h < nh) {
+                    part[2 * kMaxH + (kGroups * h + grp) * D + r] = o[0][h];
+                    part[2 * kMaxH + (kGroups * h + grp) * D + 128 + r] = o[1][h];
+                    if (r == 0) {
+                        part[grp * kHg + h] = red[5 * kHg + h];
+                        part[kMaxH + grp * kHg + h] = l[h];
+                    }
+                }
+            grp_or(false);                                // red is read before the next use
+            return true;
+        };
         uint32_t gt = 0, ns = 0;
         bool ok = true, stop = false;
         DecSeg nx{};
-        bool more = next_seg(a, k, nx);
-        if (more && !begin(nx, 0)) more = false;
-        for (; more; ++ns) {
+        for (;; ++ns) {
+            const bool more = next_seg(a, k, nx);
+            if (more && !begin(nx, ns)) break;
+            if (ns > 0 && !finish(sg, gt - 1)) stop = true;   // the segment before, under this one's first products
+            if (!more) break;
             sg = nx;
             const float *sk = a.scales + (size_t)sg.b * 2 * a.w, *sv = sk + a.w;
             const float* qs = reinterpret_cast<const float*>(smem + OFF_QS) + grp * kHg;
             const float* fresh = reinterpret_cast<const float*>(smem + OFF_STG + (ns & 1) * STG_BYTES + 2 * D);
             const int slot = a.pos[sg.b] % a.w;
-            float m[kHg], l[kHg], vref = 0.f;
+            float m[kHg], l[kHg];
+            vref = 0.f;
 #pragma unroll
             for (int h = 0; h < kHg; ++h) {
                 m[h] = -INFINITY;
@@ -606,6 +657,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
             }
             int x = sg.t0 * kTile + r;
             float k_next = x < sg.n ? sk[x] : 0.f, v_next = x < sg.n ? sv[x] : 0.f;
+#pragma unroll 1
             for (int t = 0; !stop && t < sg.nt; ++t) {
                 const uint32_t i = gt + t, buf = i & 1;
                 const bool valid = x < sg.n;
@@ -630,9 +682,9 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 bool move = vs > vref;
                 {
                     float s1[kHg], s2[kHg];
-                    tmem_ld8(tl + TM_S + buf * 64, s);
-                    tmem_ld8(tl + TM_S + buf * 64 + 16, s1);
-                    tmem_ld8(tl + TM_S + buf * 64 + 32, s2);
+                    tmem_ld4(tl + TM_S + buf * 64, s);
+                    tmem_ld4(tl + TM_S + buf * 64 + 16, s1);
+                    tmem_ld4(tl + TM_S + buf * 64 + 32, s2);
                     tmem_wait_ld();
 #pragma unroll
                     for (int h = 0; h < kHg; ++h) {
@@ -688,11 +740,11 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                         for (int c = 0; c < 2 * kWParts; ++c) {
                             const uint32_t col = tl + TM_O + (c / kWParts) * 64 + (c % kWParts) * 16;
                             float o[kHg];
-                            tmem_ld8(col, o);
+                            tmem_ld4(col, o);
                             tmem_wait_ld();
 #pragma unroll
                             for (int h = 0; h < kHg; ++h) o[h] *= f[h];
-                            tmem_st8f(col, o);
+                            tmem_st4f(col, o);
                         }
                         tmem_wait_st();
                     }
@@ -701,7 +753,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 // weights: row part * 16 + head row, byte = slot, in 128-byte rows swizzled by the row
                 uint8_t* wb = smem + OFF_W + buf * W_BYTES + grp * (kHg * kTile) + (r & 15);
                 const float wv = fmaf(vs, kAlpha / vref, vs - vs);    // a scale that is not finite: NaN
-                const uint32_t ch = (uint32_t)(r >> 4);
+                const uint32_t ch = (uint32_t)(r >> 4) ^ (uint32_t)(grp * kHg & 7);   // swizzled by the row, grp * kHg + h
 #pragma unroll
                 for (int h = 0; h < kHg; h += 2) {
                     uint32_t c[kWParts] = {};
@@ -729,119 +781,17 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(w_full(buf));
             }
-            // the groups leave together (a failed wait of one of them): they meet in begin()
-            if (both_or(stop || !ok)) break;
-            // the next segment's queries, under this one's last products
-            more = next_seg(a, k, nx);
-            if (more && !begin(nx, ns + 1)) break;
-            const uint32_t last = gt + sg.nt - 1;
             gt += sg.nt;
-            // sums over the slots: lanes, then warps
+            // sums over the slots: lanes, then (in finish) warps
 #pragma unroll
             for (int h = 0; h < kHg; ++h) {
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
                 if (lane == 0) red[(warp & 3) * kHg + h] = l[h];
+                if (r == 0) red[5 * kHg + h] = m[h];
             }
-            ok = ok && wait_w(o_done(last & 1), (last >> 1) & 1, g, 9);
-            if (grp_or(!ok)) {
-                stop = true;
-                continue;
-            }
-            tc_fence_after();
-            float o[2][kHg];
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                float y1[kHg], y2[kHg];
-                tmem_ld8(tl + TM_O + hh * 64, o[hh]);
-                tmem_ld8(tl + TM_O + hh * 64 + 16, y1);
-                tmem_ld8(tl + TM_O + hh * 64 + 32, y2);
-                tmem_wait_ld();
-#pragma unroll
-                for (int h = 0; h < kHg; ++h)
-                    o[hh][h] = fmaf(y2[h], 1.0f / 64.0f, fmaf(y1[h], 1.0f / 8.0f, o[hh][h])) * (vref * (1.0f / kAlpha));
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(o_free);
-#pragma unroll
-            for (int h = 0; h < kHg; ++h) l[h] = (red[h] + red[kHg + h]) + (red[2 * kHg + h] + red[3 * kHg + h]);
-            if (sg.c0 == sg.c1) {
-#pragma unroll
-                for (int h = 0; h < kHg; ++h)
-                    if (h < nh) {
-                        const float inv = 1.0f / l[h];
-                        __nv_bfloat16* y = a.out + ((size_t)sg.b * a.H + 2 * h + grp) * D + r;
-                        y[0] = __float2bfloat16_rn(o[0][h] * inv);
-                        y[128] = __float2bfloat16_rn(o[1][h] * inv);
-                    }
-                grp_or(false);                            // red is read before the next use
-                continue;
-            }
-            const int pitch = part_pitch(a.H);
-            float* part = a.part + (size_t)(blockIdx.x + sg.b) * pitch;
-#pragma unroll
-            for (int h = 0; h < kHg; ++h)
-                if (h < nh) {
-                    part[2 * kMaxH + (2 * h + grp) * D + r] = o[0][h];
-                    part[2 * kMaxH + (2 * h + grp) * D + 128 + r] = o[1][h];
-                    if (r == 0) {
-                        part[grp * kHg + h] = m[h];
-                        part[kMaxH + grp * kHg + h] = l[h];
-                    }
-                }
-            __threadfence();
-            grp_or(false);
-            // how many of the row's segments were done before; the last one's increment wraps the counter to 0
-            unsigned n = 0;
-            if (r == 0) n = atomicInc(a.done + 2 * sg.b + grp, (unsigned)(sg.c1 - sg.c0));
-            if (!grp_or(r == 0 && n == (unsigned)(sg.c1 - sg.c0))) continue;
-            // the last of the row's segments adds up their parts in order, with factors 2^(m_c - max) / sum: thread =
-            // (head, every 16th part) for those, (4 columns, every other head) for the sums
-            __threadfence();
-            const float* p0 = a.part + (size_t)(sg.c0 + sg.b) * pitch;
-            const int np = sg.c1 - sg.c0 + 1;
-            float* fac = reinterpret_cast<float*>(smem + OFF_MRG + grp * MRG_BYTES);
-            {
-                const int h = r >> 4, at = grp * kHg + (h < nh ? h : 0);
-                float mx = -INFINITY, ls = 0.f;
-                for (int c = r & 15; c < np; c += 16) {
-                    const float mc = __ldcg(p0 + (size_t)c * pitch + at), lc = __ldcg(p0 + (size_t)c * pitch + kMaxH + at);
-                    fac[c * kHg + h] = mc;
-                    const float mn = fmaxf(mx, mc);
-                    ls = mx == -INFINITY ? lc : fmaf(ls, ex2_approx(mx - mn), lc * ex2_approx(mc - mn));
-                    mx = mn;
-                }
-                float all = mx;
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-                ls = mx == -INFINITY ? 0.f : ls * ex2_approx(mx - all);
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-                const float inv = 1.0f / ls;
-                for (int c = r & 15; c < np; c += 16) fac[c * kHg + h] = ex2_approx(fac[c * kHg + h] - all) * inv;
-            }
-            grp_or(false);
-            float4 y[4] = {};                              // heads 2 j + (r >> 6) of the group, columns 4 (r & 63) ...
-            const float4* pc = reinterpret_cast<const float4*>(p0 + 2 * kMaxH) + (r & 63);
-            const int h0 = r >> 6;
-#pragma unroll 4
-            for (int c = 0; c < np && nh > 0; ++c, pc += pitch / 4)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int h = min(2 * j + h0, nh - 1);  // past the group's heads: loaded, not written
-                    const float4 z = __ldcg(pc + (2 * h + grp) * (D / 4));
-                    const float f = fac[c * kHg + h];
-                    y[j] = make_float4(fmaf(z.x, f, y[j].x), fmaf(z.y, f, y[j].y), fmaf(z.z, f, y[j].z), fmaf(z.w, f, y[j].w));
-                }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int h = 2 * j + h0;
-                if (h < nh)
-                    reinterpret_cast<uint2*>(a.out + ((size_t)sg.b * a.H + 2 * h + grp) * D)[r & 63] =
-                        make_uint2(bf16x2(y[j].x, y[j].y), bf16x2(y[j].z, y[j].w));
-            }
-            grp_or(false);                                // the factors are read before the next use
+            // the groups leave together (a failed wait of one of them): they meet in begin()
+            if (both_or(stop || !ok)) break;
         }
         tmem_wait_ld();
         tmem_wait_st();
@@ -854,15 +804,68 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
     }
 }
 
+// The rows of several segments from their parts, in order: block = (head, row), thread = 4 columns.  A row without a token
+// is zero.
+constexpr int kMergeLoads = 8;         // parts in flight
+__global__ void __launch_bounds__(D / 4, 12) mqa_decode8_merge_kernel(int H, const int* pos, const int2* meta, const float* part,
+                                                                  __nv_bfloat16* out) {
+    pdl_launch();
+    pdl_wait();
+    const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x, pitch = part_pitch(H);
+    uint2* row = reinterpret_cast<uint2*>(out + ((size_t)b * H + h) * D) + t;
+    const int p = pos[b];
+    const int2 c = meta[b];            // not written for a row without a token
+    if (p < 0) {
+        *row = make_uint2(0, 0);
+        return;
+    }
+    if (c.x == c.y) return;
+    const float* p0 = part + (size_t)(c.x + b) * pitch;
+    const int np = c.y - c.x + 1;
+    float mx = -INFINITY, l = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int c0 = 0; c0 < np; c0 += kMergeLoads) {
+        float m[kMergeLoads], s[kMergeLoads];
+        float4 z[kMergeLoads];
+#pragma unroll
+        for (int i = 0; i < kMergeLoads; ++i) {
+            m[i] = -INFINITY;
+            if (c0 + i < np) {
+                const float* pc = p0 + (size_t)(c0 + i) * pitch;
+                m[i] = pc[head_row(h)];
+                s[i] = pc[kMaxH + head_row(h)];
+                z[i] = reinterpret_cast<const float4*>(pc + 2 * kMaxH + h * D)[t];
+            }
+        }
+        float mn = mx;
+#pragma unroll
+        for (int i = 0; i < kMergeLoads; ++i) mn = fmaxf(mn, m[i]);
+        const float old = mx == -INFINITY ? 0.f : ex2_approx(mx - mn);
+        l *= old;
+        y = make_float4(y.x * old, y.y * old, y.z * old, y.w * old);
+#pragma unroll
+        for (int i = 0; i < kMergeLoads; ++i)
+            if (c0 + i < np) {
+                const float f = ex2_approx(m[i] - mn);
+                l = fmaf(s[i], f, l);
+                y = make_float4(fmaf(z[i].x, f, y.x), fmaf(z[i].y, f, y.y), fmaf(z[i].z, f, y.z), fmaf(z[i].w, f, y.w));
+            }
+        mx = mn;
+    }
+    const float inv = 1.0f / l;
+    *row = make_uint2(bf16x2(y.x * inv, y.y * inv), bf16x2(y.z * inv, y.w * inv));
+}
+
 struct DecLayout {
-    size_t done, part, total;
+    size_t meta, part, total;
 };
 inline DecLayout dec_layout(const rglru_mqa_dims* d) {
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     const size_t B = (size_t)d->batch;
     DecLayout l{};
     size_t o = 256;                    // the status word
-    l.done = o; o = up(o + 65535 * 8);   // for any batch, so that calls of any dims find their counters at 0
+    l.meta = o; o = up(o + B * sizeof(int2));
     l.part = o; o = up(o + (B + kMaxCtas) * part_pitch(d->q_heads) * 4);
     l.total = o;
     return l;
@@ -906,12 +909,12 @@ cudaError_t launch_mqa_decode8(const rglru_mqa_dims* d, const void* q, const voi
     a.v = static_cast<const __nv_bfloat16*>(v);
     a.codes = static_cast<uint8_t*>(codes);
     a.scales = scales;
-    a.done = reinterpret_cast<unsigned*>(p + l.done);
+    a.meta = reinterpret_cast<int2*>(p + l.meta);
     a.part = reinterpret_cast<float*>(p + l.part);
     a.out = static_cast<__nv_bfloat16*>(out);
     a.status = static_cast<DeviceStatus*>(ws);
     a.timeout_ns = 1000000000ull;
-    // launched behind the kernel before it on the stream, its set-up under that kernel's end
+    // both launched behind the kernel before them on the stream, their set-up under that kernel's end
     const long long tiles = (long long)B * ((w + kTile - 1) / kTile);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -923,7 +926,12 @@ cudaError_t launch_mqa_decode8(const rglru_mqa_dims* d, const void* q, const voi
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mqa_decode8_kernel, mkv, a);
+    if ((e = cudaLaunchKernelEx(&cfg, mqa_decode8_kernel, mkv, a)) != cudaSuccess) return e;
+    cfg.gridDim = dim3(d->q_heads, B);
+    cfg.blockDim = dim3(D / 4);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, mqa_decode8_merge_kernel, d->q_heads, pos, static_cast<const int2*>(a.meta),
+                              static_cast<const float*>(a.part), a.out);
 }
 
 cudaError_t launch_mqa_cache8_read(const rglru_mqa_dims* d, const void* codes, const float* scales, const int* pos,

@@ -314,9 +314,7 @@ RGLRU_API rglru_status rglru_mqa_cache8_write(const rglru_mqa_dims* dims, const 
 /* One decode token per row against the 8-bit ring: as rglru_mqa_decode, with the new key and value
  * quantised into slot pos[b] mod w before the token attends to the ring's values (its own
  * among them).  pos[b] < 0 marks a row without a token: its out is zero, its ring untouched.  Slots
- * past a ring that is not full yet may hold anything.  The workspace: zeroed by the caller before its
- * first use, and again after a TIMEOUT; it holds counters that are zero between calls
- * (of any dims), so nothing else is to write it in between. */
+ * past a ring that is not full yet may hold anything. */
 RGLRU_API size_t rglru_mqa_decode8_workspace_size(const rglru_mqa_dims* dims);
 RGLRU_API rglru_status rglru_mqa_decode8(const rglru_mqa_dims* dims, const void* q, const void* k, const void* v,
                                          const int* pos, void* codes, float* scales, void* out, void* workspace,
