@@ -495,19 +495,21 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             bar_or(false, kSoft);                         // xch is read before its next use
             tc_fence_after();
             const float inv = 1.0f / l;
-            __nv_bfloat16* orow = a.out + ((size_t)p_b * a.TH + p_row) * D + half * 128;
+            const int row0 = p_row & ~3;                  // the quad's rows, of which this lane writes 16 bytes each
+            __nv_bfloat16* dst = a.out + ((size_t)p_b * a.TH + row0) * D + half * 128 + 8 * (lane & 3);
 #pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
                 float o[32];
+                uint32_t e[16];
                 tmem_ld32(tl + TM_O + half * 128 + c, o);
                 tmem_wait_ld();
-                if (p_row < a.TH) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        reinterpret_cast<uint4*>(orow + c)[e] =
-                            make_uint4(bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                       bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-                }
+                for (int i = 0; i < 16; ++i) e[i] = bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+                quad_transpose(e);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (row0 + i < a.TH)
+                        *reinterpret_cast<uint4*>(dst + (size_t)i * D + c) = make_uint4(e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]);
             }
             if (half == 0 && p_row < a.TH) a.lse[(size_t)p_b * a.THp + p_row] = p_m + log2f(l);
             tc_fence_before();
@@ -687,8 +689,8 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
-    pdl_launch();
     pdl_wait();
+    pdl_launch();                                        // mqa_dkv_kernel may run beside this one: delta is complete
 
     // Number i of the pair's key tiles uses each of the three buffers for the i-th time.
     if (warp == kWarpTma) {
@@ -839,33 +841,39 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         auto finish = [&](int kp) {
             if (!wait_w(dq_done, kp & 1, g, 12)) return false;
             tc_fence_after();
-            // turn back: columns [64 half, +64) and their partners 128 further
-            __nv_bfloat16* orow = a.dq + ((size_t)p_b * a.TH + p_row) * D + half * 64;
+            // turn back: columns [64 half, +64) and their partners 128 further; stores as in the forward
+            const int row0 = p_row & ~3;
+            __nv_bfloat16* dst = a.dq + ((size_t)p_b * a.TH + row0) * D + half * 64 + 8 * (lane & 3);
             const float4* cs = reinterpret_cast<const float4*>(a.cs + (size_t)(min(p_row, a.TH - 1) / a.H) * (D / 2) + half * 64);
 #pragma unroll 1
-            for (int c = 0; c < 64; c += 16) {
-                float x1[16], x2[16];
-                float4 fs[8];
+            for (int c = 0; c < 64; c += 32) {
+                uint32_t o1[16], o2[16];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) fs[e] = cs[c / 2 + e];   // (cos, sin) of two pairs
-                tmem_ld16(tl + TM_DQ + half * 64 + c, x1);
-                tmem_ld16(tl + TM_DQ + 128 + half * 64 + c, x2);
-                tmem_wait_ld();
-                if (p_row < a.TH) {
-                    uint32_t o1[8], o2[8];
+                for (int g16 = 0; g16 < 2; ++g16) {
+                    float x1[16], x2[16];
+                    float4 fs[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) fs[e] = cs[c / 2 + 8 * g16 + e];   // (cos, sin) of two pairs
+                    tmem_ld16(tl + TM_DQ + half * 64 + c + 16 * g16, x1);
+                    tmem_ld16(tl + TM_DQ + 128 + half * 64 + c + 16 * g16, x2);
+                    tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float4 f = fs[e];
                         const float y0 = x1[2 * e] * a.scale, y1 = x1[2 * e + 1] * a.scale;
                         const float z0 = x2[2 * e] * a.scale, z1 = x2[2 * e + 1] * a.scale;
-                        o1[e] = bf16x2(y0 * f.x + z0 * f.y, y1 * f.z + z1 * f.w);
-                        o2[e] = bf16x2(z0 * f.x - y0 * f.y, z1 * f.z - y1 * f.w);
+                        o1[8 * g16 + e] = bf16x2(y0 * f.x + z0 * f.y, y1 * f.z + z1 * f.w);
+                        o2[8 * g16 + e] = bf16x2(z0 * f.x - y0 * f.y, z1 * f.z - y1 * f.w);
                     }
-                    reinterpret_cast<uint4*>(orow + c)[0] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-                    reinterpret_cast<uint4*>(orow + c)[1] = make_uint4(o1[4], o1[5], o1[6], o1[7]);
-                    reinterpret_cast<uint4*>(orow + 128 + c)[0] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
-                    reinterpret_cast<uint4*>(orow + 128 + c)[1] = make_uint4(o2[4], o2[5], o2[6], o2[7]);
                 }
+                quad_transpose(o1);
+                quad_transpose(o2);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (row0 + i < a.TH) {
+                        *reinterpret_cast<uint4*>(dst + (size_t)i * D + c) = make_uint4(o1[4 * i], o1[4 * i + 1], o1[4 * i + 2], o1[4 * i + 3]);
+                        *reinterpret_cast<uint4*>(dst + (size_t)i * D + 128 + c) = make_uint4(o2[4 * i], o2[4 * i + 1], o2[4 * i + 2], o2[4 * i + 3]);
+                    }
             }
             tc_fence_before();
             __syncwarp();
@@ -1063,7 +1071,6 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
     pdl_launch();
-    pdl_wait();
     Segs segs(a, cl, G);
     Seg sg{};
 
@@ -1293,6 +1300,9 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         tmem_wait_ld();
         tmem_wait_st();
     }
+    // the kernel before, mqa_dq_kernel, let this one start when all that this one reads was there; the kernel behind it
+    // has to find that one complete too
+    pdl_wait();
     tc_fence_before();
     __syncthreads();
     cluster_sync();

@@ -163,6 +163,24 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// Four lanes with 64 bytes of a row each (four 16-byte pieces e[4 k ..]) hand them round so that lane j has piece j of the
+// four rows (row i of the quad in e[4 i ..]): a store of a warp then writes 8 rows of 64 bytes, not 32 of 16.
+__device__ __forceinline__ void quad_transpose(uint32_t (&e)[16]) {
+#pragma unroll
+    for (int step = 1; step < 4; step *= 2) {
+        const bool up = threadIdx.x & step;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k & step) continue;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                uint32_t &lo = e[4 * k + w], &hi = e[4 * (k + step) + w];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, step);
+                if (up) lo = got; else hi = got;
+            }
+        }
+    }
+}
 // 32 lanes x 32 bits, 4 consecutive columns per thread
 __device__ __forceinline__ void tmem_st4f(uint32_t taddr, const float (&v)[4]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "f"(v[0]), "f"(v[1]),
