@@ -90,11 +90,31 @@ __device__ __forceinline__ SlotCodes quantise_slot(const double (&x)[8]) {
     for (int e = 0; e < 8; ++e) m = max(m, __double_as_longlong(fabs(x[e])));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float s = (float)(__longlong_as_double(max(m, __double_as_longlong(kFloor))) / 448.0);
-    const double r = 1.0 / (double)s;
+    // Products with reciprocals off by 2^-52 instead of fp64 divisions, which took half of the fp64 pipe's time: rounded to
+    // fp32 they are the quotients unless those are within 2^-51 of the middle of two fp32 numbers.  1 / s from its
+    // fp32 value by two Newton steps (2^-22, 2^-44, 2^-52; s is at least 2^-126, so its reciprocal is finite).
+    const float s = (float)(__longlong_as_double(max(m, __double_as_longlong(kFloor))) * (1.0 / 448.0));
+    const double ds = (double)s;
+    double r = (double)__frcp_rn(s);
+    r = fma(r, fma(-ds, r, 1.0), r);
+    r = fma(r, fma(-ds, r, 1.0), r);
     float q[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) q[e] = (float)(x[e] * r);
+    return SlotCodes{e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16, e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16, s};
+}
+// The same from fp32 (a value: nothing to rotate).  Rounding the quotients of bf16 numbers once to fp32 gives what rounding
+// them to fp64 first gives: x / s with 8 bits over 24 is never within 2^-54 of the middle of two fp32 numbers.
+__device__ __forceinline__ SlotCodes quantise_slot(const float (&x)[8]) {
+    int m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_int(fabsf(x[e])));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float s = __fdiv_rn(__int_as_float(max(m, __float_as_int((float)kFloor))), 448.0f);
+    float q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = __fdiv_rn(x[e], s);
     return SlotCodes{e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16, e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16, s};
 }
 __device__ __forceinline__ void store_slot(const SlotCodes& c, int lane, uint8_t* codes, float* scale) {
@@ -110,17 +130,12 @@ __device__ __forceinline__ void turn64(const float (&x)[8], const double2* cs, i
         y[4 + e] = (double)x[4 + e] * a.x + (double)x[e] * a.y;
     }
 }
-__device__ __forceinline__ void widen(const float (&x)[8], double (&y)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = (double)x[e];
-}
-
 // ---------------------------------------------------------------- write -------------------------------
 // Block = (token, up to kWriteRows batch rows): the angles of the token's position once for all of them (they are
 // half of the arithmetic), while the rows' keys and values are on their way; a warp per row.  The last min(len, w)
 // tokens of a row go into their slots.
 constexpr int kWriteRows = 8;
-__global__ void __launch_bounds__(32 * kWriteRows) mqa_cache8_write_kernel(int B, int T, int w, int pos0, RopeBase base,
+__global__ void __launch_bounds__(32 * kWriteRows, 6) mqa_cache8_write_kernel(int B, int T, int w, int pos0, RopeBase base,
                                                                            const int* lengths, const __nv_bfloat16* k,
                                                                            const __nv_bfloat16* v, uint8_t* codes, float* scales) {
     __shared__ double2 cs[D / 2];
@@ -148,43 +163,45 @@ __global__ void __launch_bounds__(32 * kWriteRows) mqa_cache8_write_kernel(int B
     turn64(x, cs, lane, y);
     store_slot(quantise_slot(y), lane, codes + s * D, scales + s);
     unpack(pv, x);
-    widen(x, y);
-    store_slot(quantise_slot(y), lane, codes + (s + w) * D, scales + s + w);
+    store_slot(quantise_slot(x), lane, codes + (s + w) * D, scales + s + w);
 }
 
 // ---------------------------------------------------------------- read ---------------------------------
-// 16 lanes a slot, 16 codes each, kReadSlots slots a half warp, their loads in flight together: bound by HBM
-constexpr int kReadSlots = 4, kReadBlock = 16 * kReadSlots;          // slots of a block of 256 threads
+// A warp takes kReadSlots slots, a lane 8 codes of each, their loads in flight together: bound by HBM
+constexpr int kReadSlots = 8, kReadBlock = 8 * kReadSlots;           // slots of a block of 8 warps
 __global__ void __launch_bounds__(256) mqa_cache8_read_kernel(long long slots, int w, const int* pos,
                                                               const uint8_t* codes, const float* scales,
                                                               __nv_bfloat16* cache) {
-    const long long s0 = (long long)blockIdx.x * kReadBlock + (threadIdx.x >> 4);
-    const int c = threadIdx.x & 15;
-    uint4 u[kReadSlots];
+    const long long s0 = (long long)blockIdx.x * kReadBlock + (threadIdx.x >> 5) * kReadSlots;
+    const int lane = threadIdx.x & 31;
+    unsigned half = (unsigned)s0 / (unsigned)w;          // 2 row + (key, value); 2 B w < 2^31
+    int slot = (int)((unsigned)s0 - half * (unsigned)w);
+    uint2 u[kReadSlots];
     float f[kReadSlots];
     bool have[kReadSlots];
 #pragma unroll
     for (int i = 0; i < kReadSlots; ++i) {
-        const long long s = s0 + 16 * i;
-        have[i] = s < slots && (!pos || s % w <= pos[s / (2 * (long long)w)]);
+        const long long s = s0 + i;
+        have[i] = s < slots && (!pos || slot <= pos[half >> 1]);
+        if (++slot == w) {
+            slot = 0;
+            ++half;
+        }
         if (have[i]) {
-            u[i] = reinterpret_cast<const uint4*>(codes + s * D)[c];
+            u[i] = __ldcs(reinterpret_cast<const uint2*>(codes + s * D) + lane);
             f[i] = scales[s];
         }
     }
 #pragma unroll
     for (int i = 0; i < kReadSlots; ++i) {
         if (!have[i]) continue;
-        const uint32_t q[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-        uint32_t o[8];
+        uint32_t o[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 x = e4m3x2_values((q[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+        for (int e = 0; e < 4; ++e) {
+            const float2 x = e4m3x2_values(((e < 2 ? u[i].x : u[i].y) >> (16 * (e & 1))) & 0xffffu);
             o[e] = bf16x2(f[i] * x.x, f[i] * x.y);
         }
-        uint4* dst = reinterpret_cast<uint4*>(cache + (s0 + 16 * i) * D) + 2 * c;
-        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        __stcs(reinterpret_cast<uint4*>(cache + (s0 + i) * D) + lane, make_uint4(o[0], o[1], o[2], o[3]));
     }
 }
 
@@ -529,9 +546,14 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 if (i >= a.H) {
                     const int half = i - a.H;
                     unpack(load_pairs(in + (kMaxH + half) * D, lane), z);
-                    double d[8];
-                    if (half) widen(z, d); else turn64(z, cs, lane, d);
-                    const SlotCodes c = quantise_slot(d);
+                    SlotCodes c;
+                    if (half) {
+                        c = quantise_slot(z);
+                    } else {
+                        double d[8];
+                        turn64(z, cs, lane, d);
+                        c = quantise_slot(d);
+                    }
                     const size_t at = ((size_t)x.b * 2 + half) * a.w + slot;
                     store_slot(c, lane, a.codes + at * D, a.scales + at);
                     store_slot(c, lane, stg + half * D, reinterpret_cast<float*>(stg + 2 * D) + half);
