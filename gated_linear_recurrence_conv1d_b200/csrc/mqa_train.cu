@@ -228,6 +228,7 @@ struct Args {
     const int* lo;              // [B, T]
     const float2* cs;           // [T, d/2]
     float* lse;                 // [B, THp], log2 domain
+    int8_t* low;                // [B, T, H, d]: the bits of out below its bf16, 8 of them
     float* delta;               // [B, THp]
     const long long* cum;       // [B nkt + 1]: 64-row tiles before each key tile
     float* part;                // partial dk, dv of (cluster, key tile)
@@ -279,14 +280,27 @@ struct QTiles {
 // Each CTA loads half of every K tile (64 keys) and of every V tile (128 of its columns), so a key tile costs
 // an SM 64 KB for 2048 tensor cycles: half of what a CTA alone would pull from L2.  8 softmax warps, thread =
 // (row, 64 of the 128 keys): P = 2^(c s - m) with a reference maximum m that moves only when a score
-// passes it by 2^8 (then O and the sum are rescaled; the two threads of a row meet for that only).  P is
-// rounded to bf16 for the MMA; the sum adds the fp32 values.  The S of the next tile runs under the
-// softmax of this one.
+// passes it by 2^8 (then O and the sums are rescaled; the two threads of a row meet for that only).  P is rounded to
+// bf16 for the MMA, and O is divided by the sum of the rounded weights; L takes the sum of the fp32 ones.  The S
+// of the next tile runs under the softmax of this one.
+// Beside out the forward keeps the next 8 bits of each of its elements for delta = dO . out.  Where one key holds nearly
+// all of a row's weight, dP of that key and delta cancel: dS is what the small weights leave of the difference,
+// and a delta from out in bf16, or from weights that do not sum to one, was off by more than dS itself (documents
+// of 2 tokens: dq off by 0.5 to 30 %, now by 0.3 %).  The bytes cost HBM time of 1.3 KB a row instead of 1.
 namespace fw {
+// Two fp32 values rounded to bf16 (to nearest, ties away from zero, so that bit 15 of the value alone says whether
+// it was rounded up), and bits 8 to 15 of four: as a signed byte, what to add to the rounded value's bits
+__device__ __forceinline__ uint32_t bf16x2_away(float a, float b) {
+    return __byte_perm(__float_as_uint(a) + 0x8000u, __float_as_uint(b) + 0x8000u, 0x7632);
+}
+__device__ __forceinline__ uint32_t low_bytes(const float* x) {
+    return __byte_perm(__byte_perm(__float_as_uint(x[0]), __float_as_uint(x[1]), 0x0051),
+                       __byte_perm(__float_as_uint(x[2]), __float_as_uint(x[3]), 0x0051), 0x5410);
+}
 constexpr int BK = 128;
 constexpr uint32_t SLOT = 32768;
 constexpr int NSLOT = 5;
-constexpr uint32_t OFF_Q = 0, OFF_SLOT = 65536, OFF_X = OFF_SLOT + NSLOT * SLOT, OFF_BAR = OFF_X + 1024;
+constexpr uint32_t OFF_Q = 0, OFF_SLOT = 65536, OFF_X = OFF_SLOT + NSLOT * SLOT, OFF_BAR = OFF_X + 1536;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TM_O = 0, TM_S = 256;
@@ -485,31 +499,47 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         // next query tile and the next: the tensor pipe has that P and two S ahead of it meanwhile
         bool pending = false;
         int p_b = 0, p_row = 0;
-        float p_m = 0.f, p_l = 0.f;
+        float p_m = 0.f, p_l = 0.f, p_w = 0.f;
         auto finish = [&](uint32_t last) {
             ok = ok && wait_w(o_done(last & 1), (last >> 1) & 1, g, 10);
             bar_or(false, kSoft);                         // xch has been read
-            xch[half * 128 + r] = p_l;
+            xch[half * 128 + r] = p_w;
+            if (half == 1) xch[256 + r] = p_l;
             if (bar_or(!ok, kSoft)) return false;
-            const float l = xch[r] + xch[128 + r];        // the row's sum from its two threads
+            const float w = xch[r] + xch[128 + r], l = p_l + xch[256 + r];       // the row's sums (l: of half 0)
             bar_or(false, kSoft);                         // xch is read before its next use
             tc_fence_after();
-            const float inv = 1.0f / l;
+            const float inv = 1.0f / w;
             const int row0 = p_row & ~3;                  // the quad's rows, of which this lane writes 16 bytes each
-            __nv_bfloat16* dst = a.out + ((size_t)p_b * a.TH + row0) * D + half * 128 + 8 * (lane & 3);
+            const size_t at = ((size_t)p_b * a.TH + row0) * D + half * 128;
+            __nv_bfloat16* dst = a.out + at + 8 * (lane & 3);
+            int8_t* low = a.low + at + 16 * (lane & 3);
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                float o[32];
-                uint32_t e[16];
-                tmem_ld32(tl + TM_O + half * 128 + c, o);
-                tmem_wait_ld();
+            for (int c = 0; c < 128; c += 64) {
+                uint32_t lb[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) e[i] = bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
-                quad_transpose(e);
+                for (int h = 0; h < 64; h += 32) {
+                    float o[32];
+                    uint32_t e[16];
+                    tmem_ld32(tl + TM_O + half * 128 + c + h, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] *= inv;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) e[i] = bf16x2_away(o[2 * i], o[2 * i + 1]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) lb[h / 4 + i] = low_bytes(o + 4 * i);
+                    quad_transpose(e);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (row0 + i < a.TH)
+                            *reinterpret_cast<uint4*>(dst + (size_t)i * D + c + h) = make_uint4(e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]);
+                }
+                quad_transpose(lb);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (row0 + i < a.TH)
-                        *reinterpret_cast<uint4*>(dst + (size_t)i * D + c) = make_uint4(e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]);
+                        *reinterpret_cast<uint4*>(low + (size_t)i * D + c) = make_uint4(lb[4 * i], lb[4 * i + 1], lb[4 * i + 2], lb[4 * i + 3]);
             }
             if (half == 0 && p_row < a.TH) a.lse[(size_t)p_b * a.THp + p_row] = p_m + log2f(l);
             tc_fence_before();
@@ -525,7 +555,7 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             const int lo_row = a.lo[(size_t)t.b * a.T + tok];
             // a tile inside every row's keys needs no mask: [lo of the CTA's last token, its first token]
             const int full_lo = a.lo[(size_t)t.b * a.T + min(row0 + 127, a.TH - 1) / a.H], full_hi = min(row0, a.TH - 1) / a.H;
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, wsum = 0.f;    // sums of the weights, and of the weights as rounded for P V
             for (int j = 0; j < q.n; ++j) {
                 const uint32_t i = gt + j, buf = i & 1;
                 ok = ok && wait_w(s_full(buf), (i >> 1) & 1, g, 8);
@@ -559,6 +589,7 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     const float f = move && m != -INFINITY ? ex2_approx(m - mx) : 1.0f;
                     if (move) m = mx;
                     l *= f;
+                    wsum *= f;
                     if (j > 0) {
                         ok = wait_w(o_done((i - 1) & 1), ((i - 1) >> 1) & 1, g, 9);
                         tc_fence_after();
@@ -577,16 +608,18 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 }
                 const float nm = m == -INFINITY ? 0.f : -m;
                 uint32_t p[32];
-                float l0 = 0.f, l1 = 0.f;
+                const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(nm, nm);
+                float2 l2 = make_float2(0.f, 0.f), w2 = l2;
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
-                    const float p0 = ex2_approx(fmaf(s[2 * c], a.scale_log2, nm));
-                    const float p1 = ex2_approx(fmaf(s[2 * c + 1], a.scale_log2, nm));
-                    l0 += p0;
-                    l1 += p1;
-                    p[c] = bf16x2(p0, p1);
+                    const float2 x = fma2(make_float2(s[2 * c], s[2 * c + 1]), sc2, nm2);
+                    const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                    l2 = add2(l2, e);
+                    p[c] = bf16x2(e.x, e.y);
+                    w2 = add2(w2, make_float2(__uint_as_float(p[c] << 16), __uint_as_float(p[c] & 0xffff0000u)));
                 }
-                l += l0 + l1;
+                l += l2.x + l2.y;
+                wsum += w2.x + w2.y;
                 tmem_st32(tl + TM_S + buf * BK + half * 64, p);
                 tmem_wait_st();
                 tc_fence_before();
@@ -603,6 +636,7 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             p_row = row;
             p_m = m;
             p_l = l;
+            p_w = wsum;
             gt += q.n;
         }
         if (!stop && pending) finish(gt - 1);
@@ -1353,19 +1387,25 @@ __global__ void __launch_bounds__(256) mqa_dkv_sum_kernel(const Args a, int G) {
 }
 
 // ---------------------------------------------------------------- backward: delta ------------------------
-// delta = dO . out per query row (a warp takes kDeltaRows rows, their loads in flight together: bound by HBM)
+// delta = dO . out per query row (a warp takes kDeltaRows rows, their loads in flight together: bound by HBM), of out in
+// the 16 bits of significand that the forward kept of it
 constexpr int kDeltaRows = 4, kDeltaWarps = 8;
+__device__ __forceinline__ float with_low(uint32_t hi, uint32_t byte) {
+    return __uint_as_float(hi + (uint32_t)((int)(byte << 24) >> 16));
+}
 __global__ void __launch_bounds__(32 * kDeltaWarps) mqa_delta_kernel(const Args a, const __nv_bfloat16* dout) {
     pdl_launch();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long row0 = ((long long)blockIdx.x * kDeltaWarps + warp) * kDeltaRows, rows = (long long)a.B * a.TH;
     uint4 x[kDeltaRows], y[kDeltaRows];
+    uint2 w[kDeltaRows];
 #pragma unroll
     for (int i = 0; i < kDeltaRows; ++i) {
         if (row0 + i >= rows) break;
         x[i] = reinterpret_cast<const uint4*>(dout + (row0 + i) * D)[lane];
         y[i] = reinterpret_cast<const uint4*>(a.out + (row0 + i) * D)[lane];
+        w[i] = reinterpret_cast<const uint2*>(a.low + (row0 + i) * D)[lane];
     }
 #pragma unroll
     for (int i = 0; i < kDeltaRows; ++i) {
@@ -1375,8 +1415,9 @@ __global__ void __launch_bounds__(32 * kDeltaWarps) mqa_delta_kernel(const Args 
         float s = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
-            s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
+            const uint32_t two = (e < 2 ? w[i].x : w[i].y) >> (16 * (e & 1));
+            s = fmaf(__uint_as_float(xs[e] << 16), with_low(ys[e] << 16, two), s);
+            s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), with_low(ys[e] & 0xffff0000u, two >> 8), s);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -1384,9 +1425,10 @@ __global__ void __launch_bounds__(32 * kDeltaWarps) mqa_delta_kernel(const Args 
     }
 }
 
-// What the forward keeps: lse, first keys and last queries, the backward's line, angles, the rotated queries and keys.
+// What the forward keeps: lse, first keys and last queries, the backward's line, angles, the rotated queries and keys, the
+// low bytes of out.
 struct SaveLayout {
-    size_t lse, lo, last, cum, cs, q_rot, k_rot, total;
+    size_t lse, lo, last, cum, cs, q_rot, k_rot, low, total;
 };
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 inline size_t row_pitch(const rglru_mqa_dims* d) { return ((size_t)d->seq_len * d->q_heads + 63) & ~size_t(63); }
@@ -1402,6 +1444,7 @@ inline SaveLayout save_layout(const rglru_mqa_dims* d) {
     l.cs = o; o = up256(o + (size_t)d->seq_len * (D / 2) * sizeof(float2));
     l.q_rot = o; o = up256(o + tok * d->q_heads * D * 2);
     l.k_rot = o; o = up256(o + tok * D * 2);
+    l.low = o; o = up256(o + tok * d->q_heads * D);
     l.total = o;
     return l;
 }
@@ -1431,6 +1474,7 @@ inline Args make_args(const rglru_mqa_dims* d, void* save, void* ws) {
     a.cs = reinterpret_cast<const float2*>(p + l.cs);
     a.lo = reinterpret_cast<const int*>(p + l.lo);
     a.lse = reinterpret_cast<float*>(p + l.lse);
+    a.low = reinterpret_cast<int8_t*>(p + l.low);
     a.delta = reinterpret_cast<float*>(w + wl.delta);
     a.cum = reinterpret_cast<const long long*>(p + l.cum);
     a.part = reinterpret_cast<float*>(w + wl.part);

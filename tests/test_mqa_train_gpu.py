@@ -129,6 +129,38 @@ def test_score_scales(scale):
         assert np.sqrt(np.mean((g - r) ** 2)) <= 5e-3 * max(1.0, 16 * scale) * np.sqrt(np.mean(r * r)), n
 
 
+def test_short_documents():
+    """Rows of one and two keys: dS_1 = -dS_2 = P_1 P_2 (dP_1 - dP_2), what is left where dP_1 and delta cancel if
+    P_2 is small.  Four roundings enter it (q~ and k~ through the scores, the weights behind out, dS), and the
+    other factor and the result: inside the seven of the RMS bar, as long as delta itself is finer than bf16."""
+    B, T, H = 2, 64, 16
+    x, reset = _problem(B, T, H, seed=21)
+    reset = np.zeros((B, T), dtype=np.uint8)
+    reset[:, ::2] = 1
+    ref = mqa_train.train_step(x["q"], x["k"], x["v"], x["dout"], 2048, reset)
+    _close(Run(x, reset, 2048).step(), ref, "documents of two")
+
+
+@pytest.mark.parametrize("w,scale", [(2, 0.67), (2, 0.25), (5, 0.67)])
+def test_gradients_where_one_key_has_nearly_all_the_weight(w, scale):
+    """Scores that lie several units apart and have no rounding error: the queries and keys fill only pairs whose
+    angle is below 1e-8, so turning them leaves bf16 values in [1/2, 1] as they are.  What is rounded is the
+    weights behind out (a weight that is a fraction P of the row's moves delta by P 2^-8 of its dP), dS, the
+    result: three of the seven of the RMS bar."""
+    B, T, H = 3, 33, 5
+    rng = np.random.default_rng(77)
+    x, _ = _problem(B, T, H, seed=22)
+    for n in ("q", "k"):
+        a = rng.uniform(0.5, 1.0, x[n].shape) * rng.choice([-1.0, 1.0], x[n].shape)
+        a[..., :64] = 0.0
+        a[..., 128:192] = 0.0
+        x[n] = inputs.f32_to_bf16_bits(a.astype(np.float32))
+    ref = mqa_train.train_step(x["q"], x["k"], x["v"], x["dout"], w, scale=scale, base=1e20)
+    run = Run(x, None, w, scale=scale)
+    run.dims.rope_base = 1e20
+    _close(run.step(), ref, f"w{w} scale {scale}")
+
+
 def test_gradient_against_differences():
     """<dx, e> against (L(x + h e) - L(x - h e)) / 2h along random directions, L = <dout, out> from the kernel's
     own forward: out is bf16 (2^-8 relative, 1.7e-3 RMS), so L over n values is off by 1.7e-3 |dout| |out| / sqrt(n)
@@ -173,7 +205,8 @@ def test_rows_do_not_see_each_other():
     x, reset = _problem(2, 150, 3, seed=2, docs=40)
     big = {n: a.copy() for n, a in x.items()}
     for n in big:
-        big[n][1] = inputs.f32_to_bf16_bits(1e30 * np.ones(a_shape := big[n][1].shape, dtype=np.float32)) if n == "v" else big[n][1]
+        if n == "v":
+            big[n][1] = inputs.f32_to_bf16_bits(1e30 * np.ones(big[n][1].shape, dtype=np.float32))
     a, b = Run(x, reset, 64).step().bits(), Run(big, reset, 64).step().bits()
     assert all(torch.equal(a[n][0], b[n][0]) for n in NAMES)
 
