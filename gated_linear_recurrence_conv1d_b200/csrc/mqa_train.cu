@@ -227,9 +227,9 @@ struct Args {
     float scale, scale_log2;
     const int* lo;              // [B, T]
     const float2* cs;           // [T, d/2]
-    float* lse;                 // [B, THp], log2 domain
+    float* neg_lse;             // [B, THp], -L, log2 domain
     int8_t* low;                // [B, T, H, d]: the bits of out below its bf16, 8 of them
-    float* delta;               // [B, THp]
+    float* neg_delta;           // [B, THp]
     const long long* cum;       // [B nkt + 1]: 64-row tiles before each key tile
     float* part;                // partial dk, dv of (cluster, key tile)
     int nkt;                    // 128-key tiles of a batch row
@@ -541,7 +541,7 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     if (row0 + i < a.TH)
                         *reinterpret_cast<uint4*>(low + (size_t)i * D + c) = make_uint4(lb[4 * i], lb[4 * i + 1], lb[4 * i + 2], lb[4 * i + 3]);
             }
-            if (half == 0 && p_row < a.TH) a.lse[(size_t)p_b * a.THp + p_row] = p_m + log2f(l);
+            if (half == 0 && p_row < a.TH) a.neg_lse[(size_t)p_b * a.THp + p_row] = -(p_m + log2f(l));
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_pair(lead_free);
@@ -924,8 +924,8 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             const int lo_row = live ? a.lo[(size_t)t.b * a.T + tok] : 0x7fffffff;   // a row past the end sees no key
             const int full_lo = row0 + 127 < a.TH ? a.lo[(size_t)t.b * a.T + (row0 + 127) / a.H] : 0x7fffffff;
             const int full_hi = min(row0, a.TH - 1) / a.H;
-            const float lse = live ? a.lse[(size_t)t.b * a.THp + row] : 0.f;
-            const float delta = live ? a.delta[(size_t)t.b * a.THp + row] : 0.f;
+            const float nl = live ? a.neg_lse[(size_t)t.b * a.THp + row] : 0.f;
+            const float nd = live ? a.neg_delta[(size_t)t.b * a.THp + row] : 0.f;
             for (int j = 0; j < q.n; ++j) {
                 const uint32_t par = (gt + j) & 1;
                 if (!(ok = wait_w(s_full, par, g, 10))) break;
@@ -940,7 +940,11 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 const int key0 = t.lo + j * BK;
                 const bool whole = key0 >= full_lo && key0 + BK - 1 <= full_hi;
 #pragma unroll
-                for (int c = 0; c < 64; ++c) s[c] = ex2_approx(fmaf(s[c], a.scale_log2, -lse));
+                for (int c = 0; c < 64; c += 2) {
+                    const float2 x = fma2(make_float2(s[c], s[c + 1]), make_float2(a.scale_log2, a.scale_log2), make_float2(nl, nl));
+                    s[c] = ex2_approx(x.x);
+                    s[c + 1] = ex2_approx(x.y);
+                }
                 if (!whole) {
                     const int c_lo = lo_row - (key0 + half * 64), c_hi = tok - (key0 + half * 64);
 #pragma unroll
@@ -955,8 +959,11 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     tmem_ld32(tl + TM_DP + half * 64 + 32 * e, dp);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        v[16 * e + c] = bf16x2(s[32 * e + 2 * c] * (dp[2 * c] - delta), s[32 * e + 2 * c + 1] * (dp[2 * c + 1] - delta));
+                    for (int c = 0; c < 16; ++c) {
+                        const float2 x = mul2(make_float2(s[32 * e + 2 * c], s[32 * e + 2 * c + 1]),
+                                              add2(make_float2(dp[2 * c], dp[2 * c + 1]), make_float2(nd, nd)));
+                        v[16 * e + c] = bf16x2(x.x, x.y);
+                    }
                 }
                 tmem_st32(tl + TM_DP + half * 64, v);
                 tmem_wait_st();
@@ -1116,7 +1123,7 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         if (lane == 0) {
             const CUtensorMap *map_a = rank == 0 ? &map_k : &map_v, *map_x = rank == 0 ? &map_q : &map_do,
                               *map_y = rank == 0 ? &map_do : &map_q;
-            const float* vec = rank == 0 ? a.lse : a.delta;
+            const float* vec = rank == 0 ? a.neg_lse : a.neg_delta;
             uint32_t L = 0, gi = 0;
             bool ok = true;
             auto load = [&](const CUtensorMap* m, int row, uint32_t box, int c0, int nc) {   // nc boxes from column block c0
@@ -1259,10 +1266,13 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         const float4 f = vec[c];
-                        s[4 * c] = ex2_approx(fmaf(s[4 * c], a.scale_log2, -f.x));
-                        s[4 * c + 1] = ex2_approx(fmaf(s[4 * c + 1], a.scale_log2, -f.y));
-                        s[4 * c + 2] = ex2_approx(fmaf(s[4 * c + 2], a.scale_log2, -f.z));
-                        s[4 * c + 3] = ex2_approx(fmaf(s[4 * c + 3], a.scale_log2, -f.w));
+                        const float2 k = make_float2(a.scale_log2, a.scale_log2);
+                        const float2 x = fma2(make_float2(s[4 * c], s[4 * c + 1]), k, make_float2(f.x, f.y));
+                        const float2 y = fma2(make_float2(s[4 * c + 2], s[4 * c + 3]), k, make_float2(f.z, f.w));
+                        s[4 * c] = ex2_approx(x.x);
+                        s[4 * c + 1] = ex2_approx(x.y);
+                        s[4 * c + 2] = ex2_approx(y.x);
+                        s[4 * c + 3] = ex2_approx(y.y);
                     }
                     if (!whole) {
 #pragma unroll
@@ -1294,10 +1304,14 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         const float4 f = vec[c];
-                        s[4 * c] = __uint_as_float(v[2 * c] << 16) * (s[4 * c] - f.x);
-                        s[4 * c + 1] = __uint_as_float(v[2 * c] & 0xffff0000u) * (s[4 * c + 1] - f.y);
-                        s[4 * c + 2] = __uint_as_float(v[2 * c + 1] << 16) * (s[4 * c + 2] - f.z);
-                        s[4 * c + 3] = __uint_as_float(v[2 * c + 1] & 0xffff0000u) * (s[4 * c + 3] - f.w);
+                        const float2 p = make_float2(__uint_as_float(v[2 * c] << 16), __uint_as_float(v[2 * c] & 0xffff0000u));
+                        const float2 q = make_float2(__uint_as_float(v[2 * c + 1] << 16), __uint_as_float(v[2 * c + 1] & 0xffff0000u));
+                        const float2 x = mul2(p, add2(make_float2(s[4 * c], s[4 * c + 1]), make_float2(f.x, f.y)));
+                        const float2 y = mul2(q, add2(make_float2(s[4 * c + 2], s[4 * c + 3]), make_float2(f.z, f.w)));
+                        s[4 * c] = x.x;
+                        s[4 * c + 1] = x.y;
+                        s[4 * c + 2] = y.x;
+                        s[4 * c + 3] = y.y;
                     }
                     if (!whole) {
 #pragma unroll
@@ -1421,7 +1435,7 @@ __global__ void __launch_bounds__(32 * kDeltaWarps) mqa_delta_kernel(const Args 
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) a.delta[row / a.TH * a.THp + row % a.TH] = s;
+        if (lane == 0) a.neg_delta[row / a.TH * a.THp + row % a.TH] = -s;
     }
 }
 
@@ -1473,9 +1487,9 @@ inline Args make_args(const rglru_mqa_dims* d, void* save, void* ws) {
     a.scale = d->scale; a.scale_log2 = d->scale * kLog2e;
     a.cs = reinterpret_cast<const float2*>(p + l.cs);
     a.lo = reinterpret_cast<const int*>(p + l.lo);
-    a.lse = reinterpret_cast<float*>(p + l.lse);
+    a.neg_lse = reinterpret_cast<float*>(p + l.lse);
     a.low = reinterpret_cast<int8_t*>(p + l.low);
-    a.delta = reinterpret_cast<float*>(w + wl.delta);
+    a.neg_delta = reinterpret_cast<float*>(w + wl.delta);
     a.cum = reinterpret_cast<const long long*>(p + l.cum);
     a.part = reinterpret_cast<float*>(w + wl.part);
     a.status = static_cast<DeviceStatus*>(ws);
