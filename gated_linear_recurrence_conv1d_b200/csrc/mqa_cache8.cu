@@ -212,9 +212,9 @@ __global__ void __launch_bounds__(256) mqa_cache8_read_kernel(long long slots, i
 //   S^T = K Qp^T   (M 128 slots, N 48 = 16 heads x 3 parts, K 256; e4m3, fp32 sums)
 //   O^T += V^T Wp^T (M 128 columns twice, N 48 = 16 heads x 3 parts, K 128 slots)
 // straight from the codes in shared memory (V^T is the value tile read MN-major).  Four groups of 4 warps, each
-// with every fourth head, thread = slot: s = (S0 + S1 / 16 + S2 / 256) 2^e c scale_k, p = 2^(s - m) with a reference maximum m per head that moves
-// when a score passes it by more than 8 times, and the weight p scale_v, normalised by a power of two
-// vref >= the value scales seen so far, as three e5m2 parts: off by at most 2^-9 of itself, half of what bf16
+// with every fourth head, thread = slot: s = (S0 + S1 / 16 + S2 / 256) 2^e c scale_k, p = 2^(s - m) with a
+// reference maximum m per head that moves when a score passes it by more than 8 times, and the weight
+// p scale_v, normalised by a power of two vref >= the value scales seen so far, as three e5m2 parts: off by at most 2^-9 of itself, half of what bf16
 // would leave, down to weights of 2^-29 (e4m3 parts end at 2^-16, which shows where one slot has nearly all
 // the weight and a small value).  p adds to the thread's own sum in fp32.  O stays in TMEM for the whole segment; when m or vref
 // moves it is rescaled there (each group has its own vref and its own columns of S, W and O, so within a
@@ -518,7 +518,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 : "memory");
             return o != 0;
         };
-        auto both_or = [&](bool v) {                                 // the OR of v over both groups
+        auto all_or = [&](bool v) {                                 // the OR of v over all groups
             uint32_t o;
             asm volatile(
                 "{\n\t.reg .pred p, q;\n\t"
@@ -539,7 +539,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
             if (threadIdx.x < D / 2) rope_cos_sin(a.base, threadIdx.x, (double)p, cs[threadIdx.x].x, cs[threadIdx.x].y);
             const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(smem + OFF_IN + (n & 1) * IN_BYTES);
             const bool here = wait_w(in_full(n & 1), (n >> 1) & 1, g, 12);
-            if (both_or(!here)) return false;             // the angles are there too
+            if (all_or(!here)) return false;             // the angles are there too
 #pragma unroll 1
             for (int i = wi; i < a.H + (fresh ? 2 : 0); i += kSoftWarps) {
                 float y[8], z[8];
@@ -813,7 +813,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 if (r == 0) red[5 * kHg + h] = m[h];
             }
             // the groups leave together (a failed wait of one of them): they meet in begin()
-            if (both_or(stop || !ok)) break;
+            if (all_or(stop || !ok)) break;
         }
         tmem_wait_ld();
         tmem_wait_st();
@@ -836,7 +836,9 @@ __global__ void __launch_bounds__(D / 4, 12) mqa_decode8_merge_kernel(int H, con
     const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x, pitch = part_pitch(H);
     uint2* row = reinterpret_cast<uint2*>(out + ((size_t)b * H + h) * D) + t;
     const int p = pos[b];
-    const int2 c = meta[b];            // not written for a row without a token
+    // Not written for a row without a token.  Kept inside the parts, for a pos that was changed under way (a caller's
+    // missing dependency between streams): its output is then any, but nothing else is touched.
+    const int2 m2 = meta[b], c = make_int2(min(max(m2.x, 0), kMaxCtas - 1), min(max(m2.y, 0), kMaxCtas - 1));
     if (p < 0) {
         *row = make_uint2(0, 0);
         return;
