@@ -237,18 +237,19 @@ constexpr int kQParts = 3, kQRows = kQParts * kMaxH;
 constexpr uint32_t Q_BYTES = kQRows * D;              // 12288: 2 boxes of [48 x 128 B]
 constexpr int kWParts = 3, kWRows = kWParts * kMaxH;
 constexpr uint32_t W_BYTES = kWRows * kTile;          // 6144: [48 x 128 slots]
-constexpr uint32_t RED_BYTES = 128;                   // of a group: [4 warps][kHg], [4] scales, [kHg] maxima
+constexpr uint32_t RED_BYTES = 192;                   // of a group: [4 warps][kHg], [4] scales; a segment's [4 warps][kHg] sums, [kHg] maxima
 constexpr uint32_t STG_BYTES = 2 * D + 16;            // the new slot: key and value codes, their scales
-constexpr uint32_t OFF_Q = kNBuf * TILE_BYTES, OFF_W = OFF_Q + Q_BYTES, OFF_CS = OFF_W + 2 * W_BYTES;
+constexpr uint32_t OFF_Q = kNBuf * TILE_BYTES, OFF_W = OFF_Q + 2 * Q_BYTES, OFF_CS = OFF_W + 2 * W_BYTES;
 constexpr uint32_t IN_BYTES = (kMaxH + 2) * D * 2;     // a segment's queries, new key and value
-constexpr uint32_t OFF_IN = OFF_CS + D / 2 * 16, OFF_STG = OFF_IN + 2 * IN_BYTES;
-constexpr uint32_t OFF_QS = OFF_STG + 2 * STG_BYTES, OFF_RED = OFF_QS + 64;
+constexpr uint32_t OFF_IN = OFF_CS + 2 * (D / 2 * 16), OFF_STG = OFF_IN + 2 * IN_BYTES;
+constexpr uint32_t OFF_QS = OFF_STG + 2 * STG_BYTES, OFF_RED = OFF_QS + 2 * 64;
 constexpr uint32_t OFF_BAR = OFF_RED + kGroups * RED_BYTES;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TM_S = 0, TM_O = 128, TMEM_COLS = 256;     // S: two buffers, 64 apart; O: two halves, 64 apart
 constexpr int kSoftWarps = 4 * kGroups, kSoft = 32 * kSoftWarps, kWarpTma = kSoftWarps, kWarpMma = kSoftWarps + 1;
-constexpr int kThreads = kSoft + 64;
+constexpr int kPrepWarps = 2;          // five warps a scheduler in all, with 96 registers as without them
+constexpr int kThreads = kSoft + 64 + 32 * kPrepWarps;
 
 constexpr float kAlpha = 4096.0f;                     // weights are held as alpha p: p <= 8 keeps them below 57344
 
@@ -319,6 +320,20 @@ __device__ __forceinline__ bool next_seg(const DecArgs& a, Walk& k, DecSeg& s) {
     return true;
 }
 
+// the OR of v over the threads that meet at barrier `id`
+__device__ __forceinline__ bool named_or(bool v, int id, int threads) {
+    uint32_t o;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "barrier.red.or.pred p, %2, %3, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(o)
+        : "r"((uint32_t)v), "r"(id), "r"(threads)
+        : "memory");
+    return o != 0;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -330,11 +345,13 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
     auto s_full = [&](uint32_t i) { return bars + 16 * kNBuf + 8 * i; };
     auto w_full = [&](uint32_t i) { return bars + 16 * kNBuf + 16 + 8 * i; };
     auto o_done = [&](uint32_t i) { return bars + 16 * kNBuf + 32 + 8 * i; };
-    const uint32_t o_free = bars + 16 * kNBuf + 48, mma_done = o_free + 8, q_ready = o_free + 16;
-    auto in_full = [&](uint32_t i) { return bars + 16 * kNBuf + 72 + 8 * i; };
-    auto in_free = [&](uint32_t i) { return bars + 16 * kNBuf + 88 + 8 * i; };
-    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 16 * kNBuf + 104);
-    const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 16 * kNBuf + 112), a.status, a.timeout_ns};
+    const uint32_t o_free = bars + 16 * kNBuf + 48, mma_done = o_free + 8;
+    auto q_ready = [&](uint32_t i) { return bars + 16 * kNBuf + 64 + 8 * i; };
+    auto q_free = [&](uint32_t i) { return bars + 16 * kNBuf + 80 + 8 * i; };
+    auto in_full = [&](uint32_t i) { return bars + 16 * kNBuf + 96 + 8 * i; };
+    auto in_free = [&](uint32_t i) { return bars + 16 * kNBuf + 112 + 8 * i; };
+    volatile uint32_t* tmem_s = reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + 16 * kNBuf + 128);
+    const Guard g{reinterpret_cast<volatile int*>(smem + OFF_BAR + 16 * kNBuf + 136), a.status, a.timeout_ns};
     unsigned* scan = reinterpret_cast<unsigned*>(smem);            // before the first load: per-warp sums
     Walk* walk_s = reinterpret_cast<Walk*>(smem + OFF_W);            // before the first weights
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -349,10 +366,11 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
             mbar_init(w_full(i), kSoftWarps);
             mbar_init(o_done(i), 1);
             mbar_init(in_full(i), 1);
-            mbar_init(in_free(i), kSoftWarps);
+            mbar_init(in_free(i), 1);
+            mbar_init(q_ready(i), 1);
+            mbar_init(q_free(i), 1);
         }
         mbar_init(o_free, kSoftWarps);
-        mbar_init(q_ready, kSoftWarps);
         mbar_init(mma_done, 1);
         *g.abort = 0;
         fence_barrier_init();
@@ -407,18 +425,105 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
     __syncthreads();                                                 // walk_s and scan give way to the tiles
     DecSeg sg{};
 
+    // Segment n's queries, and its new slot if it holds it, into shared memory (and the ring), by `warps` warps, of which
+    // this is number wi
+    auto prepare = [&](const DecSeg& x, uint32_t n, int wi, int warps, double2* cs, auto all_or) {
+        uint8_t* stg = smem + OFF_STG + (n & 1) * STG_BYTES;
+        const int p = a.pos[x.b], slot = p % a.w;
+        const bool fresh = slot >= x.t0 * kTile && slot < (x.t0 + x.nt) * kTile;
+        for (int j = 32 * wi + lane; j < D / 2; j += 32 * warps) rope_cos_sin(a.base, j, (double)p, cs[j].x, cs[j].y);
+        const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(smem + OFF_IN + (n & 1) * IN_BYTES);
+        const bool here = wait_w(in_full(n & 1), (n >> 1) & 1, g, 12);
+        if (all_or(!here)) return false;             // the angles are there too
+#pragma unroll 1
+        for (int i = wi; i < a.H + (fresh ? 2 : 0); i += warps) {
+            float y[8], z[8];
+            if (i >= a.H) {
+                const int half = i - a.H;
+                unpack(load_pairs(in + (kMaxH + half) * D, lane), z);
+                SlotCodes c;
+                if (half) {
+                    c = quantise_slot(z);
+                } else {
+                    double d[8];
+                    turn64(z, cs, lane, d);
+                    c = quantise_slot(d);
+                }
+                const size_t at = ((size_t)x.b * 2 + half) * a.w + slot;
+                store_slot(c, lane, a.codes + at * D, a.scales + at);
+                store_slot(c, lane, stg + half * D, reinterpret_cast<float*>(stg + 2 * D) + half);
+                continue;
+            }
+            unpack(load_pairs(in + i * D, lane), z);
+            float mq = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float c = (float)cs[4 * lane + e].x, s = (float)cs[4 * lane + e].y;
+                y[e] = z[e] * c - z[4 + e] * s;
+                y[4 + e] = z[4 + e] * c + z[e] * s;
+                mq = fmaxf(mq, fmaxf(fabsf(y[e]), fabsf(y[4 + e])));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, o));
+            // mq / 448 rounded up to a power of two (at least 2^-100, so that its reciprocal is finite)
+            const float r448 = fminf(fmaxf(mq, 448.0f * 7.9e-31f), 3.0e38f) * (1.0f / 448.0f);
+            int e2 = (__float_as_int(r448) >> 23) - 127;
+            if (__float_as_int(r448) & 0x7fffff) ++e2;
+            const float up = __int_as_float((e2 + 127) << 23), down = __int_as_float((127 - e2) << 23);
+            if (lane == 0)                            // a query with an infinity: NaN
+                reinterpret_cast<float*>(smem + OFF_QS + (n & 1) * 64)[head_row(i)] = mq < INFINITY ? up : __int_as_float(0x7fffffff);
+            uint32_t c[kQParts][2] = {};
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                float u = y[e] * down, v = y[e + 1] * down;
+#pragma unroll
+                for (int part = 0; part < kQParts; ++part) {
+                    const uint32_t cc = e4m3x2(u, v);
+                    const float2 f = e4m3x2_values(cc);
+                    c[part][e >> 2] |= cc << (8 * (e & 2));
+                    u = (u - f.x) * 16.0f;
+                    v = (v - f.y) * 16.0f;
+                }
+            }
+            // row part * 16 + head_row of the two [48 x 128 bytes] blocks, 16-byte chunks swizzled by the row
+#pragma unroll
+            for (int part = 0; part < kQParts; ++part) {
+                const int row = part * kMaxH + head_row(i);
+                uint8_t* dst = smem + OFF_Q + (n & 1) * Q_BYTES + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
+                *reinterpret_cast<uint32_t*>(dst) = c[part][0];
+                *reinterpret_cast<uint32_t*>(dst + Q_BYTES / 2) = c[part][1];
+            }
+        }
+        fence_proxy_async_smem();
+        if (all_or(false)) return false;              // (never: a barrier) every warp's part is there
+        if (wi == 0 && lane == 0) {
+            mbar_arrive(in_free(n & 1));
+            mbar_arrive(q_ready(n & 1));
+        }
+        return true;
+    };
+
     if (warp == kWarpTma) {
         if (lane == 0) {
+            // a segment's inputs before the tiles of the segment before it
+            Walk kn = k;
             uint32_t L = 0, ns = 0;
-            bool ok = true;
-            for (; ok && next_seg(a, k, sg); ++ns) {
-                // the segment's inputs before its tiles, which would queue in front of them for microseconds
+            auto load_in = [&]() {
+                if (!next_seg(a, kn, sg)) return true;
                 const uint32_t e = ns & 1, row_bytes = (uint32_t)a.H * D * 2, in = sb + OFF_IN + e * IN_BYTES;
-                if (ns > 1 && !(ok = wait(in_free(e), ((ns >> 1) - 1) & 1, g, 11))) break;
+                if (ns > 1 && !wait(in_free(e), ((ns >> 1) - 1) & 1, g, 11)) return false;
+                ++ns;
                 mbar_arrive_expect_tx(in_full(e), row_bytes + 2 * D * 2);
                 bulk_load(in, a.q + (size_t)sg.b * a.H * D, row_bytes, in_full(e));
                 bulk_load(in + kMaxH * D * 2, a.k + (size_t)sg.b * D, D * 2, in_full(e));
                 bulk_load(in + kMaxH * D * 2 + D * 2, a.v + (size_t)sg.b * D, D * 2, in_full(e));
+                return true;
+            };
+            bool ok = load_in();
+            while (ok && next_seg(a, k, sg)) {
+                const DecSeg here = sg;
+                if (!(ok = load_in())) break;
+                sg = here;
                 for (int t = 0; ok && t < sg.nt; ++t)
                     for (int kv = 0; kv < 2; ++kv, ++L) {
                         const uint32_t s = L % kNBuf, u = L / kNBuf;
@@ -440,58 +545,74 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
     } else if (warp == kWarpMma) {
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint32_t id_s = idesc_fp8(kQRows, 0, 0), id_o = idesc_fp8(kWRows, 1, 1);
-        uint32_t gt = 0, ns = 0;
-        bool ok = true;
-        // the new key's (half 0) or value's (1) codes over row `slot` of the tile in buffer s
-        auto put_new = [&](uint32_t s, int slot, int half) {
+        // S runs one tile ahead of the weighted sum, across segments
+        Walk kp = k;
+        DecSeg sp{};
+        uint32_t is = 0, ns = 0;                                     // tiles with S issued, segments with S begun
+        int ts = 0, slot_s = 0;                                      // the next S: its tile, the segment's new slot from its first
+        bool ok = true, more = next_seg(a, k, sg);
+        // segment n's new key's (half 0) or value's (1) codes over row `slot` of the tile in buffer s
+        auto put_new = [&](uint32_t n, uint32_t s, int slot, int half) {
             if (lane < 16) {
-                const uint4 c = *reinterpret_cast<const uint4*>(smem + OFF_STG + (ns & 1) * STG_BYTES + half * D + lane * 16);
+                const uint4 c = *reinterpret_cast<const uint4*>(smem + OFF_STG + (n & 1) * STG_BYTES + half * D + lane * 16);
                 *reinterpret_cast<uint4*>(smem + s * TILE_BYTES + (lane >> 3) * 16384 + slot * 128 + (((lane & 7) ^ (slot & 7)) << 4)) = c;
             }
             fence_proxy_async_smem();
             __syncwarp();
         };
-        for (; ok && next_seg(a, k, sg); ++ns) {
-            if (!(ok = wait_w(q_ready, ns & 1, g, 10))) break;
-            const int slot = a.pos[sg.b] % a.w - sg.t0 * kTile;       // the new slot, from the segment's first
-            for (int t = 0; ok && t <= sg.nt; ++t) {
-                if (t < sg.nt) {
-                    const uint32_t i = gt + t, l = 2 * i, s = l % kNBuf, buf = i & 1;
-                    if (!(ok = wait_w(full(s), (l / kNBuf) & 1, g, 2))) break;
-                    if (slot >= t * kTile && slot < (t + 1) * kTile) put_new(s, slot - t * kTile, 0);
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int ks = 0; ks < D / 32; ++ks)
-                            mma_fp8(tm + TM_S + buf * 64, desc_k_sw128(sb + s * TILE_BYTES + (ks >> 2) * 16384 + (ks & 3) * 32),
-                                     desc_k_sw128(sb + OFF_Q + (ks >> 2) * (Q_BYTES / 2) + (ks & 3) * 32), id_s,
-                                     ks > 0 ? 1u : 0u);
-                        mma_commit(s_full(buf));
-                        mma_commit(empty(s));
-                    }
-                    __syncwarp();
-                }
-                if (t >= 1) {
-                    const uint32_t i = gt + t - 1, l = 2 * i + 1, s = l % kNBuf, buf = i & 1;
-                    if (t == 1 && ns > 0 && !(ok = wait_w(o_free, (ns - 1) & 1, g, 3))) break;
-                    if (!(ok = wait_w(full(s), (l / kNBuf) & 1, g, 4))) break;
-                    if (!(ok = wait_w(w_full(buf), (i >> 1) & 1, g, 5))) break;
-                    if (slot >= (t - 1) * kTile && slot < t * kTile) put_new(s, slot - (t - 1) * kTile, 1);
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh)               // columns [128 hh, 128 hh + 128)
-#pragma unroll
-                            for (int ks = 0; ks < kTile / 32; ++ks)
-                                mma_fp8(tm + TM_O + hh * 64, desc_mn_sw128(sb + s * TILE_BYTES + hh * 16384 + ks * 4096, 16384),
-                                         desc_k_sw128(sb + OFF_W + buf * W_BYTES + ks * 32), id_o, (t > 1 || ks > 0) ? 1u : 0u);
-                        mma_commit(o_done(buf));
-                        mma_commit(empty(s));
-                    }
-                    __syncwarp();
-                }
+        auto issue_s = [&]() {
+            if (ts == 0) {
+                if (!wait_w(q_ready(ns & 1), (ns >> 1) & 1, g, 10)) return false;
+                slot_s = a.pos[sg.b] % a.w - sg.t0 * kTile;
             }
-            gt += sg.nt;
+            const uint32_t l = 2 * is, s = l % kNBuf, buf = is & 1, e = ns & 1;
+            if (!wait_w(full(s), (l / kNBuf) & 1, g, 2)) return false;
+            if (slot_s >= ts * kTile && slot_s < (ts + 1) * kTile) put_new(ns, s, slot_s - ts * kTile, 0);
+            tc_fence_after();
+            const bool last = ts + 1 == sg.nt;
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < D / 32; ++ks)
+                    mma_fp8(tm + TM_S + buf * 64, desc_k_sw128(sb + s * TILE_BYTES + (ks >> 2) * 16384 + (ks & 3) * 32),
+                             desc_k_sw128(sb + OFF_Q + e * Q_BYTES + (ks >> 2) * (Q_BYTES / 2) + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
+                mma_commit(s_full(buf));
+                mma_commit(empty(s));
+                if (last) mma_commit(q_free(e));
+            }
+            __syncwarp();
+            ++is;
+            ++ts;
+            if (last) {
+                ts = 0;
+                ++ns;
+                more = next_seg(a, k, sg);
+            }
+            return true;
+        };
+        if (more) ok = issue_s();
+        uint32_t i = 0, np = 0;
+        for (; ok && next_seg(a, kp, sp); ++np) {
+            const int slot = a.pos[sp.b] % a.w - sp.t0 * kTile;       // the new slot, from the segment's first
+            for (int t = 0; t < sp.nt; ++t, ++i) {
+                if (more && !(ok = issue_s())) break;
+                const uint32_t l = 2 * i + 1, s = l % kNBuf, buf = i & 1;
+                if (t == 0 && np > 0 && !(ok = wait_w(o_free, (np - 1) & 1, g, 3))) break;
+                if (!(ok = wait_w(full(s), (l / kNBuf) & 1, g, 4))) break;
+                if (!(ok = wait_w(w_full(buf), (i >> 1) & 1, g, 5))) break;
+                if (slot >= t * kTile && slot < (t + 1) * kTile) put_new(np, s, slot - t * kTile, 1);
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh)                   // columns [128 hh, 128 hh + 128)
+#pragma unroll
+                        for (int ks = 0; ks < kTile / 32; ++ks)
+                            mma_fp8(tm + TM_O + hh * 64, desc_mn_sw128(sb + s * TILE_BYTES + hh * 16384 + ks * 4096, 16384),
+                                     desc_k_sw128(sb + OFF_W + buf * W_BYTES + ks * 32), id_o, (t > 0 || ks > 0) ? 1u : 0u);
+                    mma_commit(o_done(buf));
+                    mma_commit(empty(s));
+                }
+                __syncwarp();
+            }
         }
         if (elect_one()) mma_commit(mma_done);
         __syncwarp();
@@ -501,113 +622,24 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
             }
         }
         __syncwarp();
+    } else if (warp > kWarpMma) {
+        // the segments after the first, while the one before is worked on: n overwrites the queries, scales and new slot
+        // of n - 2, whose S is done (q_free) and whose softmax is (o_free)
+        auto prep_or = [&](bool v) { return named_or(v, 6, 32 * kPrepWarps); };
+        bool some = next_seg(a, k, sg);
+        for (uint32_t n = 1; some && (some = next_seg(a, k, sg)); ++n) {
+            bool ok = n < 2 || wait_w(q_free(n & 1), ((n >> 1) - 1) & 1, g, 13);
+            ok = ok && (n < 2 || wait_w(o_free, (n - 2) & 1, g, 14));
+            if (prep_or(!ok) || !prepare(sg, n, warp - kWarpMma - 1, kPrepWarps, reinterpret_cast<double2*>(smem + OFF_CS) + D / 2, prep_or)) break;
+        }
     } else {
         const int grp = warp >> 2, r = threadIdx.x & 127;            // group; slot of a tile, then column
         const int nh = (a.H + kGroups - 1 - grp) / kGroups;          // this group's heads: kGroups i + grp, i < nh
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + grp * kHg;
         float* red = reinterpret_cast<float*>(smem + OFF_RED + grp * RED_BYTES);
-        auto grp_or = [&](bool v) {                                  // the OR of v over the group's 128 threads
-            uint32_t o;
-            asm volatile(
-                "{\n\t.reg .pred p, q;\n\t"
-                "setp.ne.u32 q, %1, 0;\n\t"
-                "barrier.red.or.pred p, %2, 128, q;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(o)
-                : "r"((uint32_t)v), "r"(1 + grp)
-                : "memory");
-            return o != 0;
-        };
-        auto all_or = [&](bool v) {                                 // the OR of v over all groups
-            uint32_t o;
-            asm volatile(
-                "{\n\t.reg .pred p, q;\n\t"
-                "setp.ne.u32 q, %1, 0;\n\t"
-                "barrier.red.or.pred p, 5, 512, q;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(o)
-                : "r"((uint32_t)v)
-                : "memory");
-            return o != 0;
-        };
-        // a segment's queries, and its new slot if it holds it, into shared memory (and the ring)
-        auto begin = [&](const DecSeg& x, uint32_t n) {
-            double2* cs = reinterpret_cast<double2*>(smem + OFF_CS);
-            uint8_t* stg = smem + OFF_STG + (n & 1) * STG_BYTES;
-            const int p = a.pos[x.b], slot = p % a.w, wi = threadIdx.x >> 5;
-            const bool fresh = slot >= x.t0 * kTile && slot < (x.t0 + x.nt) * kTile;
-            if (threadIdx.x < D / 2) rope_cos_sin(a.base, threadIdx.x, (double)p, cs[threadIdx.x].x, cs[threadIdx.x].y);
-            const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(smem + OFF_IN + (n & 1) * IN_BYTES);
-            const bool here = wait_w(in_full(n & 1), (n >> 1) & 1, g, 12);
-            if (all_or(!here)) return false;             // the angles are there too
-#pragma unroll 1
-            for (int i = wi; i < a.H + (fresh ? 2 : 0); i += kSoftWarps) {
-                float y[8], z[8];
-                if (i >= a.H) {
-                    const int half = i - a.H;
-                    unpack(load_pairs(in + (kMaxH + half) * D, lane), z);
-                    SlotCodes c;
-                    if (half) {
-                        c = quantise_slot(z);
-                    } else {
-                        double d[8];
-                        turn64(z, cs, lane, d);
-                        c = quantise_slot(d);
-                    }
-                    const size_t at = ((size_t)x.b * 2 + half) * a.w + slot;
-                    store_slot(c, lane, a.codes + at * D, a.scales + at);
-                    store_slot(c, lane, stg + half * D, reinterpret_cast<float*>(stg + 2 * D) + half);
-                    continue;
-                }
-                unpack(load_pairs(in + i * D, lane), z);
-                float mq = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float c = (float)cs[4 * lane + e].x, s = (float)cs[4 * lane + e].y;
-                    y[e] = z[e] * c - z[4 + e] * s;
-                    y[4 + e] = z[4 + e] * c + z[e] * s;
-                    mq = fmaxf(mq, fmaxf(fabsf(y[e]), fabsf(y[4 + e])));
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, o));
-                // mq / 448 rounded up to a power of two (at least 2^-100, so that its reciprocal is finite)
-                const float r448 = fminf(fmaxf(mq, 448.0f * 7.9e-31f), 3.0e38f) * (1.0f / 448.0f);
-                int e2 = (__float_as_int(r448) >> 23) - 127;
-                if (__float_as_int(r448) & 0x7fffff) ++e2;
-                const float up = __int_as_float((e2 + 127) << 23), down = __int_as_float((127 - e2) << 23);
-                if (lane == 0)                            // a query with an infinity: NaN
-                    reinterpret_cast<float*>(smem + OFF_QS)[head_row(i)] = mq < INFINITY ? up : __int_as_float(0x7fffffff);
-                uint32_t c[kQParts][2] = {};
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    float u = y[e] * down, v = y[e + 1] * down;
-#pragma unroll
-                    for (int part = 0; part < kQParts; ++part) {
-                        const uint32_t cc = e4m3x2(u, v);
-                        const float2 f = e4m3x2_values(cc);
-                        c[part][e >> 2] |= cc << (8 * (e & 2));
-                        u = (u - f.x) * 16.0f;
-                        v = (v - f.y) * 16.0f;
-                    }
-                }
-                // row part * 16 + head_row of the two [48 x 128 bytes] blocks, 16-byte chunks swizzled by the row
-#pragma unroll
-                for (int part = 0; part < kQParts; ++part) {
-                    const int row = part * kMaxH + head_row(i);
-                    uint8_t* dst = smem + OFF_Q + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
-                    *reinterpret_cast<uint32_t*>(dst) = c[part][0];
-                    *reinterpret_cast<uint32_t*>(dst + Q_BYTES / 2) = c[part][1];
-                }
-            }
-            fence_proxy_async_smem();
-            asm volatile("bar.sync 5, 512;" ::: "memory");            // the scales and codes are there for every warp
-            if (lane == 0) {
-                mbar_arrive(in_free(n & 1));
-                mbar_arrive(q_ready);
-            }
-            return true;
-        };
-        float vref = 0.f;
+        auto grp_or = [&](bool v) { return named_or(v, 1 + grp, 128); };     // over the group's threads
+        float vref = 0.f, p_vref = 0.f;
+        float *sums = red + 5 * kHg, *maxima = red + 9 * kHg;
         // a segment's output, its last tile number `last`: the row's, or a part of it
         auto finish = [&](const DecSeg& x, uint32_t last) {
             if (grp_or(!wait_w(o_done(last & 1), (last >> 1) & 1, g, 9))) return false;
@@ -622,13 +654,13 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 tmem_wait_ld();
 #pragma unroll
                 for (int h = 0; h < kHg; ++h)
-                    o[hh][h] = fmaf(y2[h], 1.0f / 64.0f, fmaf(y1[h], 1.0f / 8.0f, o[hh][h])) * (vref * (1.0f / kAlpha));
+                    o[hh][h] = fmaf(y2[h], 1.0f / 64.0f, fmaf(y1[h], 1.0f / 8.0f, o[hh][h])) * (p_vref * (1.0f / kAlpha));
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free);
 #pragma unroll
-            for (int h = 0; h < kHg; ++h) l[h] = (red[h] + red[kHg + h]) + (red[2 * kHg + h] + red[3 * kHg + h]);
+            for (int h = 0; h < kHg; ++h) l[h] = (sums[h] + sums[kHg + h]) + (sums[2 * kHg + h] + sums[3 * kHg + h]);
             if (x.t0 == 0 && r == 0 && grp == 0) a.meta[x.b] = make_int2(x.c0, x.c1);
             if (x.c0 == x.c1) {
 #pragma unroll
@@ -650,24 +682,25 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                     part[2 * kMaxH + (kGroups * h + grp) * D + r] = o[0][h];
                     part[2 * kMaxH + (kGroups * h + grp) * D + 128 + r] = o[1][h];
                     if (r == 0) {
-                        part[grp * kHg + h] = red[5 * kHg + h];
+                        part[grp * kHg + h] = maxima[h];
                         part[kMaxH + grp * kHg + h] = l[h];
                     }
                 }
-            grp_or(false);                                // red is read before the next use
+            grp_or(false);                                // sums and maxima are read before the next use
             return true;
         };
-        uint32_t gt = 0, ns = 0;
-        bool ok = true, stop = false;
-        DecSeg nx{};
-        for (;; ++ns) {
-            const bool more = next_seg(a, k, nx);
-            if (more && !begin(nx, ns)) break;
-            if (ns > 0 && !finish(sg, gt - 1)) stop = true;   // the segment before, under this one's first products
-            if (!more) break;
-            sg = nx;
+        uint32_t gt = 0;
+        bool ok = true, stop = false, pending = false;
+        DecSeg prev{};
+        Walk k0 = k;
+        if (next_seg(a, k0, sg)) {                                   // the first segment is prepared by all of these warps
+            auto soft_or = [&](bool v) { return named_or(v, 5, kSoft); };
+            stop = !prepare(sg, 0, warp, kSoftWarps, reinterpret_cast<double2*>(smem + OFF_CS), soft_or);
+        }
+        for (uint32_t ns = 0; !stop && next_seg(a, k, sg); ++ns) {
+            ok = ok && wait_w(q_ready(ns & 1), (ns >> 1) & 1, g, 12);
             const float *sk = a.scales + (size_t)sg.b * 2 * a.w, *sv = sk + a.w;
-            const float* qs = reinterpret_cast<const float*>(smem + OFF_QS) + grp * kHg;
+            const float* qs = reinterpret_cast<const float*>(smem + OFF_QS + (ns & 1) * 64) + grp * kHg;
             const float* fresh = reinterpret_cast<const float*>(smem + OFF_STG + (ns & 1) * STG_BYTES + 2 * D);
             const int slot = a.pos[sg.b] % a.w;
             float m[kHg], l[kHg];
@@ -802,19 +835,24 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(w_full(buf));
+                // the segment before, under this one's first products
+                if (t == 0 && pending && !finish(prev, gt - 1)) stop = true;
             }
+            if (stop) break;
             gt += sg.nt;
             // sums over the slots: lanes, then (in finish) warps
 #pragma unroll
             for (int h = 0; h < kHg; ++h) {
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-                if (lane == 0) red[(warp & 3) * kHg + h] = l[h];
-                if (r == 0) red[5 * kHg + h] = m[h];
+                if (lane == 0) sums[(warp & 3) * kHg + h] = l[h];
+                if (r == 0) maxima[h] = m[h];
             }
-            // the groups leave together (a failed wait of one of them): they meet in begin()
-            if (all_or(stop || !ok)) break;
+            prev = sg;
+            p_vref = vref;
+            pending = true;
         }
+        if (!stop && pending) finish(prev, gt - 1);
         tmem_wait_ld();
         tmem_wait_st();
     }
