@@ -242,7 +242,7 @@ constexpr uint32_t STG_BYTES = 2 * D + 16;            // the new slot: key and v
 constexpr uint32_t OFF_Q = kNBuf * TILE_BYTES, OFF_W = OFF_Q + 2 * Q_BYTES, OFF_CS = OFF_W + 2 * W_BYTES;
 constexpr uint32_t IN_BYTES = (kMaxH + 2) * D * 2;     // a segment's queries, new key and value
 constexpr uint32_t OFF_IN = OFF_CS + 2 * (D / 2 * 16), OFF_STG = OFF_IN + 2 * IN_BYTES;
-constexpr uint32_t OFF_QS = OFF_STG + 2 * STG_BYTES, OFF_RED = OFF_QS + 2 * 64;
+constexpr uint32_t OFF_QS = OFF_STG + 2 * STG_BYTES, OFF_SEG = OFF_QS + 2 * 64, OFF_RED = OFF_SEG + 2 * 32;
 constexpr uint32_t OFF_BAR = OFF_RED + kGroups * RED_BYTES;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -295,7 +295,9 @@ struct Walk {
 };
 struct DecSeg {
     int b, t0, nt, n, c0, c1;            // row, its first tile here, tiles here, slots of the row, the row's CTAs
+    int last, slot;                      // the CTA's last one; the row's new slot
 };
+static_assert(sizeof(DecSeg) == 32, "two int4");
 // the CTA whose piece [total c / G, total (c + 1) / G) holds x: the last c with total c < (x + 1) G
 __device__ __forceinline__ int owner(unsigned x, unsigned total, unsigned G) { return (int)(((x + 1) * G - 1) / total); }
 __device__ __forceinline__ bool next_seg(const DecArgs& a, Walk& k, DecSeg& s) {
@@ -317,6 +319,8 @@ __device__ __forceinline__ bool next_seg(const DecArgs& a, Walk& k, DecSeg& s) {
     s.c0 = whole ? (int)blockIdx.x : owner(k.row_beg, k.total, k.G);
     s.c1 = whole ? (int)blockIdx.x : owner(k.row_beg + tiles - 1, k.total, k.G);
     k.pos += s.nt;
+    s.last = k.pos >= k.end;
+    s.slot = a.pos[s.b] % a.w;
     return true;
 }
 
@@ -429,7 +433,8 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
     // this is number wi
     auto prepare = [&](const DecSeg& x, uint32_t n, int wi, int warps, double2* cs, auto all_or) {
         uint8_t* stg = smem + OFF_STG + (n & 1) * STG_BYTES;
-        const int p = a.pos[x.b], slot = p % a.w;
+        const int p = a.pos[x.b], slot = x.slot;
+        if (wi == 0 && lane == 0) *reinterpret_cast<DecSeg*>(smem + OFF_SEG + (n & 1) * 32) = x;
         const bool fresh = slot >= x.t0 * kTile && slot < (x.t0 + x.nt) * kTile;
         for (int j = 32 * wi + lane; j < D / 2; j += 32 * warps) rope_cos_sin(a.base, j, (double)p, cs[j].x, cs[j].y);
         const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(smem + OFF_IN + (n & 1) * IN_BYTES);
@@ -563,7 +568,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
         auto issue_s = [&]() {
             if (ts == 0) {
                 if (!wait_w(q_ready(ns & 1), (ns >> 1) & 1, g, 10)) return false;
-                slot_s = a.pos[sg.b] % a.w - sg.t0 * kTile;
+                slot_s = sg.slot - sg.t0 * kTile;
             }
             const uint32_t l = 2 * is, s = l % kNBuf, buf = is & 1, e = ns & 1;
             if (!wait_w(full(s), (l / kNBuf) & 1, g, 2)) return false;
@@ -592,7 +597,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
         if (more) ok = issue_s();
         uint32_t i = 0, np = 0;
         for (; ok && next_seg(a, kp, sp); ++np) {
-            const int slot = a.pos[sp.b] % a.w - sp.t0 * kTile;       // the new slot, from the segment's first
+            const int slot = sp.slot - sp.t0 * kTile;       // the new slot, from the segment's first
             for (int t = 0; t < sp.nt; ++t, ++i) {
                 if (more && !(ok = issue_s())) break;
                 const uint32_t l = 2 * i + 1, s = l % kNBuf, buf = i & 1;
@@ -641,7 +646,8 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
         float vref = 0.f, p_vref = 0.f;
         float *sums = red + 5 * kHg, *maxima = red + 9 * kHg;
         // a segment's output, its last tile number `last`: the row's, or a part of it
-        auto finish = [&](const DecSeg& x, uint32_t last) {
+        auto finish = [&](uint32_t n, uint32_t last) {
+            const DecSeg x = *reinterpret_cast<const DecSeg*>(smem + OFF_SEG + (n & 1) * 32);
             if (grp_or(!wait_w(o_done(last & 1), (last >> 1) & 1, g, 9))) return false;
             tc_fence_after();
             float o[2][kHg], l[kHg];
@@ -690,19 +696,22 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
             return true;
         };
         uint32_t gt = 0;
-        bool ok = true, stop = false, pending = false;
-        DecSeg prev{};
-        Walk k0 = k;
-        if (next_seg(a, k0, sg)) {                                   // the first segment is prepared by all of these warps
+        bool ok = true, stop = true;
+        uint32_t ns = 0;
+        if (next_seg(a, k, sg)) {                                    // the first segment is prepared by all of these warps
             auto soft_or = [&](bool v) { return named_or(v, 5, kSoft); };
             stop = !prepare(sg, 0, warp, kSoftWarps, reinterpret_cast<double2*>(smem + OFF_CS), soft_or);
         }
-        for (uint32_t ns = 0; !stop && next_seg(a, k, sg); ++ns) {
-            ok = ok && wait_w(q_ready(ns & 1), (ns >> 1) & 1, g, 12);
+        for (bool last = false; !stop && !last; ++ns) {
+            if (grp_or(!wait_w(q_ready(ns & 1), (ns >> 1) & 1, g, 12))) {
+                stop = true;
+                break;
+            }
+            const DecSeg sg = *reinterpret_cast<const DecSeg*>(smem + OFF_SEG + (ns & 1) * 32);
+            last = sg.last;
             const float *sk = a.scales + (size_t)sg.b * 2 * a.w, *sv = sk + a.w;
             const float* qs = reinterpret_cast<const float*>(smem + OFF_QS + (ns & 1) * 64) + grp * kHg;
             const float* fresh = reinterpret_cast<const float*>(smem + OFF_STG + (ns & 1) * STG_BYTES + 2 * D);
-            const int slot = a.pos[sg.b] % a.w;
             float m[kHg], l[kHg];
             vref = 0.f;
 #pragma unroll
@@ -716,7 +725,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
             for (int t = 0; !stop && t < sg.nt; ++t) {
                 const uint32_t i = gt + t, buf = i & 1;
                 const bool valid = x < sg.n;
-                const bool is_new = x == slot;            // the ring's own scale of it may be read before it is written
+                const bool is_new = x == sg.slot;            // the ring's own scale of it may be read before it is written
                 const float ks = (is_new ? fresh[0] : k_next) * a.scale_log2, vs = is_new ? fresh[1] : v_next;
                 x += kTile;                               // the next tile's scales while this one is worked on
                 k_next = x < sg.n ? sk[x] : 0.f;
@@ -836,7 +845,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(w_full(buf));
                 // the segment before, under this one's first products
-                if (t == 0 && pending && !finish(prev, gt - 1)) stop = true;
+                if (t == 0 && ns > 0 && !finish(ns - 1, gt - 1)) stop = true;
             }
             if (stop) break;
             gt += sg.nt;
@@ -848,11 +857,9 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 if (lane == 0) sums[(warp & 3) * kHg + h] = l[h];
                 if (r == 0) maxima[h] = m[h];
             }
-            prev = sg;
             p_vref = vref;
-            pending = true;
         }
-        if (!stop && pending) finish(prev, gt - 1);
+        if (!stop) finish(ns - 1, gt - 1);
         tmem_wait_ld();
         tmem_wait_st();
     }
