@@ -242,7 +242,7 @@ constexpr uint32_t STG_BYTES = 2 * D + 16;            // the new slot: key and v
 constexpr uint32_t OFF_Q = kNBuf * TILE_BYTES, OFF_W = OFF_Q + 2 * Q_BYTES, OFF_CS = OFF_W + 2 * W_BYTES;
 constexpr uint32_t IN_BYTES = (kMaxH + 2) * D * 2;     // a segment's queries, new key and value
 constexpr uint32_t OFF_IN = OFF_CS + 2 * (D / 2 * 16), OFF_STG = OFF_IN + 2 * IN_BYTES;
-constexpr uint32_t OFF_QS = OFF_STG + 2 * STG_BYTES, OFF_SEG = OFF_QS + 2 * 64, OFF_RED = OFF_SEG + 2 * 32;
+constexpr uint32_t OFF_QS = OFF_STG + 2 * STG_BYTES, OFF_SEG = OFF_QS + 2 * 64, OFF_SC = OFF_SEG + 2 * 32, OFF_RED = OFF_SC + 2 * 2 * kTile * 4;
 constexpr uint32_t OFF_BAR = OFF_RED + kGroups * RED_BYTES;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -437,6 +437,13 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
         if (wi == 0 && lane == 0) *reinterpret_cast<DecSeg*>(smem + OFF_SEG + (n & 1) * 32) = x;
         const bool fresh = slot >= x.t0 * kTile && slot < (x.t0 + x.nt) * kTile;
         for (int j = 32 * wi + lane; j < D / 2; j += 32 * warps) rope_cos_sin(a.base, j, (double)p, cs[j].x, cs[j].y);
+        // the scales of the first tile (the new slot's come from elsewhere: these may be read before it is written)
+        float2* sc = reinterpret_cast<float2*>(smem + OFF_SC) + (n & 1) * kTile;
+        for (int j = 32 * wi + lane; j < kTile; j += 32 * warps) {
+            const int at = x.t0 * kTile + j;
+            const float* src = a.scales + (size_t)x.b * 2 * a.w + at;
+            sc[j] = at < x.n ? make_float2(src[0], src[a.w]) : make_float2(0.f, 0.f);
+        }
         const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(smem + OFF_IN + (n & 1) * IN_BYTES);
         const bool here = wait_w(in_full(n & 1), (n >> 1) & 1, g, 12);
         if (all_or(!here)) return false;             // the angles are there too
@@ -510,11 +517,10 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
 
     if (warp == kWarpTma) {
         if (lane == 0) {
-            // a segment's inputs before the tiles of the segment before it
-            Walk kn = k;
+            // a segment's inputs behind the first tile of the segment before it
             uint32_t L = 0, ns = 0;
             auto load_in = [&]() {
-                if (!next_seg(a, kn, sg)) return true;
+                if (!next_seg(a, k, sg)) return true;
                 const uint32_t e = ns & 1, row_bytes = (uint32_t)a.H * D * 2, in = sb + OFF_IN + e * IN_BYTES;
                 if (ns > 1 && !wait(in_free(e), ((ns >> 1) - 1) & 1, g, 11)) return false;
                 ++ns;
@@ -525,19 +531,20 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 return true;
             };
             bool ok = load_in();
-            while (ok && next_seg(a, k, sg)) {
+            for (bool on = ns > 0; ok && on;) {
                 const DecSeg here = sg;
-                if (!(ok = load_in())) break;
-                sg = here;
-                for (int t = 0; ok && t < sg.nt; ++t)
+                on = !here.last;
+                for (int t = 0; ok && t < here.nt; ++t) {
                     for (int kv = 0; kv < 2; ++kv, ++L) {
                         const uint32_t s = L % kNBuf, u = L / kNBuf;
                         if (u > 0 && !(ok = wait(empty(s), (u - 1) & 1, g, 1))) break;
                         mbar_arrive_expect_tx(full(s), TILE_BYTES);
                         for (int c = 0; c < 2; ++c)
-                            tma_load_2d(sb + s * TILE_BYTES + c * 16384, &map_kv, c * 128, (2 * sg.b + kv) * a.w + (sg.t0 + t) * kTile,
+                            tma_load_2d(sb + s * TILE_BYTES + c * 16384, &map_kv, c * 128, (2 * here.b + kv) * a.w + (here.t0 + t) * kTile,
                                         full(s));
                     }
+                    if (t == 0 && ok) ok = load_in();
+                }
             }
             const uint64_t t0 = globaltimer_ns();
             for (uint32_t l = L > kNBuf ? L - kNBuf : 0; l < L; ++l)
@@ -551,11 +558,10 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint32_t id_s = idesc_fp8(kQRows, 0, 0), id_o = idesc_fp8(kWRows, 1, 1);
         // S runs one tile ahead of the weighted sum, across segments
-        Walk kp = k;
-        DecSeg sp{};
         uint32_t is = 0, ns = 0;                                     // tiles with S issued, segments with S begun
         int ts = 0, slot_s = 0;                                      // the next S: its tile, the segment's new slot from its first
-        bool ok = true, more = next_seg(a, k, sg);
+        bool ok = true, more = next_seg(a, k, sg);                   // the segments themselves: as they were prepared
+        auto seg = [&](uint32_t n) { return *reinterpret_cast<const DecSeg*>(smem + OFF_SEG + (n & 1) * 32); };
         // segment n's new key's (half 0) or value's (1) codes over row `slot` of the tile in buffer s
         auto put_new = [&](uint32_t n, uint32_t s, int slot, int half) {
             if (lane < 16) {
@@ -568,6 +574,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
         auto issue_s = [&]() {
             if (ts == 0) {
                 if (!wait_w(q_ready(ns & 1), (ns >> 1) & 1, g, 10)) return false;
+                sg = seg(ns);
                 slot_s = sg.slot - sg.t0 * kTile;
             }
             const uint32_t l = 2 * is, s = l % kNBuf, buf = is & 1, e = ns & 1;
@@ -590,13 +597,16 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
             if (last) {
                 ts = 0;
                 ++ns;
-                more = next_seg(a, k, sg);
+                more = !sg.last;
             }
             return true;
         };
-        if (more) ok = issue_s();
         uint32_t i = 0, np = 0;
-        for (; ok && next_seg(a, kp, sp); ++np) {
+        bool on = more;
+        if (more) ok = issue_s();
+        for (; ok && on; ++np) {
+            const DecSeg sp = seg(np);
+            on = !sp.last;
             const int slot = sp.slot - sp.t0 * kTile;       // the new slot, from the segment's first
             for (int t = 0; t < sp.nt; ++t, ++i) {
                 if (more && !(ok = issue_s())) break;
@@ -720,7 +730,8 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 l[h] = 0.f;
             }
             int x = sg.t0 * kTile + r;
-            float k_next = x < sg.n ? sk[x] : 0.f, v_next = x < sg.n ? sv[x] : 0.f;
+            const float2 sc0 = reinterpret_cast<const float2*>(smem + OFF_SC)[(ns & 1) * kTile + r];
+            float k_next = sc0.x, v_next = sc0.y;
 #pragma unroll 1
             for (int t = 0; !stop && t < sg.nt; ++t) {
                 const uint32_t i = gt + t, buf = i & 1;
