@@ -10,6 +10,7 @@
 // product with the fp64 reciprocal, off by 2^-52: after the rounding to fp32 a quotient that is exactly
 // on a border, which has 5 bits, is on it again.)
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -241,7 +242,8 @@ constexpr uint32_t RED_BYTES = 192;                   // of a group: [4 warps][k
 constexpr uint32_t STG_BYTES = 2 * D + 16;            // the new slot: key and value codes, their scales
 constexpr uint32_t OFF_Q = kNBuf * TILE_BYTES, OFF_W = OFF_Q + 2 * Q_BYTES, OFF_CS = OFF_W + 2 * W_BYTES;
 constexpr uint32_t IN_BYTES = (kMaxH + 2) * D * 2;     // a segment's queries, new key and value
-constexpr uint32_t OFF_IN = OFF_CS + 2 * (D / 2 * 16), OFF_STG = OFF_IN + 2 * IN_BYTES;
+constexpr uint32_t CS_BYTES = D / 2 * (16 + 8);         // cos, sin in fp64 (the new key), then in fp32 (the queries)
+constexpr uint32_t OFF_IN = OFF_CS + 2 * CS_BYTES, OFF_STG = OFF_IN + 2 * IN_BYTES;
 constexpr uint32_t OFF_QS = OFF_STG + 2 * STG_BYTES, OFF_SEG = OFF_QS + 2 * 64, OFF_SC = OFF_SEG + 2 * 32, OFF_RED = OFF_SC + 2 * 2 * kTile * 4;
 constexpr uint32_t OFF_BAR = OFF_RED + kGroups * RED_BYTES;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;
@@ -431,15 +433,30 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
 
     // Segment n's queries, and its new slot if it holds it, into shared memory (and the ring), by `warps` warps, of which
     // this is number wi
-    auto prepare = [&](const DecSeg& x, uint32_t n, int wi, int warps, double2* cs, auto all_or) {
+    auto prepare = [&](const DecSeg& x, uint32_t n, int wi, auto num_warps, uint8_t* angles, auto all_or) {
+        constexpr int warps = decltype(num_warps)::value;
+        double2* cs = reinterpret_cast<double2*>(angles);
+        float2* csf = reinterpret_cast<float2*>(angles + D / 2 * 16);
         uint8_t* stg = smem + OFF_STG + (n & 1) * STG_BYTES;
         const int p = a.pos[x.b], slot = x.slot;
         if (wi == 0 && lane == 0) *reinterpret_cast<DecSeg*>(smem + OFF_SEG + (n & 1) * 32) = x;
         const bool fresh = slot >= x.t0 * kTile && slot < (x.t0 + x.nt) * kTile;
-        for (int j = 32 * wi + lane; j < D / 2; j += 32 * warps) rope_cos_sin(a.base, j, (double)p, cs[j].x, cs[j].y);
+#pragma unroll
+        for (int j0 = 0; j0 < D / 2; j0 += 32 * warps) {
+            const int j = j0 + 32 * wi + lane;
+            if (j < D / 2) {
+                double2 c;
+                rope_cos_sin(a.base, j, (double)p, c.x, c.y);
+                cs[j] = c;
+                csf[j] = make_float2((float)c.x, (float)c.y);
+            }
+        }
         // the scales of the first tile (the new slot's come from elsewhere: these may be read before it is written)
         float2* sc = reinterpret_cast<float2*>(smem + OFF_SC) + (n & 1) * kTile;
-        for (int j = 32 * wi + lane; j < kTile; j += 32 * warps) {
+#pragma unroll
+        for (int j0 = 0; j0 < kTile; j0 += 32 * warps) {
+            const int j = j0 + 32 * wi + lane;
+            if (j >= kTile) break;
             const int at = x.t0 * kTile + j;
             const float* src = a.scales + (size_t)x.b * 2 * a.w + at;
             sc[j] = at < x.n ? make_float2(src[0], src[a.w]) : make_float2(0.f, 0.f);
@@ -470,7 +487,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
             float mq = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float c = (float)cs[4 * lane + e].x, s = (float)cs[4 * lane + e].y;
+                const float c = csf[4 * lane + e].x, s = csf[4 * lane + e].y;
                 y[e] = z[e] * c - z[4 + e] * s;
                 y[4 + e] = z[4 + e] * c + z[e] * s;
                 mq = fmaxf(mq, fmaxf(fabsf(y[e]), fabsf(y[4 + e])));
@@ -612,8 +629,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 if (more && !(ok = issue_s())) break;
                 const uint32_t l = 2 * i + 1, s = l % kNBuf, buf = i & 1;
                 if (t == 0 && np > 0 && !(ok = wait_w(o_free, (np - 1) & 1, g, 3))) break;
-                if (!(ok = wait_w(full(s), (l / kNBuf) & 1, g, 4))) break;
-                if (!(ok = wait_w(w_full(buf), (i >> 1) & 1, g, 5))) break;
+                if (!(ok = wait_w(full(s), (l / kNBuf) & 1, w_full(buf), (i >> 1) & 1, g, 4))) break;
                 if (slot >= t * kTile && slot < (t + 1) * kTile) put_new(np, s, slot - t * kTile, 1);
                 tc_fence_after();
                 if (elect_one()) {
@@ -645,7 +661,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
         for (uint32_t n = 1; some && (some = next_seg(a, k, sg)); ++n) {
             bool ok = n < 2 || wait_w(q_free(n & 1), ((n >> 1) - 1) & 1, g, 13);
             ok = ok && (n < 2 || wait_w(o_free, (n - 2) & 1, g, 14));
-            if (prep_or(!ok) || !prepare(sg, n, warp - kWarpMma - 1, kPrepWarps, reinterpret_cast<double2*>(smem + OFF_CS) + D / 2, prep_or)) break;
+            if (prep_or(!ok) || !prepare(sg, n, warp - kWarpMma - 1, std::integral_constant<int, kPrepWarps>{}, smem + OFF_CS + CS_BYTES, prep_or)) break;
         }
     } else {
         const int grp = warp >> 2, r = threadIdx.x & 127;            // group; slot of a tile, then column
@@ -710,7 +726,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
         uint32_t ns = 0;
         if (next_seg(a, k, sg)) {                                    // the first segment is prepared by all of these warps
             auto soft_or = [&](bool v) { return named_or(v, 5, kSoft); };
-            stop = !prepare(sg, 0, warp, kSoftWarps, reinterpret_cast<double2*>(smem + OFF_CS), soft_or);
+            stop = !prepare(sg, 0, warp, std::integral_constant<int, kSoftWarps>{}, smem + OFF_CS, soft_or);
         }
         for (bool last = false; !stop && !last; ++ns) {
             if (grp_or(!wait_w(q_ready(ns & 1), (ns >> 1) & 1, g, 12))) {
