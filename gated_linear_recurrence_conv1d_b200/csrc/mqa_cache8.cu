@@ -441,6 +441,16 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
         const int p = a.pos[x.b], slot = x.slot;
         if (wi == 0 && lane == 0) *reinterpret_cast<DecSeg*>(smem + OFF_SEG + (n & 1) * 32) = x;
         const bool fresh = slot >= x.t0 * kTile && slot < (x.t0 + x.nt) * kTile;
+        // the scales of the first tile, stored at the end (the new slot's come from elsewhere: these may be read before it is
+        // written)
+        constexpr int kPer = (kTile + 32 * warps - 1) / (32 * warps);
+        float2 sc[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int j = 32 * (i * warps + wi) + lane, at = x.t0 * kTile + j;
+            const float* src = a.scales + (size_t)x.b * 2 * a.w + at;
+            sc[i] = j < kTile && at < x.n ? make_float2(src[0], src[a.w]) : make_float2(0.f, 0.f);
+        }
 #pragma unroll
         for (int j0 = 0; j0 < D / 2; j0 += 32 * warps) {
             const int j = j0 + 32 * wi + lane;
@@ -450,16 +460,6 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 cs[j] = c;
                 csf[j] = make_float2((float)c.x, (float)c.y);
             }
-        }
-        // the scales of the first tile (the new slot's come from elsewhere: these may be read before it is written)
-        float2* sc = reinterpret_cast<float2*>(smem + OFF_SC) + (n & 1) * kTile;
-#pragma unroll
-        for (int j0 = 0; j0 < kTile; j0 += 32 * warps) {
-            const int j = j0 + 32 * wi + lane;
-            if (j >= kTile) break;
-            const int at = x.t0 * kTile + j;
-            const float* src = a.scales + (size_t)x.b * 2 * a.w + at;
-            sc[j] = at < x.n ? make_float2(src[0], src[a.w]) : make_float2(0.f, 0.f);
         }
         const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(smem + OFF_IN + (n & 1) * IN_BYTES);
         const bool here = wait_w(in_full(n & 1), (n >> 1) & 1, g, 12);
@@ -522,6 +522,11 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 *reinterpret_cast<uint32_t*>(dst) = c[part][0];
                 *reinterpret_cast<uint32_t*>(dst + Q_BYTES / 2) = c[part][1];
             }
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int j = 32 * (i * warps + wi) + lane;
+            if (j < kTile) reinterpret_cast<float2*>(smem + OFF_SC)[(n & 1) * kTile + j] = sc[i];
         }
         fence_proxy_async_smem();
         if (all_or(false)) return false;              // (never: a barrier) every warp's part is there
