@@ -367,14 +367,14 @@ _CODES, _BYTES = (torch.float8_e4m3fn, torch.uint8), (torch.uint8,)
 def _addresses(where: str, *wanted):
     """wanted: (name, tensor or None, shape or None, dtypes) -> the tensors' addresses (None for none).  The C ABI sees
     addresses only, so a tensor of another shape, type or device than the dims say is refused here."""
-    device, out = -1, []
+    device, out = None, []
     for name, t, shape, dtypes in wanted:
         if t is None:
             out.append(None)
             continue
         at = t.get_device()
         if at != device:
-            if at < 0 or device >= 0:
+            if at < 0 or device is not None:
                 raise ValueError(f"{where}: {name} must be a CUDA tensor on the same device as the others, got {t.device}")
             if at != torch._C._cuda_getDevice():
                 raise ValueError(f"{where}: {name} is on {t.device}, the current device is "
