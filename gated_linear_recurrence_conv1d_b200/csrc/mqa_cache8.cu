@@ -134,11 +134,12 @@ __device__ __forceinline__ void turn64(const float (&x)[8], const double2* cs, i
 // ---------------------------------------------------------------- write -------------------------------
 // Block = (token, up to kWriteRows batch rows): the angles of the token's position once for all of them (they are
 // half of the arithmetic), while the rows' keys and values are on their way; a warp per row.  The last min(len, w)
-// tokens of a row go into their slots.
+// tokens of a row go into their slots.  Bound by fp64 arithmetic and latency: 8 rows of 2048 tokens in 13 us, of which
+// the bytes need 4 (a block a row: 22.6 us, its own angles each time; fp64 divisions: 14.4 us).
 constexpr int kWriteRows = 8;
-__global__ void __launch_bounds__(32 * kWriteRows, 6) mqa_cache8_write_kernel(int B, int T, int w, int pos0, RopeBase base,
-                                                                           const int* lengths, const __nv_bfloat16* k,
-                                                                           const __nv_bfloat16* v, uint8_t* codes, float* scales) {
+__global__ void __launch_bounds__(32 * kWriteRows, 6)
+mqa_cache8_write_kernel(int B, int T, int w, int pos0, RopeBase base, const int* lengths, const __nv_bfloat16* k,
+                        const __nv_bfloat16* v, uint8_t* codes, float* scales) {
     __shared__ double2 cs[D / 2];
     const int t = blockIdx.x + (lengths ? 0 : max(0, T - w));
     const int lane = threadIdx.x & 31, b = blockIdx.y * kWriteRows + (threadIdx.x >> 5);
@@ -168,7 +169,8 @@ __global__ void __launch_bounds__(32 * kWriteRows, 6) mqa_cache8_write_kernel(in
 }
 
 // ---------------------------------------------------------------- read ---------------------------------
-// A warp takes kReadSlots slots, a lane 8 codes of each, their loads in flight together: bound by HBM
+// A warp takes kReadSlots slots, a lane 8 codes of each, their loads in flight together: bound by HBM (64 rings of
+// 2048 slots: 34.5 us, 5.9 TB/s; with 4 slots a warp and a division for each 41 us).
 constexpr int kReadSlots = 8, kReadBlock = 8 * kReadSlots;           // slots of a block of 8 warps
 __global__ void __launch_bounds__(256) mqa_cache8_read_kernel(long long slots, int w, const int* pos,
                                                               const uint8_t* codes, const float* scales,
@@ -215,22 +217,26 @@ __global__ void __launch_bounds__(256) mqa_cache8_read_kernel(long long slots, i
 // straight from the codes in shared memory (V^T is the value tile read MN-major).  Four groups of 4 warps, each
 // with every fourth head, thread = slot: s = (S0 + S1 / 16 + S2 / 256) 2^e c scale_k, p = 2^(s - m) with a
 // reference maximum m per head that moves when a score passes it by more than 8 times, and the weight
-// p scale_v, normalised by a power of two vref >= the value scales seen so far, as three e5m2 parts: off by at most 2^-9 of itself, half of what bf16
-// would leave, down to weights of 2^-29 (e4m3 parts end at 2^-16, which shows where one slot has nearly all
-// the weight and a small value).  p adds to the thread's own sum in fp32.  O stays in TMEM for the whole segment; when m or vref
-// moves it is rescaled there (each group has its own vref and its own columns of S, W and O, so within a
-// segment the groups never meet).  A row inside one segment is written at once; else the segments leave (m, sum, O) and
-// mqa_decode8_merge_kernel adds them up in order.  (The segment that finishes last doing that here, by a counter of the
-// row, took longer at the end of the kernel, and its registers spilled the softmax's.)
-// At the beginning of a segment (the first tiles are on their way meanwhile, and after the first segment the last
-// products of the segment before run) the softmax warps rotate the row's queries and write their parts as the B
-// operand: with 2^e the power of two that brings the head's largest element into (224, 448],
-// q~ = 2^e (x0 + x1 / 16 + x2 / 256) + r, x0 = e4m3(q~ 2^-e), x1 = e4m3(16 (q~ 2^-e - x0)), ...: a part is off by at most
-// 2^-4 of itself, so |r| <= 2^-12 |q~| (or 2^-18 448 2^e where x2 is below e4m3's normal numbers), less than
-// bf16 would leave.  The segment that holds the row's new slot also rotates and quantises the new key and value, writes them
-// to the ring and hands them to the MMA warp, which puts them into the tiles that it has (they may have been
-// loaded before the ring was written).
-// The step reads every code once: bound by HBM.
+// p scale_v, normalised by a power of two vref >= the value scales seen so far, as three e5m2 parts: off by at
+// most 2^-9 of itself, half of what bf16 would leave, down to weights of 2^-29 (e4m3 parts end at 2^-16, which
+// shows where one slot has nearly all the weight and a small value).  p adds to the thread's own sum in fp32.  O
+// stays in TMEM for the whole segment; when m or vref moves it is rescaled there (each group has its own vref and
+// its own columns of S, W and O, so within a segment the groups never meet).  A row inside one segment is written
+// at once; else the segments leave (m, sum, O) and mqa_decode8_merge_kernel adds them up in order.  (The segment
+// that finishes last doing that here, by a counter of the row, took longer at the end of the kernel, and its
+// registers spilled the softmax's.)
+// Before a segment its row's queries are rotated and their parts written as the B operand: with 2^e the power of two that
+// brings the head's largest element into (224, 448], q~ = 2^e (x0 + x1 / 16 + x2 / 256) + r, x0 = e4m3(q~ 2^-e),
+// x1 = e4m3(16 (q~ 2^-e - x0)), ...: a part is off by at most 2^-4 of itself, so |r| <= 2^-12 |q~| (or
+// 2^-18 448 2^e where x2 is below e4m3's normal numbers), less than bf16 would leave.  The segment that holds the
+// row's new slot also rotates and quantises the new key and value, writes them to the ring and hands them to the
+// MMA warp, which puts them into the tiles that it has (they may have been loaded before the ring was written).
+// All softmax warps prepare a CTA's first segment; two warps of their own the next one while a segment is worked on,
+// with two buffers for everything prepared.  S runs one tile ahead of the weighted sum, across segments, and a
+// segment's output is written after the first weights of the next.
+// The step reads every code once: bound by HBM.  256 full rings of 2048 slots, 10 heads: 55.7 us (272 MB; streaming
+// alone would take 42), of which about 10 us pass at the two ends (the angles, the first tile's way through, the merge) and
+// 3.5 us at each change of the row; a tile of 64 KB takes 1.39 us, and 1.05 us when the rings are in L2.
 constexpr uint32_t TILE_BYTES = kTile * D;            // 32768: 2 boxes of [128 slots x 128 B]
 constexpr int kNBuf = 5;
 constexpr int kMaxCtas = 148;
@@ -904,7 +910,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
 }
 
 // The rows of several segments from their parts, in order: block = (head, row), thread = 4 columns.  A row without a token
-// is zero.
+// is zero.  Bound by latency (two dependent loads, then the parts of a row together): 1.5 us behind the attention.
 constexpr int kMergeLoads = 8;         // parts in flight
 __global__ void __launch_bounds__(D / 4, 12) mqa_decode8_merge_kernel(int H, const int* pos, const int2* meta, const float* part,
                                                                   __nv_bfloat16* out) {

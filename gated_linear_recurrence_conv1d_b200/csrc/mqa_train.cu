@@ -72,7 +72,7 @@ __device__ __forceinline__ int scan_before(int v, int start, int* warp_v, int& a
 // Blocks [0, B): a row's first key of every token, lo = max(0, t - w + 1, start of its document), and the last token
 // that sees it, last = min(T - 1, t + w - 1, end of its document): a running maximum forwards and a running
 // minimum backwards over the tokens that start a document.  The other blocks: cosine and sine of position
-// pos0 + t, pair j, [T][d/2], angle and reduction in fp64.
+// pos0 + t, pair j, [T][d/2], angle and reduction in fp64.  Bound by latency: 4 us, 9 us at 8 rows of 2048 tokens.
 __global__ void __launch_bounds__(kScanThreads) mqa_prepare_kernel(int B, int T, int w, const uint8_t* reset, int* lo, int* last,
                                                                    int pos0, RopeBase base, float2* cs) {
     pdl_launch();
@@ -143,7 +143,8 @@ __global__ void __launch_bounds__(kScanThreads) mqa_prepare_kernel(int B, int T,
 }
 
 // Blocks but the last: 16 threads a token, 8 pairs each, over its H query heads and its key: bound by HBM (q and k in
-// and out), so the rows of a few heads are in flight together.  The last block: the line of (key tile, row
+// and out: 185 MB for 16384 tokens of 10 heads, 43 us), so the rows of a few heads are in flight together.  The
+// last block: the line of (key tile, row
 // tile) products that the backward cuts into pieces: cum[j] = the row tiles of the key tiles before j, a
 // key tile's rows being those from its first key's token to the last token that sees its last key.
 constexpr int kTurnRows = 4, kTurnThreads = 256, kKeyTile = 128, kRowTile = 64;
@@ -286,7 +287,10 @@ struct QTiles {
 // Beside out the forward keeps the next 8 bits of each of its elements for delta = dO . out.  Where one key holds nearly
 // all of a row's weight, dP of that key and delta cancel: dS is what the small weights leave of the difference,
 // and a delta from out in bf16, or from weights that do not sum to one, was off by more than dS itself (documents
-// of 2 tokens: dq off by 0.5 to 30 %, now by 0.3 %).  The bytes cost HBM time of 1.3 KB a row instead of 1.
+// of 2 tokens: dq off by 0.5 to 30 %, now by 0.3 %).  The bytes cost 8 us of the 145.
+// Bound by the tensor pipe and its hand-overs: 8 rows of 2048 tokens, 10 heads, window 2048 (172 GFLOP) in 145 us,
+// 1.18 PFLOP/s.  The exponentials take about half of a key tile's 2048 tensor cycles, in pairs of fp32 operations
+// with everything around them.
 namespace fw {
 // Two fp32 values rounded to bf16 (to nearest, ties away from zero, so that bit 15 of the value alone says whether
 // it was rounded up), and bits 8 to 15 of four: as a signed byte, what to add to the rounded value's bits
@@ -662,8 +666,9 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 // pipe, so each has the other two's time to arrive, and dS of tile j is formed under S of tile j + 1.
 // 8 warps, thread = (row, 64 of the 128 keys): P = 2^(c s - L), dS = P (dP - delta), the row's L and delta in
 // registers.  dq of a query tile is written after the first dS of the next.
-// (Key tiles of 64 with two buffers of S and dP: 1.5 times slower.  An MMA of N 64 reads 5 KB of shared memory a CTA
-// in the time of 32 cycles, one of N 128 6 KB in 64, and shared memory gives 128 bytes a cycle.)
+// (Key tiles of 64 with two buffers of S and dP: 242 us instead of 202.  An MMA of N 64 reads 5 KB of shared memory a
+// CTA in the time of 32 cycles, one of N 128 6 KB in 64, and shared memory gives 128 bytes a cycle.)
+// Bound by the tensor pipe: 8 x 2048 tokens, 10 heads, window 2048 (258 GFLOP) in 187 us, 1.38 PFLOP/s.
 namespace bq {
 constexpr int BK = 128;
 constexpr uint32_t SLOT = 32768;
@@ -1002,6 +1007,9 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 // (cum = the line's length before each key tile), so that every cluster has the same work whatever the
 // documents; a piece of a key tile leaves its sums in fp32 as part number (cluster + key tile), and
 // mqa_dkv_sum_kernel adds the parts of a key tile in order: the same bits at every run.
+// Bound by shared memory and the tensor pipe together (a row tile's operands are read twice, 64 rows at a time):
+// 8 x 2048 tokens, 10 heads, window 2048 (344 GFLOP) in 303 us, 1.13 PFLOP/s.  (Row tiles of 128, which need P^T in
+// shared memory: 448 us.  Both warpgroups on every row tile: 337 us.)
 namespace bk {
 constexpr int BR = kRowTile, BKEY = kKeyTile;
 constexpr uint32_t SLOT = 32768;
@@ -1361,7 +1369,8 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 }
 
 // The sum of a key tile's parts in the clusters' order; dk is scaled and turned back.  Thread = (key, 4 columns of the
-// first half and their partners of the second); block = 32 keys x 32 columns twice; z = 0: dv, 1: dk.
+// first half and their partners of the second); block = 32 keys x 32 columns twice; z = 0: dv, 1: dk.  Bound by reading the
+// parts (128 KB each: 53 MB at 128 key tiles and 74 clusters, mostly still in L2).
 __global__ void __launch_bounds__(256) mqa_dkv_sum_kernel(const Args a, int G) {
     using namespace bk;
     pdl_launch();
@@ -1401,8 +1410,8 @@ __global__ void __launch_bounds__(256) mqa_dkv_sum_kernel(const Args a, int G) {
 }
 
 // ---------------------------------------------------------------- backward: delta ------------------------
-// delta = dO . out per query row (a warp takes kDeltaRows rows, their loads in flight together: bound by HBM), of out in
-// the 16 bits of significand that the forward kept of it
+// delta = dO . out per query row, of out in the 16 bits of significand that the forward kept of it.  A warp takes kDeltaRows
+// rows, their loads in flight together: bound by HBM (1280 bytes a row; 210 MB for 163840 rows: 32 us).
 constexpr int kDeltaRows = 4, kDeltaWarps = 8;
 __device__ __forceinline__ float with_low(uint32_t hi, uint32_t byte) {
     return __uint_as_float(hi + (uint32_t)((int)(byte << 24) >> 16));

@@ -125,7 +125,11 @@ def test_decode_steps_match_the_oracle(B, H, w, start, steps):
     assert binding.read_device_status(ws) == binding.RGLRU_OK
 
 
-@pytest.mark.parametrize("B,H,w", [(80, 10, 2048), (160, 4, 700), (7, 16, 333)])
+@pytest.mark.parametrize("B,H,w", [
+    (80, 10, 2048), (160, 4, 700), (7, 16, 333),
+    (1300, 5, 100),                    # many short rings, several to an SM
+    (500, 16, 300),
+])
 def test_decode_of_rows_at_any_point(B, H, w):
     """Full and partly filled rings of values of many sizes, empty rows among them."""
     rng = np.random.default_rng([1, B])
@@ -151,6 +155,55 @@ def test_decode_of_rows_at_any_point(B, H, w):
         else:
             _close(g[b], y, a, f"row {b} pos {pos[b]}")
     _same(codes, scales, c, s)
+
+
+def test_decode_without_any_token():
+    rng = np.random.default_rng(12)
+    B, H, w = 9, 4, 50
+    c, s = _ring(rng, B, w)
+    codes, scales, pos = _dev(c), _dev(s), torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    x = [binding.to_device(_bf16(rng, sh)) for sh in ((B, H, D), (B, D), (B, D))]
+    dims = binding.make_mqa_dims(B, 1, H, D, w)
+    ws = torch.full((binding.mqa_decode8_workspace_size(dims),), 0xff, dtype=torch.uint8, device="cuda")
+    ws[:16] = 0
+    out = torch.full((B, H, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    binding.mqa_decode8(dims, *x, pos, codes, scales, out, ws)
+    assert torch.all(out == 0)
+    _same(codes, scales, c, s)
+    assert binding.read_device_status(ws) == binding.RGLRU_OK
+
+
+def test_decode_graphs_that_share_a_workspace():
+    """Two captured decodes of unequal shapes in one workspace, replayed in turn on one stream."""
+    rng = np.random.default_rng(13)
+    cases = []
+    for B, H, w in ((3, 16, 600), (200, 2, 130)):
+        c, s = _ring(rng, B, w)
+        x = [binding.to_device(_bf16(rng, sh)) for sh in ((B, H, D), (B, D), (B, D))]
+        pos = torch.tensor(rng.integers(-1, 2 * w, B).astype(np.int32), device="cuda")
+        cases.append(dict(dims=binding.make_mqa_dims(B, 1, H, D, w), x=x, pos=pos, ring=(_dev(c), _dev(s)), out=torch.zeros_like(x[0])))
+    ws = binding.alloc_workspace(max(binding.mqa_decode8_workspace_size(m["dims"]) for m in cases))
+
+    def step(m, stream=None):
+        binding.mqa_decode8(m["dims"], *m["x"], m["pos"], *m["ring"], m["out"], ws, stream=stream)
+
+    want = []
+    for m in cases:
+        step(m)
+        want.append(m["out"].clone())
+    torch.cuda.synchronize()
+    stream, graphs = torch.cuda.Stream(), []
+    for m in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            step(m, stream)
+        graphs.append(g)
+    for _ in range(5):
+        for m, g, y in zip(cases, graphs, want):
+            m["out"].fill_(float("nan"))
+            g.replay()
+            assert torch.equal(m["out"], y)
+    assert binding.read_device_status(ws) == binding.RGLRU_OK
 
 
 def test_decode_of_keys_and_values_of_unequal_sizes():
