@@ -244,6 +244,12 @@ struct Args {
 // lo_t is non-decreasing in t, so a tile's keys are [lo of its first token, its last token].
 struct QTile {
     int b, r0, lo, t1;          // batch row, first query row of the pair, first key, last token
+    // The last key tile may hold no key that a row sees in its second half: then S has 64 columns, 32 keys of each CTA, and
+    // the product with V or K half the keys (3 % of the step's products at 1000 keys a row).
+    template <int BK>
+    __device__ __forceinline__ bool half(int j) const {
+        return t1 + 1 - (lo + j * BK) <= BK / 2;
+    }
 };
 // walks a pair's tiles; the load of the next tile's first key is in flight while a tile is worked on
 template <int BK>
@@ -378,7 +384,7 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         tma_load_3d_pair(dst + c * 16384, &map_v, (int)rank * 128 + c * 64, key0, q.b, bar);
                 } else {
                     for (int c = 0; c < 4; ++c)
-                        tma_load_3d_pair(dst + c * 8192, &map_k, c * 64, key0 + (int)rank * 64, q.b, bar);
+                        tma_load_3d_pair(dst + c * 8192, &map_k, c * 64, key0 + (int)rank * (q.half<BK>(j) ? 32 : 64), q.b, bar);
                 }
                 ++L;
                 return true;
@@ -431,7 +437,7 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     } else if (warp == kWarpMma) {
         if (rank == 0) {
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t id_s = idesc_bf16(256, BK, 0), id_o = idesc_bf16(256, D, 1);
+            const uint32_t id_full = idesc_bf16(256, BK, 0), id_half = idesc_bf16(256, BK / 2, 0), id_o = idesc_bf16(256, D, 1);
             // S runs two key tiles ahead of P V, across query tiles
             QTiles<BK> qs(a, pair, npairs), qp = qs;
             int js = 0;
@@ -441,7 +447,7 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             auto issue_s = [&]() {                                   // S of the next key tile, from the next slot (which is there)
                 if (js == 0 && !wait_w(q_full, qs.k & 1, g, 3)) return false;
                 tc_fence_after();
-                const uint32_t s = L % NSLOT, buf = gs & 1;
+                const uint32_t s = L % NSLOT, buf = gs & 1, id_s = qs.t.half<BK>(js) ? id_half : id_full;
                 ++L;
                 ++gs;
                 const bool last = ++js == qs.n;
@@ -470,13 +476,15 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     if (!(ok = wait_w(p_full(buf), (gt >> 1) & 1, full(s), (L / NSLOT) & 1, full(lk % NSLOT), (lk / NSLOT) & 1, g, 6))) break;
                     ++L;
                     tc_fence_after();
+                    const int steps = qp.t.half<BK>(j) ? BK / 32 : BK / 16;
                     if (elect_one()) {                               // O += P_j V_j
                         // P of keys [16 ks, 16 ks + 16): the two halves of a row sit 64 columns apart
 #pragma unroll
                         for (int ks = 0; ks < BK / 16; ++ks)
-                            mma_ts_pair(tm + TM_O, tm + TM_S + buf * BK + (ks >> 2) * 64 + (ks & 3) * 8,
-                                        desc_mn_sw128(sb + OFF_SLOT + s * SLOT + ks * 2048, 16384), id_o,
-                                        (j > 0 || ks > 0) ? 1u : 0u);
+                            if (ks < steps)
+                                mma_ts_pair(tm + TM_O, tm + TM_S + buf * BK + (ks >> 2) * 64 + (ks & 3) * 8,
+                                            desc_mn_sw128(sb + OFF_SLOT + s * SLOT + ks * 2048, 16384), id_o,
+                                            (j > 0 || ks > 0) ? 1u : 0u);
                         mma_commit_pair(o_done(buf));
                         mma_commit_pair(empty(s));
                     }
@@ -747,7 +755,8 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         tma_load_3d_pair(sb + OFF_SLOT + slot * SLOT + c * 16384, m, (int)rank * 128 + c * 64, key0, q.b, full(slot) + lead);
                 } else {                                             // this CTA's 64 keys, all columns
                     for (int c = 0; c < 4; ++c)
-                        tma_load_3d_pair(sb + OFF_SLOT + slot * SLOT + c * 8192, m, c * 64, key0 + (int)rank * 64, q.b, full(slot) + lead);
+                        tma_load_3d_pair(sb + OFF_SLOT + slot * SLOT + c * 8192, m, c * 64, key0 + (int)rank * (q.half<BK>(j) ? 32 : 64), q.b,
+                                         full(slot) + lead);
                 }
                 return true;
             };
@@ -807,13 +816,14 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     } else if (warp == kWarpMma) {
         if (rank == 0) {
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t id_s = idesc_bf16(256, BK, 0), id_q = idesc_bf16(256, D, 1);
+            const uint32_t id_full = idesc_bf16(256, BK, 0), id_half = idesc_bf16(256, BK / 2, 0), id_q = idesc_bf16(256, D, 1);
             QTiles<BK> qs(a, pair, npairs), qd = qs;                 // S and dP run one key tile ahead of dQ, across query tiles
             int js = 0;
             uint32_t i = 0;                                          // the key tile whose dQ is next
             bool more = qs.advance(a), ok = true;
             // 256 rows (at off_a) times the 128 keys in a slot (which are there)
             auto issue = [&](uint32_t off_a, uint32_t d, uint32_t slot, uint32_t done, uint32_t rows_free) {
+                const uint32_t id_s = qs.t.half<BK>(js) ? id_half : id_full;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -848,13 +858,15 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     if (j == 0 && qd.k > 0 && !(ok = wait_w(dq_free, (qd.k - 1) & 1, g, 8))) break;
                     if (!(ok = wait_w(ds_full, i & 1, full(KD), i & 1, g, 6))) break;
                     tc_fence_after();
+                    const int steps = qd.t.half<BK>(j) ? BK / 32 : BK / 16;
                     if (elect_one()) {
                         // dS of keys [16 ks, 16 ks + 16): the two halves of a row sit 64 columns apart
 #pragma unroll
                         for (int ks = 0; ks < BK / 16; ++ks)
-                            mma_ts_pair(tm + TM_DQ, tm + TM_DP + (ks >> 2) * 64 + (ks & 3) * 8,
-                                        desc_mn_sw128(sb + OFF_SLOT + KD * SLOT + ks * 2048, 16384), id_q,
-                                        (j > 0 || ks > 0) ? 1u : 0u);
+                            if (ks < steps)
+                                mma_ts_pair(tm + TM_DQ, tm + TM_DP + (ks >> 2) * 64 + (ks & 3) * 8,
+                                            desc_mn_sw128(sb + OFF_SLOT + KD * SLOT + ks * 2048, 16384), id_q,
+                                            (j > 0 || ks > 0) ? 1u : 0u);
                         mma_commit_pair(empty(KD));
                         if (j == qd.n - 1) mma_commit_pair(dq_done);
                     }
