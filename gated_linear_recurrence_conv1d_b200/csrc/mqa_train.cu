@@ -292,8 +292,8 @@ struct QTiles {
 // of the next tile runs under the softmax of this one.
 // Beside out the forward keeps the next 8 bits of each of its elements for delta = dO . out.  Where one key holds nearly
 // all of a row's weight, dP of that key and delta cancel: dS is what the small weights leave of the difference,
-// and a delta from out in bf16, or from weights that do not sum to one, was off by more than dS itself (documents
-// of 2 tokens: dq off by 0.5 to 30 %, now by 0.3 %).  The bytes cost 8 us of the 145.
+// and a delta from out in bf16, or from weights that do not sum to one, can be off by more than dS itself (rows of two
+// keys: dq of a row off by up to 6 %, over many rows 0.45 % RMS instead of 0.34 %).  The bytes cost 8 us of the 145.
 // Bound by the tensor pipe and its hand-overs: 8 rows of 2048 tokens, 10 heads, window 2048 (172 GFLOP) in 145 us,
 // 1.18 PFLOP/s.  The exponentials take about half of a key tile's 2048 tensor cycles, in pairs of fp32 operations
 // with everything around them.

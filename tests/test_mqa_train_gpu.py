@@ -130,23 +130,23 @@ def test_score_scales(scale):
 
 
 def test_short_documents():
-    """Rows of one and two keys: dS_1 = -dS_2 = P_1 P_2 (dP_1 - dP_2), what is left where dP_1 and delta cancel if
-    P_2 is small.  Four roundings enter it (q~ and k~ through the scores, the weights behind out, dS), and the
-    other factor and the result: inside the seven of the RMS bar, as long as delta itself is finer than bf16."""
+    """Rows of one and two keys: dS_1 = -dS_2 = P_1 P_2 (dP_1 - dP_2), what is left where dP_1 and delta cancel."""
     B, T, H = 2, 64, 16
-    x, reset = _problem(B, T, H, seed=21)
+    x, _ = _problem(B, T, H, seed=21)
     reset = np.zeros((B, T), dtype=np.uint8)
     reset[:, ::2] = 1
     ref = mqa_train.train_step(x["q"], x["k"], x["v"], x["dout"], 2048, reset)
     _close(Run(x, reset, 2048).step(), ref, "documents of two")
 
 
-@pytest.mark.parametrize("w,scale", [(2, 0.67), (2, 0.25), (5, 0.67)])
-def test_gradients_where_one_key_has_nearly_all_the_weight(w, scale):
-    """Scores that lie several units apart and have no rounding error: the queries and keys fill only pairs whose
-    angle is below 1e-8, so turning them leaves bf16 values in [1/2, 1] as they are.  What is rounded is the
-    weights behind out (a weight that is a fraction P of the row's moves delta by P 2^-8 of its dP), dS, the
-    result: three of the seven of the RMS bar."""
+@pytest.mark.parametrize("scale", [0.67, 0.25])
+def test_gradients_where_one_key_has_nearly_all_the_weight(scale):
+    """A window of two, and scores that lie several units apart without a rounding error: the queries and keys fill
+    only pairs whose angle is below 1e-8, so turning them leaves their bf16 values as they are.  Then
+    dS_1 = P_1 P_2 (dP_1 - dP_2) = -dS_2 and dq = scale (dS_1 k_1 + dS_2 k_2).  Relative to dS: the weights behind out
+    are rounded (2^-8 each of the two), dS itself is (2^-8), a score is off by fp32 sums (256 terms, 2^-16 of 50: under
+    2^-10), so 4 2^-8.  Relative to the products behind the difference: out has 16 bits in delta (2^-15), the fp32
+    sums of dP and delta 256 2^-24 each: P_j 2^-15 of sum |dO| |out| and 2^-15 of sum |dO| |v|.  The result: 2^-8."""
     B, T, H = 3, 33, 5
     rng = np.random.default_rng(77)
     x, _ = _problem(B, T, H, seed=22)
@@ -155,10 +155,23 @@ def test_gradients_where_one_key_has_nearly_all_the_weight(w, scale):
         a[..., :64] = 0.0
         a[..., 128:192] = 0.0
         x[n] = inputs.f32_to_bf16_bits(a.astype(np.float32))
-    ref = mqa_train.train_step(x["q"], x["k"], x["v"], x["dout"], w, scale=scale, base=1e20)
-    run = Run(x, None, w, scale=scale)
+    ref = mqa_train.train_step(x["q"], x["k"], x["v"], x["dout"], 2, scale=scale, base=1e20)
+    run = Run(x, None, 2, scale=scale)
     run.dims.rope_base = 1e20
-    _close(run.step(), ref, f"w{w} scale {scale}")
+    _close(run.step(), ref, f"scale {scale}")
+
+    q, k, v, g = (inputs.bf16_bits_to_f32(x[n]).astype(np.float64) for n in ("q", "k", "v", "dout"))
+    q, g, out = q[:, 1:], g[:, 1:], ref["out"][:, 1:]
+    k1, k2, v1, v2 = (y[:, :, None] for y in (k[:, :-1], k[:, 1:], v[:, :-1], v[:, 1:]))
+    dot = lambda a, b: np.sum(a * b, -1, keepdims=True)  # noqa: E731
+    s = scale * (dot(q, k2) - dot(q, k1))
+    p1, p2 = 1.0 / (1.0 + np.exp(s)), 1.0 / (1.0 + np.exp(-s))
+    ds = np.abs(p1 * p2 * (dot(g, v1) - dot(g, v2)))
+    terms = dot(np.abs(g), np.abs(out)) + np.maximum(dot(np.abs(g), np.abs(v1)), dot(np.abs(g), np.abs(v2)))
+    tol = scale * (4 * 2.0 ** -8 * ds * (np.abs(k1) + np.abs(k2)) + 2.0 ** -15 * terms * (p1 * np.abs(k1) + p2 * np.abs(k2)))
+    err = np.abs(to_np(run.r["dq"])[:, 1:] - ref["dq"][:, 1:])
+    assert np.min(np.minimum(p1, p2)) < 1e-3
+    assert np.all(err <= tol + 2.0 ** -8 * np.abs(ref["dq"][:, 1:])), float(np.max(err / np.maximum(tol, 1e-30)))
 
 
 def test_gradient_against_differences():
