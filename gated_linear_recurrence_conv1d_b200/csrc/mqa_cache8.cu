@@ -234,9 +234,9 @@ __global__ void __launch_bounds__(256) mqa_cache8_read_kernel(long long slots, i
 // All softmax warps prepare a CTA's first segment; two warps of their own the next one while a segment is worked on,
 // with two buffers for everything prepared.  S runs one tile ahead of the weighted sum, across segments, and a
 // segment's output is written after the first weights of the next.
-// The step reads every code once: bound by HBM.  256 full rings of 2048 slots, 10 heads: 55.7 us (272 MB; streaming
+// The step reads every code once: bound by HBM.  256 full rings of 2048 slots, 10 heads: 55.0 us (272 MB; streaming
 // alone would take 42), of which about 10 us pass at the two ends (the angles, the first tile's way through, the merge) and
-// 3.5 us at each change of the row; a tile of 64 KB takes 1.39 us, and 1.05 us when the rings are in L2.
+// 2.5 us at each change of the row; a tile of 64 KB takes 1.39 us, and 1.05 us when the rings are in L2.
 constexpr uint32_t TILE_BYTES = kTile * D;            // 32768: 2 boxes of [128 slots x 128 B]
 constexpr int kNBuf = 5;
 constexpr int kMaxCtas = 148;
@@ -909,14 +909,19 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
     }
 }
 
-// The rows of several segments from their parts, in order: block = (head, row), thread = 4 columns.  A row without a token
-// is zero.  Bound by latency (two dependent loads, then the parts of a row together): 1.5 us behind the attention.
-constexpr int kMergeLoads = 8;         // parts in flight
-__global__ void __launch_bounds__(D / 4, 12) mqa_decode8_merge_kernel(int H, const int* pos, const int2* meta, const float* part,
-                                                                  __nv_bfloat16* out) {
+// The rows of several segments from their parts, in order: block = (kHeads heads, row), thread = 4 columns, kLoads parts
+// in flight.  A row without a token is zero.  Bound by latency (two dependent loads, then the parts of a row together).
+// <1, 8> while there are fewer rows than CTAs, so that a row may have many parts (one ring of 2048: 16, two rounds of
+// loads).  Else <2, 4>: most rows have one to three parts, and the blocks, half as many, are resident together (256
+// rings of 2048: a step of 55.0 us instead of 55.6; 592 rings of 896, every row in one piece: 57.2 instead of 59.6).
+template <int kHeads, int kLoads>
+__global__ void __launch_bounds__(kHeads * D / 4, kHeads == 1 ? 12 : 9)
+mqa_decode8_merge_kernel(int H, const int* pos, const int2* meta, const float* part, __nv_bfloat16* out) {
     pdl_launch();
     pdl_wait();
-    const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x, pitch = part_pitch(H);
+    const int h = blockIdx.x * kHeads + threadIdx.x / (D / 4), b = blockIdx.y, t = threadIdx.x % (D / 4);
+    const int pitch = part_pitch(H);
+    if (h >= H) return;
     uint2* row = reinterpret_cast<uint2*>(out + ((size_t)b * H + h) * D) + t;
     const int p = pos[b];
     // Not written for a row without a token.  Kept inside the parts, for a pos that was changed under way (a caller's
@@ -932,11 +937,11 @@ __global__ void __launch_bounds__(D / 4, 12) mqa_decode8_merge_kernel(int H, con
     float mx = -INFINITY, l = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int c0 = 0; c0 < np; c0 += kMergeLoads) {
-        float m[kMergeLoads], s[kMergeLoads];
-        float4 z[kMergeLoads];
+    for (int c0 = 0; c0 < np; c0 += kLoads) {
+        float m[kLoads], s[kLoads];
+        float4 z[kLoads];
 #pragma unroll
-        for (int i = 0; i < kMergeLoads; ++i) {
+        for (int i = 0; i < kLoads; ++i) {
             m[i] = -INFINITY;
             if (c0 + i < np) {
                 const float* pc = p0 + (size_t)(c0 + i) * pitch;
@@ -947,12 +952,12 @@ __global__ void __launch_bounds__(D / 4, 12) mqa_decode8_merge_kernel(int H, con
         }
         float mn = mx;
 #pragma unroll
-        for (int i = 0; i < kMergeLoads; ++i) mn = fmaxf(mn, m[i]);
+        for (int i = 0; i < kLoads; ++i) mn = fmaxf(mn, m[i]);
         const float old = mx == -INFINITY ? 0.f : ex2_approx(mx - mn);
         l *= old;
         y = make_float4(y.x * old, y.y * old, y.z * old, y.w * old);
 #pragma unroll
-        for (int i = 0; i < kMergeLoads; ++i)
+        for (int i = 0; i < kLoads; ++i)
             if (c0 + i < np) {
                 const float f = ex2_approx(m[i] - mn);
                 l = fmaf(s[i], f, l);
@@ -1027,18 +1032,22 @@ cudaError_t launch_mqa_decode8(const rglru_mqa_dims* d, const void* q, const voi
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<long long>(tiles, std::min(sms, kMaxCtas)));
+    const int ctas = (int)std::min<long long>(tiles, std::min(sms, kMaxCtas));
+    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, mqa_decode8_kernel, mkv, a)) != cudaSuccess) return e;
-    cfg.gridDim = dim3(d->q_heads, B);
-    cfg.blockDim = dim3(D / 4);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, mqa_decode8_merge_kernel, d->q_heads, pos, static_cast<const int2*>(a.meta),
-                              static_cast<const float*>(a.part), a.out);
+    auto merge = [&](auto kern, int heads) {
+        cfg.gridDim = dim3((d->q_heads + heads - 1) / heads, B);
+        cfg.blockDim = dim3(heads * D / 4);
+        return cudaLaunchKernelEx(&cfg, kern, d->q_heads, pos, static_cast<const int2*>(a.meta), static_cast<const float*>(a.part),
+                                  a.out);
+    };
+    return B < ctas ? merge(mqa_decode8_merge_kernel<1, 8>, 1) : merge(mqa_decode8_merge_kernel<2, 4>, 2);
 }
 
 cudaError_t launch_mqa_cache8_read(const rglru_mqa_dims* d, const void* codes, const float* scales, const int* pos,
