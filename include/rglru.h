@@ -280,17 +280,17 @@ RGLRU_API rglru_status rglru_mqa_decode(const rglru_mqa_dims* dims, const void* 
 RGLRU_API size_t rglru_mqa_save_size(const rglru_mqa_dims* dims);
 RGLRU_API size_t rglru_mqa_train_workspace_size(const rglru_mqa_dims* dims);
 
-/* q [B, T, H, d], k, v [B, T, d] -> out [B, T, H, d], and *save.  Errors as rglru_mqa_prefill; a save
- * that is missing or smaller than the queried size is WORKSPACE. */
+/* q [B, T, H, d], k, v [B, T, d] -> out [B, T, H, d], and *save, neither of which may alias an input.
+ * Errors as rglru_mqa_prefill; a save that is missing or smaller than the queried size is WORKSPACE. */
 RGLRU_API rglru_status rglru_mqa_forward(const rglru_mqa_dims* dims, const void* q, const void* k, const void* v,
                                          const uint8_t* reset, int pos0, void* out, void* save, size_t save_bytes,
                                          void* workspace, size_t workspace_bytes, void* stream);
 
-/* With v the forward's values, out its output and dout [B, T, H, d] = dL/dout, writes the gradients
- * of L: dq [B, T, H, d], dk, dv [B, T, d] (bf16, overwritten; dk and dv are summed over the query
- * heads and every query that sees the key, in fp32).  The result does not depend on the order in
- * which the GPU runs its blocks: the same call gives the same bits.  Outputs must not alias inputs
- * or each other.  Errors as rglru_mqa_forward. */
+/* With v the forward's values, out its output, unchanged (save holds further bits of it), and dout
+ * [B, T, H, d] = dL/dout, writes the gradients of L: dq [B, T, H, d], dk, dv [B, T, d] (bf16,
+ * overwritten; dk and dv are summed over the query heads and every query that sees the key, in
+ * fp32).  The result does not depend on the order in which the GPU runs its blocks: the same call
+ * gives the same bits.  Outputs must not alias inputs or each other.  Errors as rglru_mqa_forward. */
 RGLRU_API rglru_status rglru_mqa_backward(const rglru_mqa_dims* dims, const void* v, const void* out, const void* dout,
                                           const void* save, size_t save_bytes, void* dq, void* dk, void* dv,
                                           void* workspace, size_t workspace_bytes, void* stream);

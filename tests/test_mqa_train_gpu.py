@@ -1,10 +1,10 @@
 """rglru_mqa_forward / rglru_mqa_backward against the fp64 oracle of oracle/mqa_train.py on the same bf16 inputs.
 
 Tolerances.  The kernels round to bf16 (half a step: 2^-8 relative) the rotated queries and keys, the softmax
-weights P, the gradient of the scores dS, the saved output behind delta, and the result; sums are fp32.
+weights P, the gradient of the scores dS, and the result; delta sees the output with 16 bits; sums are fp32.
   * RMS: every one of these roundings is off by 2^-8 u, u uniform in [0, 1] over a step and halved where the
     mantissa is large: 1.7e-3 RMS relative.  A gradient chains at most seven of them that are independent
-    (q~, k~ in the scores, P or dS twice, delta, the other factor, the result): sqrt(7) 1.7e-3 = 4.5e-3, so
+    (q~, k~ in the scores, P or dS twice, the weights behind delta, the other factor, the result): sqrt(7) 1.7e-3 = 4.5e-3, so
     5e-3, the framework's bar for bf16.  2^-16 of the RMS of the terms' absolute sums is added: where the
     terms cancel exactly (a token that sees one key only), what remains is fp32 rounding of those terms.
   * Element by element: |g - r| <= 2^-5 a, a = the sum of the absolute values of the terms (rounding a factor
