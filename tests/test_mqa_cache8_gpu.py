@@ -330,3 +330,33 @@ def test_decode_on_two_streams_and_replayed():
         f2 = (f[0].clone(), f[1].clone(), torch.empty_like(a))
         step(m, f2)
         assert torch.equal(a, f2[2]), p
+
+
+def test_rings_past_32_bits():
+    """2100 rings of 4096 slots are 4.4 10^9 bytes: the last rows agree with the same rows in a batch of their own (bf16
+    of sums in another order: one step of 2^-7), and their new slots are the same bytes."""
+    B, H, w, n = 2100, 3, 4096, 2
+    rng = np.random.default_rng(21)
+    codes = torch.randint(0, 0x70, (B, 2, w, D), dtype=torch.uint8, device="cuda")
+    scales = torch.rand(B, 2, w, device="cuda") * 0.01
+    x = [binding.to_device(_bf16(rng, s)) for s in ((B, H, D), (B, D), (B, D))]
+    pos = torch.full((B,), 3 * w + 77, dtype=torch.int32, device="cuda")
+
+    def step(codes, scales, pos, *x):
+        dims = binding.make_mqa_dims(pos.shape[0], 1, H, D, w)
+        ws = binding.alloc_workspace(binding.mqa_decode8_workspace_size(dims))
+        out = torch.empty_like(x[0])
+        binding.mqa_decode8(dims, *x, pos, codes, scales, out, ws)
+        assert binding.read_device_status(ws) == binding.RGLRU_OK
+        return out
+
+    own = (codes[-n:].clone(), scales[-n:].clone(), pos[-n:].clone(), *(t[-n:].clone() for t in x))
+    y, z = to_np(step(codes, scales, pos, *x)[-n:]), to_np(step(*own))
+    assert np.all(np.abs(y - z) <= 2.0 ** -7 * np.abs(z) + 2.0 ** -12 * np.max(np.abs(z)))
+    assert torch.equal(codes[-n:], own[0]) and torch.equal(scales[-n:], own[1])
+    cache = torch.empty(B, 2, w, D, dtype=torch.bfloat16, device="cuda")
+    dims = binding.make_mqa_dims(B, 1, H, D, w)
+    binding.mqa_cache8_read(dims, codes, scales, cache)
+    small = torch.empty(n, 2, w, D, dtype=torch.bfloat16, device="cuda")
+    binding.mqa_cache8_read(binding.make_mqa_dims(n, 1, H, D, w), own[0], own[1], small)
+    assert torch.equal(cache[-n:], small)
