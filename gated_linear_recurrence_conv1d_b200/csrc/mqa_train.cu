@@ -299,7 +299,9 @@ struct QTiles {
 // with everything around them.
 namespace fw {
 // Two fp32 values rounded to bf16 (to nearest, ties away from zero, so that bit 15 of the value alone says whether
-// it was rounded up), and bits 8 to 15 of four: as a signed byte, what to add to the rounded value's bits
+// it was rounded up), and bits 8 to 15 of four: as a signed byte, what to add to the rounded value's bits.  A NaN has to
+// be quiet_nan(), which stays itself with a byte of zero: the one that arithmetic makes, 0x7fffffff, would be carried
+// into the sign and leave as -0.
 __device__ __forceinline__ uint32_t bf16x2_away(float a, float b) {
     return __byte_perm(__float_as_uint(a) + 0x8000u, __float_as_uint(b) + 0x8000u, 0x7632);
 }
@@ -307,6 +309,7 @@ __device__ __forceinline__ uint32_t low_bytes(const float* x) {
     return __byte_perm(__byte_perm(__float_as_uint(x[0]), __float_as_uint(x[1]), 0x0051),
                        __byte_perm(__float_as_uint(x[2]), __float_as_uint(x[3]), 0x0051), 0x5410);
 }
+__device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7fc00000u); }
 constexpr int BK = 128;
 constexpr uint32_t SLOT = 32768;
 constexpr int NSLOT = 5;
@@ -535,8 +538,18 @@ mqa_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     uint32_t e[16];
                     tmem_ld32(tl + TM_O + half * 128 + c + h, o);
                     tmem_wait_ld();
+                    float2 odd = make_float2(0.f, 0.f);              // stays 0 unless a value is not finite
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] *= inv;
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 x = mul2(make_float2(o[i], o[i + 1]), make_float2(inv, inv));
+                        odd = fma2(x, make_float2(0.f, 0.f), odd);
+                        o[i] = x.x;
+                        o[i + 1] = x.y;
+                    }
+                    if (!(odd.x + odd.y == 0.f)) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = o[i] == o[i] ? o[i] : quiet_nan();
+                    }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) e[i] = bf16x2_away(o[2 * i], o[2 * i + 1]);
 #pragma unroll
