@@ -276,8 +276,8 @@ RGLRU_API rglru_status rglru_mqa_decode(const rglru_mqa_dims* dims, const void* 
  *           rotated queries and keys, so q and k may be freed or overwritten in between.
  * Both calls take a workspace of rglru_mqa_train_workspace_size bytes (scratch: nothing in it has
  * to survive from the forward to the backward).  Every input value has to be finite (a masked
- * key still enters the tensor-core products, with weight 0).  A row that sees a NaN, or whose sums
- * overflow, gets NaN in out and dq, not a number. */
+ * key still enters the tensor-core products, with weight 0).  Where a row sees a NaN or an
+ * infinity, or its sums overflow, out and dq hold what fp32 arithmetic gives: NaN or infinity. */
 RGLRU_API size_t rglru_mqa_save_size(const rglru_mqa_dims* dims);
 RGLRU_API size_t rglru_mqa_train_workspace_size(const rglru_mqa_dims* dims);
 
