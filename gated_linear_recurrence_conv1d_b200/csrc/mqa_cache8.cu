@@ -260,6 +260,9 @@ constexpr int kPrepWarps = 2;          // five warps a scheduler in all, with 96
 constexpr int kThreads = kSoft + 64 + 32 * kPrepWarps;
 
 constexpr float kAlpha = 4096.0f;                     // weights are held as alpha p: p <= 8 keeps them below 57344
+// Where the reference of the values' scales begins: alpha / vref is finite and vref / alpha a normal number, also for slots
+// whose scale is 0 (a ring of zeros that was not written there)
+constexpr float kVref0 = 0x1p-114f;
 
 struct DecArgs {
     int B, H, w;
@@ -680,7 +683,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + grp * kHg;
         float* red = reinterpret_cast<float*>(smem + OFF_RED + grp * RED_BYTES);
         auto grp_or = [&](bool v) { return named_or(v, 1 + grp, 128); };     // over the group's threads
-        float vref = 0.f, p_vref = 0.f;
+        float vref = kVref0, p_vref = kVref0;
         float *sums = red + 5 * kHg, *maxima = red + 9 * kHg;
         // a segment's output, its last tile number `last`: the row's, or a part of it
         auto finish = [&](uint32_t n, uint32_t last) {
@@ -750,7 +753,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
             const float* qs = reinterpret_cast<const float*>(smem + OFF_QS + (ns & 1) * 64) + grp * kHg;
             const float* fresh = reinterpret_cast<const float*>(smem + OFF_STG + (ns & 1) * STG_BYTES + 2 * D);
             float m[kHg], l[kHg];
-            vref = 0.f;
+            vref = kVref0;
 #pragma unroll
             for (int h = 0; h < kHg; ++h) {
                 m[h] = -INFINITY;
@@ -815,10 +818,9 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                     v = fmaxf(fmaxf(red[4 * kHg], red[4 * kHg + 1]), fmaxf(red[4 * kHg + 2], red[4 * kHg + 3]));
                     float fv = 1.0f;
                     if (v > vref) {                       // the next power of two, twice over (infinity stays)
-                        // (at least 2^-114: alpha / vref is finite, vref / alpha a normal number)
                         const unsigned e2 = (__float_as_uint(v) & 0x7f800000u) + 0x01000000u;
-                        const float p2 = __uint_as_float(max(min(e2, 0x7f000000u), 13u << 23));
-                        fv = vref == 0.f ? 1.0f : vref / p2;
+                        const float p2 = __uint_as_float(min(e2, 0x7f000000u));
+                        fv = vref / p2;
                         vref = p2;
                     }
                     float f[kHg];
