@@ -215,13 +215,16 @@ __global__ void __launch_bounds__(256) mqa_cache8_read_kernel(long long slots, i
 //   S^T = K Qp^T   (M 128 slots, N 48 = 16 heads x 3 parts, K 256; e4m3, fp32 sums)
 //   O^T += V^T Wp^T (M 128 columns twice, N 48 = 16 heads x 3 parts, K 128 slots)
 // straight from the codes in shared memory (V^T is the value tile read MN-major).  Four groups of 4 warps, each
-// with every fourth head, thread = slot: s = (S0 + S1 / 16 + S2 / 256) 2^e c scale_k, p = 2^(s - m) with a
-// reference maximum m per head that moves when a score passes it by more than 8 times, and the weight
-// p scale_v, normalised by a power of two vref >= the value scales seen so far, as three e5m2 parts: off by at
-// most 2^-9 of itself, half of what bf16 would leave, down to weights of 2^-29 (e4m3 parts end at 2^-16, which
-// shows where one slot has nearly all the weight and a small value).  p adds to the thread's own sum in fp32.  O
-// stays in TMEM for the whole segment; when m or vref moves it is rescaled there (each group has its own vref and
-// its own columns of S, W and O, so within a segment the groups never meet).  A row inside one segment is written
+// with every fourth head, thread = slot: s = (S0 + S1 / 16 + S2 / 256) 2^e c scale_k, p = 2^(s - m) for the sum of
+// the weights, and for the weighted sum of the codes alpha 2^(u - n), u = s + log2 scale_v, as three e5m2 parts.
+// m and n are reference maxima of a head's s and u, which move when one passes them by more than 3 (8 times).  A
+// reference of u, not one of s beside a largest scale: the scale of a slot that has no weight to speak of would
+// push the others' weights out of e5m2's range.  Parts: what is left of a weight w after each is at most an
+// eighth of it or 2^-17, so three (1, 1/8, 1/64) leave max(2^-9 w, 2^-23): 2^-9 of the weight, half of what bf16
+// would leave, or 2^-35 of the segment's heaviest, whose w is 2^12 at least (e4m3 parts end at 2^-22 of it, which
+// shows).  p adds to the thread's own sum in fp32.  O stays in TMEM for the whole segment, in units of 2^n / alpha;
+// when n moves it is rescaled there (each group has its own columns of S, W and O, so within a segment the groups
+// never meet).  A row inside one segment is written
 // at once; else the segments leave (m, sum, O) and mqa_decode8_merge_kernel adds them up in order.  (The segment
 // that finishes last doing that here, by a counter of the row, took longer at the end of the kernel, and its
 // registers spilled the softmax's.)
@@ -244,7 +247,7 @@ constexpr int kQParts = 3, kQRows = kQParts * kMaxH;
 constexpr uint32_t Q_BYTES = kQRows * D;              // 12288: 2 boxes of [48 x 128 B]
 constexpr int kWParts = 3, kWRows = kWParts * kMaxH;
 constexpr uint32_t W_BYTES = kWRows * kTile;          // 6144: [48 x 128 slots]
-constexpr uint32_t RED_BYTES = 192;                   // of a group: [4 warps][kHg], [4] scales; a segment's [4 warps][kHg] sums, [kHg] maxima
+constexpr uint32_t RED_BYTES = 224;                   // of a group: [4 warps][kHg] of s, of u; a segment's [4 warps][kHg] sums, [kHg] m, [kHg] n
 constexpr uint32_t STG_BYTES = 2 * D + 16;            // the new slot: key and value codes, their scales
 constexpr uint32_t OFF_Q = kNBuf * TILE_BYTES, OFF_W = OFF_Q + 2 * Q_BYTES, OFF_CS = OFF_W + 2 * W_BYTES;
 constexpr uint32_t IN_BYTES = (kMaxH + 2) * D * 2;     // a segment's queries, new key and value
@@ -259,10 +262,10 @@ constexpr int kSoftWarps = 4 * kGroups, kSoft = 32 * kSoftWarps, kWarpTma = kSof
 constexpr int kPrepWarps = 2;          // five warps a scheduler in all, with 96 registers as without them
 constexpr int kThreads = kSoft + 64 + 32 * kPrepWarps;
 
-constexpr float kAlpha = 4096.0f;                     // weights are held as alpha p: p <= 8 keeps them below 57344
-// Where the reference of the values' scales begins: alpha / vref is finite and vref / alpha a normal number, also for slots
-// whose scale is 0 (a ring of zeros that was not written there)
-constexpr float kVref0 = 0x1p-114f;
+constexpr float kLog2Alpha = 12.0f;                   // weights are held as alpha 2^(u - n): u - n <= 3 keeps them below 57344
+// Where a head's n begins: below every log2 scale, and finite, so that slots whose scale is 0 (a ring of zeros that was not
+// written there) have weight 2^(-inf - n) = 0 also where there is no other
+constexpr float kNoU = -1.0e30f;
 
 struct DecArgs {
     int B, H, w;
@@ -335,6 +338,12 @@ __device__ __forceinline__ bool next_seg(const DecArgs& a, Walk& k, DecSeg& s) {
     return true;
 }
 
+// the maximum over the warp; NaN only where every lane's is
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
 // the OR of v over the threads that meet at barrier `id`
 __device__ __forceinline__ bool named_or(bool v, int id, int threads) {
     uint32_t o;
@@ -683,8 +692,7 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + grp * kHg;
         float* red = reinterpret_cast<float*>(smem + OFF_RED + grp * RED_BYTES);
         auto grp_or = [&](bool v) { return named_or(v, 1 + grp, 128); };     // over the group's threads
-        float vref = kVref0, p_vref = kVref0;
-        float *sums = red + 5 * kHg, *maxima = red + 9 * kHg;
+        float *sums = red + 8 * kHg, *maxima = red + 12 * kHg, *maxima_u = red + 13 * kHg;
         // a segment's output, its last tile number `last`: the row's, or a part of it
         auto finish = [&](uint32_t n, uint32_t last) {
             const DecSeg x = *reinterpret_cast<const DecSeg*>(smem + OFF_SEG + (n & 1) * 32);
@@ -699,8 +707,10 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 tmem_ld4(tl + TM_O + hh * 64 + 32, y2);
                 tmem_wait_ld();
 #pragma unroll
-                for (int h = 0; h < kHg; ++h)
-                    o[hh][h] = fmaf(y2[h], 1.0f / 64.0f, fmaf(y1[h], 1.0f / 8.0f, o[hh][h])) * (p_vref * (1.0f / kAlpha));
+                for (int h = 0; h < kHg; ++h) {          // times 2^(n - m) / alpha, in two steps: it may be past fp32's ends
+                    const float e = ex2_approx(0.5f * (maxima_u[h] - maxima[h] - kLog2Alpha));
+                    o[hh][h] = fmaf(y2[h], 1.0f / 64.0f, fmaf(y1[h], 1.0f / 8.0f, o[hh][h])) * e * e;
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -752,11 +762,11 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
             const float *sk = a.scales + (size_t)sg.b * 2 * a.w, *sv = sk + a.w;
             const float* qs = reinterpret_cast<const float*>(smem + OFF_QS + (ns & 1) * 64) + grp * kHg;
             const float* fresh = reinterpret_cast<const float*>(smem + OFF_STG + (ns & 1) * STG_BYTES + 2 * D);
-            float m[kHg], l[kHg];
-            vref = kVref0;
+            float m[kHg], mu[kHg], l[kHg];
 #pragma unroll
             for (int h = 0; h < kHg; ++h) {
                 m[h] = -INFINITY;
+                mu[h] = kNoU;
                 l[h] = 0.f;
             }
             int x = sg.t0 * kTile + r;
@@ -784,7 +794,8 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 }
                 tc_fence_after();
                 float s[kHg];
-                bool move = vs > vref;
+                const float lv = __log2f(vs);            // a scale that is not finite: u is not
+                bool move = false;
                 {
                     float s1[kHg], s2[kHg];
                     tmem_ld4(tl + TM_S + buf * 64, s);
@@ -795,45 +806,37 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                     for (int h = 0; h < kHg; ++h) {
                         const float d = fmaf(s2[h], 1.0f / 256.0f, fmaf(s1[h], 1.0f / 16.0f, s[h]));
                         s[h] = valid && h < nh ? d * (qs[h] * ks) : -INFINITY;
-                        move |= s[h] > m[h] + 3.0f;
+                        move |= s[h] > m[h] + 3.0f || s[h] + lv > mu[h] + 3.0f;
                     }
                 }
                 if (grp_or(move || !ok)) {
                     // the new reference values from the 4 warps' maxima; O and the sums follow
 #pragma unroll
                     for (int h = 0; h < kHg; ++h) {
-                        float v = s[h];
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-                        if (lane == 0) red[(warp & 3) * kHg + h] = v;
+                        const float v = warp_max(s[h]), u = warp_max(s[h] + lv);
+                        if (lane == 0) {
+                            red[(warp & 3) * kHg + h] = v;
+                            red[(4 + (warp & 3)) * kHg + h] = u;
+                        }
                     }
-                    float v = vs;
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-                    if (lane == 0) red[4 * kHg + (warp & 3)] = v;
                     if (grp_or(!ok)) {
                         stop = true;
                         break;
                     }
-                    v = fmaxf(fmaxf(red[4 * kHg], red[4 * kHg + 1]), fmaxf(red[4 * kHg + 2], red[4 * kHg + 3]));
-                    float fv = 1.0f;
-                    if (v > vref) {                       // the next power of two, twice over (infinity stays)
-                        const unsigned e2 = (__float_as_uint(v) & 0x7f800000u) + 0x01000000u;
-                        const float p2 = __uint_as_float(min(e2, 0x7f000000u));
-                        fv = vref / p2;
-                        vref = p2;
-                    }
                     float f[kHg];
-                    bool any = fv != 1.0f;
+                    bool any = false;
 #pragma unroll
                     for (int h = 0; h < kHg; ++h) {
-                        f[h] = fv;
                         const float mx = fmaxf(fmaxf(red[h], red[kHg + h]), fmaxf(red[2 * kHg + h], red[3 * kHg + h]));
                         if (mx > m[h] + 3.0f) {
-                            const float e = m[h] == -INFINITY ? 1.0f : ex2_approx(m[h] - mx);
+                            l[h] *= m[h] == -INFINITY ? 1.0f : ex2_approx(m[h] - mx);
                             m[h] = mx;
-                            l[h] *= e;
-                            f[h] *= e;
+                        }
+                        const float ux = fmaxf(fmaxf(red[4 * kHg + h], red[5 * kHg + h]), fmaxf(red[6 * kHg + h], red[7 * kHg + h]));
+                        f[h] = 1.0f;
+                        if (ux > mu[h] + 3.0f) {
+                            f[h] = ex2_approx(mu[h] - ux);
+                            mu[h] = ux;
                             any = true;
                         }
                     }
@@ -856,16 +859,16 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
                 }
                 // weights: row part * 16 + head row, byte = slot, in 128-byte rows swizzled by the row
                 uint8_t* wb = smem + OFF_W + buf * W_BYTES + grp * (kHg * kTile) + (r & 15);
-                const float wv = fmaf(vs, kAlpha / vref, vs - vs);    // a scale that is not finite: NaN
                 const uint32_t ch = (uint32_t)(r >> 4) ^ (uint32_t)(grp * kHg & 7);   // swizzled by the row, grp * kHg + h
 #pragma unroll
                 for (int h = 0; h < kHg; h += 2) {
                     uint32_t c[kWParts] = {};
                     if (h < nh) {
-                        const float p0 = valid ? ex2_approx(s[h] - m[h]) : 0.f, p1 = valid && h + 1 < nh ? ex2_approx(s[h + 1] - m[h + 1]) : 0.f;
-                        l[h] += p0;
-                        l[h + 1] += p1;
-                        float w0 = valid ? p0 * wv : 0.f, w1 = valid && h + 1 < nh ? p1 * wv : 0.f;
+                        const bool two = valid && h + 1 < nh;
+                        l[h] += valid ? ex2_approx(s[h] - m[h]) : 0.f;
+                        l[h + 1] += two ? ex2_approx(s[h + 1] - m[h + 1]) : 0.f;
+                        float w0 = valid ? ex2_approx(s[h] + lv - (mu[h] - kLog2Alpha)) : 0.f;
+                        float w1 = two ? ex2_approx(s[h + 1] + lv - (mu[h + 1] - kLog2Alpha)) : 0.f;
 #pragma unroll
                         for (int part = 0; part < kWParts; ++part) {
                             c[part] = e5m2x2(w0, w1);
@@ -895,9 +898,11 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
                 if (lane == 0) sums[(warp & 3) * kHg + h] = l[h];
-                if (r == 0) maxima[h] = m[h];
+                if (r == 0) {
+                    maxima[h] = m[h];
+                    maxima_u[h] = mu[h];
+                }
             }
-            p_vref = vref;
         }
         if (!stop) finish(ns - 1, gt - 1);
         tmem_wait_ld();

@@ -1,4 +1,4 @@
-"""rglru_mqa_decode8 on rings with slots whose scales are zero.  Bars as for any decode
+"""rglru_mqa_decode8 on rings whose values' scales are zero, or lie many powers of two apart.  Bars as for any decode
 step: 2^-6 of sum P |v| per element, 5e-3 RMS."""
 
 import numpy as np
@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from gated_linear_recurrence_conv1d_b200 import binding, inputs
-from oracle import mqa_train
+from oracle import mqa, mqa_train
 from tests.gpu_util import to_np
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +60,49 @@ def test_slots_of_zero_codes_and_zero_scales(B, filled):
     pos = np.array([(700, 899, 1300, 130)[b % 4] for b in range(B)], dtype=np.int32)
     q, k, v = _bf16(rng, (B, H, D)), _bf16(rng, (B, D)), _bf16(rng, (B, D))
     _close(*_decode(c, s, q, k, v, pos), filled)
+
+
+def _floor(c, s, q, pos):
+    """[B, H]: what the weights' 8-bit parts may leave of every element beside the bar.  With n the largest s + log2 scale that
+    the head's reference was set to, a weight is w = 2^12 2^(s + log2 scale - n), and the heaviest slot's is 2^12 at
+    least.  A part (e5m2: 2 bits of mantissa, steps of 2^-16 below 2^-14) leaves an eighth of what it is given or half
+    a step, 2^-17; it is given 8 times what the one before left.  Three leave max(2^-9 w, 2^-23) of w: the first is in the
+    bar, the second is 2^-35 of the heaviest slot's weight times scale.  Codes are at most 448, and there are len slots."""
+    B, H = q.shape[:2]
+    r = np.zeros((B, H))
+    for b in range(B):
+        n = min(int(pos[b]) + 1, c.shape[2])
+        keys = mqa_train.dequantise(c[b, 0, :n], s[b, 0, :n])
+        x = mqa.rope(mqa._f64(q[b]), np.array(pos[b])) @ keys.T / 16.0
+        p = np.exp(x - x.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        r[b] = n * 2.0 ** -35 * 448.0 * (p * s[b, 1, :n].astype(np.float64)).max(-1)
+    return r
+
+
+@pytest.mark.parametrize("order", ["same tile", "largest first", "largest last"])
+@pytest.mark.parametrize("log2_ratio", [0, 20, 24, 30, 45, 90])
+def test_the_heavy_slot_has_a_small_value(log2_ratio, order):
+    """One key holds nearly all of every query's weight and its value is 2^-log2_ratio of the largest in the ring, whose key
+    has next to no weight: e^-64 = 2^-92 against the heavy one's.  A query of zeros weighs all alike."""
+    rng = np.random.default_rng([43, log2_ratio])
+    B, H, w = 40, 4, 1000                          # 320 tiles: two or three to a CTA
+    pos = (3 * w + np.arange(B) * 7).astype(np.int32)
+    q, k = _bf16(rng, (B, H, D)), _bf16(rng, (B, D))
+    v = _bf16(rng, (B, D), 2.0 ** -log2_ratio)
+    q[:, 1:3] = q[:, :1]
+    q[:, 3] = 0
+    heavy, big = {"same tile": (200, 201), "largest first": (330, 140), "largest last": (140, 330)}[order]
+    x = rng.standard_normal((B, 2, w, D))
+    x[:, 1] *= 2.0 ** -log2_ratio
+    x[:, 0] *= 0.1
+    for b in range(B):
+        qr = mqa.rope(mqa._f64(q[b, 0]), np.array(pos[b]))
+        u = qr / np.dot(qr, qr)                    # q . u = 1: scores of +32 and -32 at a scale of 1 / 16
+        x[b, 0, heavy], x[b, 0, big] = 512.0 * u, -512.0 * u
+        x[b, 1, big] = rng.standard_normal(D)
+    c, s = mqa_train.quantise(x)
+    g, ref, pav = _decode(c, s, q, k, v, pos)
+    pav += 2.0 ** 6 * _floor(c, s, q, pos)[..., None]
+    for h in range(H):
+        _close(g[:, h], ref[:, h], pav[:, h], f"head {h}")
