@@ -235,6 +235,7 @@ struct Args {
     float* part;                // partial dk, dv of (cluster, key tile)
     int nkt;                    // 128-key tiles of a batch row
     __nv_bfloat16 *out, *dq, *dk, *dv;
+    unsigned* delta_there;      // 1 from dq's first CTA on: what dk / dv read is complete (0 from the delta kernel on)
     DeviceStatus* status;
     unsigned long long timeout_ns;
 };
@@ -750,7 +751,10 @@ mqa_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
     pdl_wait();
-    pdl_launch();                                        // mqa_dkv_kernel may run beside this one: delta is complete
+    // mqa_dkv_kernel may run beside this one: all that it reads is complete, and visible here by the wait, so to those
+    // that see this flag
+    if (blockIdx.x == 0 && threadIdx.x == 0) st_release_gpu(a.delta_there, 1);
+    pdl_launch();
 
     // Number i of the pair's key tiles uses each of the three buffers for the i-th time.
     if (warp == kWarpTma) {
@@ -1139,6 +1143,10 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         tmem_alloc(smem_u32((const void*)tmem_s), 512);
         tmem_relinquish();
     }
+    // This kernel starts when mqa_dq_kernel allows it, not at that one's end, and the permission alone orders no memory.
+    // dq's flag does: released behind dq's own wait for the kernels before, acquired here ahead of every read.  Should
+    // it not be there yet, dq's end does.  (Waiting for that end always: the SMs that dq leaves early stand idle.)
+    if (threadIdx.x == 0 && ld_acquire_gpu(a.delta_there) != 1u) pdl_wait();
     tc_fence_before();
     __syncthreads();
     cluster_sync();
@@ -1157,6 +1165,7 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             const CUtensorMap *map_a = rank == 0 ? &map_k : &map_v, *map_x = rank == 0 ? &map_q : &map_do,
                               *map_y = rank == 0 ? &map_do : &map_q;
             const float* vec = rank == 0 ? a.neg_lse : a.neg_delta;
+            fence_proxy_async_global();                  // the copies below come after the flag, too
             uint32_t L = 0, gi = 0;
             bool ok = true;
             auto load = [&](const CUtensorMap* m, int row, uint32_t box, int c0, int nc) {   // nc boxes from column block c0
@@ -1381,8 +1390,7 @@ mqa_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         tmem_wait_ld();
         tmem_wait_st();
     }
-    // the kernel before, mqa_dq_kernel, let this one start when all that this one reads was there; the kernel behind it
-    // has to find that one complete too
+    // the kernel behind this one has to find mqa_dq_kernel complete too
     pdl_wait();
     tc_fence_before();
     __syncthreads();
@@ -1444,6 +1452,7 @@ __device__ __forceinline__ float with_low(uint32_t hi, uint32_t byte) {
 __global__ void __launch_bounds__(32 * kDeltaWarps) mqa_delta_kernel(const Args a, const __nv_bfloat16* dout) {
     pdl_launch();
     pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.delta_there = 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long row0 = ((long long)blockIdx.x * kDeltaWarps + warp) * kDeltaRows, rows = (long long)a.B * a.TH;
     uint4 x[kDeltaRows], y[kDeltaRows];
@@ -1502,7 +1511,7 @@ struct WsLayout {
 inline WsLayout ws_layout(const rglru_mqa_dims* d) {
     const size_t nk = (size_t)d->batch * key_tiles(d);
     WsLayout l{};
-    size_t o = 256;                    // the status word
+    size_t o = 256;                    // the status word, the flag
     l.delta = o; o = up256(o + d->batch * row_pitch(d) * 4);
     l.part = o; o = up256(o + (nk + kMaxClusters) * 2 * bk::PART_FLOATS * 4);
     l.total = o;
@@ -1527,6 +1536,7 @@ inline Args make_args(const rglru_mqa_dims* d, void* save, void* ws) {
     a.cum = reinterpret_cast<const long long*>(p + l.cum);
     a.part = reinterpret_cast<float*>(w + wl.part);
     a.status = static_cast<DeviceStatus*>(ws);
+    a.delta_there = reinterpret_cast<unsigned*>(w + 128);
     a.timeout_ns = 1000000000ull;
     return a;
 }

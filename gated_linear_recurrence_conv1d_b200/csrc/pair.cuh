@@ -64,6 +64,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
+// asynchronous copies behind this thread's view of global memory (what it has acquired of ordinary stores)
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
 // MN-major (128-byte swizzle) descriptor: atoms of 64 MN-elements x K rows of 128 B, `atom` bytes apart,
 // 8-row K groups 1024 B apart
 __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t smem_addr, uint32_t atom) {
