@@ -5,7 +5,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <algorithm>
 #include <mutex>
 
 #include "common.cuh"
@@ -387,15 +386,31 @@ static rglru_status check_mqa_cache8(const rglru_mqa_dims* d, bool tokens) {
 
 static bool positions_fit(int pos0, int n) { return pos0 >= 0 && (long long)pos0 + n <= 0x7fffffffLL; }
 
-// every pointer given, 16-byte aligned; no output (the last n_out) equal to another pointer
-static rglru_status check_tensors(const void* const* p, int n, int n_out) {
-    for (int i = 0; i < n; ++i) {
-        if (!p[i] || !aligned(p[i], 16)) return RGLRU_ERR_INVALID_ARG;
-        for (int j = std::max(i + 1, n - n_out); j < n; ++j)
-            if (p[i] == p[j]) return RGLRU_ERR_INVALID_ARG;
-    }
+// a tensor, vector or buffer of a call: `bytes` from p (p may be NULL where the argument is optional)
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+
+// the first n given, 16-byte aligned
+static rglru_status check_tensors(const Span* t, int n) {
+    for (int i = 0; i < n; ++i)
+        if (!t[i].p || !aligned(t[i].p, 16)) return RGLRU_ERR_INVALID_ARG;
     return RGLRU_OK;
 }
+
+// no byte of what is written (from t[first_out] on) in another
+static rglru_status check_apart(const Span* t, int n, int first_out) {
+    for (int j = first_out; j < n; ++j)
+        for (int i = 0; i < j; ++i) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(t[i].p), b = reinterpret_cast<uintptr_t>(t[j].p);
+            if (a && b && (a < b ? b - a < t[i].bytes : a - b < t[j].bytes)) return RGLRU_ERR_INVALID_ARG;
+        }
+    return RGLRU_OK;
+}
+
+// bytes of a bf16 tensor of `rows` rows of head_dim
+static size_t rows16(const rglru_mqa_dims* d, size_t rows) { return rows * d->head_dim * 2; }
 
 size_t rglru_mqa_save_size(const rglru_mqa_dims* dims) {
     return check_mqa_train(dims) == RGLRU_OK ? rglru::mqa_save_bytes(dims) : 0;
@@ -410,11 +425,14 @@ rglru_status rglru_mqa_forward(const rglru_mqa_dims* dims, const void* q, const 
                                void* workspace, size_t workspace_bytes, void* stream) {
     rglru_status st = check_mqa_train(dims);
     if (st != RGLRU_OK) return st;
-    const void* t[] = {q, k, v, out};
-    if ((st = check_tensors(t, 4, 1)) != RGLRU_OK) return st;
-    if (!positions_fit(pos0, dims->seq_len) || (save && save == workspace)) return RGLRU_ERR_INVALID_ARG;
-    if ((st = check_workspace(save, save_bytes, rglru_mqa_save_size(dims))) != RGLRU_OK) return st;
-    if ((st = check_workspace(workspace, workspace_bytes, rglru_mqa_train_workspace_size(dims))) != RGLRU_OK) return st;
+    const size_t B = dims->batch, tok = B * dims->seq_len, nq = rows16(dims, tok * dims->q_heads), nk = rows16(dims, tok);
+    const Span t[] = {{q, nq}, {k, nk}, {v, nk}, {reset, tok}, {out, nq}, {save, rglru_mqa_save_size(dims)},
+                      {workspace, rglru_mqa_train_workspace_size(dims)}};
+    if ((st = check_tensors(t, 3)) != RGLRU_OK || (st = check_tensors(t + 4, 1)) != RGLRU_OK) return st;
+    if (!positions_fit(pos0, dims->seq_len)) return RGLRU_ERR_INVALID_ARG;
+    if ((st = check_workspace(save, save_bytes, t[5].bytes)) != RGLRU_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, t[6].bytes)) != RGLRU_OK) return st;
+    if ((st = check_apart(t, 7, 4)) != RGLRU_OK) return st;
     return cuda_status(rglru::launch_mqa_forward(dims, q, k, v, reset, pos0, out, save, workspace,
                                                  static_cast<cudaStream_t>(stream)));
 }
@@ -424,11 +442,13 @@ rglru_status rglru_mqa_backward(const rglru_mqa_dims* dims, const void* v, const
                                 size_t workspace_bytes, void* stream) {
     rglru_status st = check_mqa_train(dims);
     if (st != RGLRU_OK) return st;
-    const void* t[] = {v, out, dout, dq, dk, dv};
-    if ((st = check_tensors(t, 6, 3)) != RGLRU_OK) return st;
-    if (save && save == workspace) return RGLRU_ERR_INVALID_ARG;
-    if ((st = check_workspace(const_cast<void*>(save), save_bytes, rglru_mqa_save_size(dims))) != RGLRU_OK) return st;
-    if ((st = check_workspace(workspace, workspace_bytes, rglru_mqa_train_workspace_size(dims))) != RGLRU_OK) return st;
+    const size_t B = dims->batch, tok = B * dims->seq_len, nq = rows16(dims, tok * dims->q_heads), nk = rows16(dims, tok);
+    const Span t[] = {{v, nk}, {out, nq}, {dout, nq}, {save, rglru_mqa_save_size(dims)}, {dq, nq}, {dk, nk}, {dv, nk},
+                      {workspace, rglru_mqa_train_workspace_size(dims)}};
+    if ((st = check_tensors(t, 3)) != RGLRU_OK || (st = check_tensors(t + 4, 3)) != RGLRU_OK) return st;
+    if ((st = check_workspace(const_cast<void*>(save), save_bytes, t[3].bytes)) != RGLRU_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, t[7].bytes)) != RGLRU_OK) return st;
+    if ((st = check_apart(t, 8, 4)) != RGLRU_OK) return st;
     return cuda_status(rglru::launch_mqa_backward(dims, v, out, dout, save, dq, dk, dv, workspace,
                                                   static_cast<cudaStream_t>(stream)));
 }
@@ -437,10 +457,12 @@ rglru_status rglru_mqa_cache8_write(const rglru_mqa_dims* dims, const void* k, c
                                     int pos0, void* codes, float* scales, void* stream) {
     rglru_status st = check_mqa_cache8(dims, true);
     if (st != RGLRU_OK) return st;
-    const void* t[] = {k, v, codes};
-    if ((st = check_tensors(t, 3, 1)) != RGLRU_OK) return st;
+    const size_t B = dims->batch, slots = B * 2 * dims->window, nk = rows16(dims, B * dims->seq_len);
+    const Span t[] = {{k, nk}, {v, nk}, {lengths, B * 4}, {codes, slots * dims->head_dim}, {scales, slots * 4}};
+    if ((st = check_tensors(t, 2)) != RGLRU_OK || (st = check_tensors(t + 3, 1)) != RGLRU_OK) return st;
     if (!scales || !aligned(scales, 4) || !aligned(lengths, 4) || !positions_fit(pos0, dims->seq_len))
         return RGLRU_ERR_INVALID_ARG;
+    if ((st = check_apart(t, 5, 3)) != RGLRU_OK) return st;
     return cuda_status(rglru::launch_mqa_cache8_write(dims, k, v, lengths, pos0, codes, scales,
                                                       static_cast<cudaStream_t>(stream)));
 }
@@ -454,10 +476,13 @@ rglru_status rglru_mqa_decode8(const rglru_mqa_dims* dims, const void* q, const 
                                void* stream) {
     rglru_status st = check_mqa_cache8(dims, false);
     if (st != RGLRU_OK) return st;
-    const void* t[] = {q, k, v, codes, out};
-    if ((st = check_tensors(t, 5, 2)) != RGLRU_OK) return st;
+    const size_t B = dims->batch, slots = B * 2 * dims->window, nq = rows16(dims, B * dims->q_heads), nk = rows16(dims, B);
+    const Span t[] = {{q, nq}, {k, nk}, {v, nk}, {pos, B * 4}, {scales, slots * 4}, {codes, slots * dims->head_dim}, {out, nq},
+                      {workspace, rglru_mqa_decode8_workspace_size(dims)}};
+    if ((st = check_tensors(t, 3)) != RGLRU_OK || (st = check_tensors(t + 5, 2)) != RGLRU_OK) return st;
     if (!pos || !aligned(pos, 4) || !scales || !aligned(scales, 4)) return RGLRU_ERR_INVALID_ARG;
-    if ((st = check_workspace(workspace, workspace_bytes, rglru_mqa_decode8_workspace_size(dims))) != RGLRU_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, t[7].bytes)) != RGLRU_OK) return st;
+    if ((st = check_apart(t, 8, 4)) != RGLRU_OK) return st;
     return cuda_status(rglru::launch_mqa_decode8(dims, q, k, v, pos, codes, scales, out, workspace,
                                                  static_cast<cudaStream_t>(stream)));
 }
@@ -466,9 +491,11 @@ rglru_status rglru_mqa_cache8_read(const rglru_mqa_dims* dims, const void* codes
                                    void* cache, void* stream) {
     rglru_status st = check_mqa_cache8(dims, false);
     if (st != RGLRU_OK) return st;
-    const void* t[] = {codes, cache};
-    if ((st = check_tensors(t, 2, 1)) != RGLRU_OK) return st;
+    const size_t B = dims->batch, slots = B * 2 * dims->window;
+    const Span t[] = {{scales, slots * 4}, {pos, B * 4}, {codes, slots * dims->head_dim}, {cache, rows16(dims, slots)}};
+    if ((st = check_tensors(t + 2, 2)) != RGLRU_OK) return st;
     if (!scales || !aligned(scales, 4) || !aligned(pos, 4)) return RGLRU_ERR_INVALID_ARG;
+    if ((st = check_apart(t, 4, 3)) != RGLRU_OK) return st;
     return cuda_status(rglru::launch_mqa_cache8_read(dims, codes, scales, pos, cache,
                                                      static_cast<cudaStream_t>(stream)));
 }

@@ -277,11 +277,13 @@ RGLRU_API rglru_status rglru_mqa_decode(const rglru_mqa_dims* dims, const void* 
  * Both calls take a workspace of rglru_mqa_train_workspace_size bytes (scratch: nothing in it has
  * to survive from the forward to the backward).  Every input value has to be finite (a masked
  * key still enters the tensor-core products, with weight 0).  Where a row sees a NaN or an
- * infinity, or its sums overflow, out and dq hold what fp32 arithmetic gives: NaN or infinity. */
+ * infinity, or its sums overflow, out and dq hold what fp32 arithmetic gives: NaN or infinity.
+ * What a call writes (outputs, save, workspace) may not overlap anything else that it is given
+ * (else INVALID_ARG); the same holds for the calls of the 8-bit ring below. */
 RGLRU_API size_t rglru_mqa_save_size(const rglru_mqa_dims* dims);
 RGLRU_API size_t rglru_mqa_train_workspace_size(const rglru_mqa_dims* dims);
 
-/* q [B, T, H, d], k, v [B, T, d] -> out [B, T, H, d], and *save, neither of which may alias an input.
+/* q [B, T, H, d], k, v [B, T, d] -> out [B, T, H, d], and *save.
  * Errors as rglru_mqa_prefill; a save that is missing or smaller than the queried size is WORKSPACE. */
 RGLRU_API rglru_status rglru_mqa_forward(const rglru_mqa_dims* dims, const void* q, const void* k, const void* v,
                                          const uint8_t* reset, int pos0, void* out, void* save, size_t save_bytes,
@@ -291,7 +293,7 @@ RGLRU_API rglru_status rglru_mqa_forward(const rglru_mqa_dims* dims, const void*
  * [B, T, H, d] = dL/dout, writes the gradients of L: dq [B, T, H, d], dk, dv [B, T, d] (bf16,
  * overwritten; dk and dv are summed over the query heads and every query that sees the key, in
  * fp32).  The result does not depend on the order in which the GPU runs its blocks: the same call
- * gives the same bits.  Outputs must not alias inputs or each other.  Errors as rglru_mqa_forward. */
+ * gives the same bits.  Errors as rglru_mqa_forward. */
 RGLRU_API rglru_status rglru_mqa_backward(const rglru_mqa_dims* dims, const void* v, const void* out, const void* dout,
                                           const void* save, size_t save_bytes, void* dq, void* dk, void* dv,
                                           void* workspace, size_t workspace_bytes, void* stream);
