@@ -106,3 +106,47 @@ def test_the_heavy_slot_has_a_small_value(log2_ratio, order):
     pav += 2.0 ** 6 * _floor(c, s, q, pos)[..., None]
     for h in range(H):
         _close(g[:, h], ref[:, h], pav[:, h], f"head {h}")
+
+
+@pytest.mark.parametrize("B", [2, 40])
+def test_what_is_not_finite_stays_where_it_belongs(B):
+    """A query with a NaN or an infinity: its head is NaN.  A slot, or a new key or value, that is not finite as a whole: its row's
+    heads are NaN, in every column.  All other rows and heads keep their bits."""
+    H, w = 6, 700
+    pos = np.array([2 * w + 11 * b for b in range(B)], dtype=np.int32)
+
+    def step(spoil):
+        rng = np.random.default_rng([47, B])
+        c, s = mqa_train.quantise(rng.standard_normal((B, 2, w, D)))
+        q, k, v = _bf16(rng, (B, H, D)), _bf16(rng, (B, D)), _bf16(rng, (B, D))
+        spoil(c, s, q, k, v)
+        dims = binding.make_mqa_dims(B, 1, H, D, w)
+        ws = binding.alloc_workspace(binding.mqa_decode8_workspace_size(dims))
+        out = torch.zeros(B, H, D, dtype=torch.bfloat16, device="cuda")
+        binding.mqa_decode8(dims, binding.to_device(q), binding.to_device(k), binding.to_device(v), _dev(pos), _dev(c), _dev(s),
+                            out, ws)
+        assert binding.read_device_status(ws) == binding.RGLRU_OK
+        return out
+
+    nan, inf = 0x7FC0, 0x7F80                      # bf16 bits
+    b = B - 1
+    head = lambda o: (o[b, 2:3], torch.cat([o[:b].flatten(), o[b, :2].flatten(), o[b, 3:].flatten()]))  # noqa: E731
+    row = lambda o: (o[b], o[:b].flatten())  # noqa: E731
+
+    def slot(half, scale):
+        def spoil(c, s, q, k, v):
+            c[b, half, 5], s[b, half, 5] = 0x7F, scale
+        return spoil
+
+    def put(name, at, bits):
+        def spoil(c, s, q, k, v):
+            dict(q=q, k=k, v=v)[name][at] = bits
+        return spoil
+
+    clean = step(lambda *x: None)
+    for part, spoil in [(head, put("q", (b, 2, 9), nan)), (head, put("q", (b, 2, 200), inf)),
+                        (row, slot(0, np.nan)), (row, slot(0, np.inf)), (row, slot(1, np.nan)), (row, slot(1, np.inf)),
+                        (row, put("k", (b, 9), nan)), (row, put("v", (b, 9), inf)), (row, put("v", (b, 9), nan))]:
+        (bad, rest), (_, same) = part(step(spoil)), part(clean)
+        assert torch.isnan(bad).all()
+        assert torch.equal(rest.view(torch.int16), same.view(torch.int16))
