@@ -35,6 +35,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pair.cuh"
 #include "sm100.cuh"
 #include "tma_maps.h"
 
@@ -156,34 +157,11 @@ __device__ __forceinline__ uint32_t idesc(int a_mn, int b_mn) {
 }
 
 // ---- the CTA pair: every tcgen05 instruction of this kernel is of cta_group::2
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish_pair() {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-// D (both CTAs' TMEM) (+)= A (both CTAs' halves) * B (both CTAs' halves)^T
-__device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t id,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(id), "r"(accumulate)
-        : "memory");
-}
-// arrive on the mbarrier at this shared address in both CTAs of the pair once every prior MMA
-// of this thread completes
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
-}
+using pr::mma_commit_pair;
+using pr::mma_ss_pair;
+using pr::tmem_alloc_pair;
+using pr::tmem_dealloc_pair;
+using pr::tmem_relinquish_pair;
 // a tile of this CTA's half into its own shared memory, its bytes counted on the leader's
 // barrier (a shared::cluster address)
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {

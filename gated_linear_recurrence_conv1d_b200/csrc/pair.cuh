@@ -1,5 +1,5 @@
 // pair.cuh -- tcgen05 and TMA wrappers of a CTA pair (cta_group::2), and bounded waits on barriers of a
-// cluster, for the attention kernels.  Rank 0 (the leader) issues the MMAs of the pair; each CTA's
+// cluster, for the attention kernels and the GEMM.  Rank 0 (the leader) issues the MMAs of the pair; each CTA's
 // TMEM holds its own 128 of the 256 rows, each CTA's shared memory half of the B operand.
 #pragma once
 
@@ -160,7 +160,6 @@ __device__ __forceinline__ bool bar_or(bool v, int threads) {
     return r != 0;
 }
 
-// two fp32 as packed bf16 (lo in the low half), round to nearest even
 // two fp32 operations in one instruction
 __device__ __forceinline__ uint64_t as_u64(float2 v) {
     return (uint64_t)__float_as_uint(v.x) | (uint64_t)__float_as_uint(v.y) << 32;
@@ -184,6 +183,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return as_float2(d);
 }
 
+// two fp32 as packed bf16 (lo in the low half), round to nearest even
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
