@@ -134,8 +134,10 @@ __device__ __forceinline__ void turn64(const float (&x)[8], const double2* cs, i
 // ---------------------------------------------------------------- write -------------------------------
 // Block = (token, up to kWriteRows batch rows): the angles of the token's position once for all of them (they are
 // half of the arithmetic), while the rows' keys and values are on their way; a warp per row.  The last min(len, w)
-// tokens of a row go into their slots.  Bound by fp64 arithmetic and latency: 8 rows of 2048 tokens in 13 us, of which
-// the bytes need 4 (a block a row: 22.6 us, its own angles each time; fp64 divisions: 14.4 us).
+// tokens of a row go into their slots.  Bound by latency and issue, not by the fp64 pipe (16 % busy; the conversions
+// between fp64 and fp32 fill theirs to 45 %): 2048 short blocks, each load -> angles -> barrier -> rotation ->
+// maximum over the warp -> store, two and a half rounds of them.  8 rows of 2048 tokens in 12.7 us, of which the
+// bytes need 4 (a block a row: 22.6 us, its own angles each time; fp64 divisions: 14.4 us).
 constexpr int kWriteRows = 8;
 __global__ void __launch_bounds__(32 * kWriteRows, 6)
 mqa_cache8_write_kernel(int B, int T, int w, int pos0, RopeBase base, const int* lengths, const __nv_bfloat16* k,
@@ -237,9 +239,10 @@ __global__ void __launch_bounds__(256) mqa_cache8_read_kernel(long long slots, i
 // All softmax warps prepare a CTA's first segment; two warps of their own the next one while a segment is worked on,
 // with two buffers for everything prepared.  S runs one tile ahead of the weighted sum, across segments, and a
 // segment's output is written after the first weights of the next.
-// The step reads every code once: bound by HBM.  256 full rings of 2048 slots, 10 heads: 55.0 us (272 MB; streaming
-// alone would take 42), of which about 10 us pass at the two ends (the angles, the first tile's way through, the merge) and
-// 2.5 us at each change of the row; a tile of 64 KB takes 1.39 us, and 1.05 us when the rings are in L2.
+// The step reads every code once: bound by HBM.  256 full rings of 2048 slots, 10 heads: 54.9 us in a graph, 58.6 us
+// launched in a loop (272 MB; streaming alone would take 42), of which about 10 us pass at the two ends (the angles,
+// the first tile's way through, the merge) and 2.5 us at each change of the row; a tile of 64 KB takes 1.40 us, and
+// 1.15 us when the rings are in L2.
 constexpr uint32_t TILE_BYTES = kTile * D;            // 32768: 2 boxes of [128 slots x 128 B]
 constexpr int kNBuf = 5;
 constexpr int kMaxCtas = 148;
@@ -919,8 +922,9 @@ mqa_decode8_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a) 
 // The rows of several segments from their parts, in order: block = (kHeads heads, row), thread = 4 columns, kLoads parts
 // in flight.  A row without a token is zero.  Bound by latency (two dependent loads, then the parts of a row together).
 // <1, 8> while there are fewer rows than CTAs, so that a row may have many parts (one ring of 2048: 16, two rounds of
-// loads).  Else <2, 4>: most rows have one to three parts, and the blocks, half as many, are resident together (256
-// rings of 2048: a step of 55.0 us instead of 55.6; 592 rings of 896, every row in one piece: 57.2 instead of 59.6).
+// loads).  Else <2, 4>: most rows have one to three parts, and the blocks, half as many, are resident together (in a
+// graph, 256 rings of 2048: a step of 55.0 us instead of 55.6; 592 rings of 896, every row in one piece: 57.2
+// instead of 59.6, now 56.1).
 template <int kHeads, int kLoads>
 __global__ void __launch_bounds__(kHeads * D / 4, kHeads == 1 ? 12 : 9)
 mqa_decode8_merge_kernel(int H, const int* pos, const int2* meta, const float* part, __nv_bfloat16* out) {

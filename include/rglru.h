@@ -303,7 +303,8 @@ RGLRU_API rglru_status rglru_mqa_backward(const rglru_mqa_dims* dims, const void
  *   codes   [B][2][window][head_dim] e4m3 bytes, slots as in the bf16 ring (rotated keys, values);
  *   scales  [B][2][window] fp32: value = code * scale, with scale = max(amax, 448 * 2^-126) / 448
  *           over the slot's 256 elements and code = x / scale rounded to e4m3 (nearest even).
- * A slot with an infinity or a NaN has scale and values that are not finite.  Dims as for
+ * A slot with an infinity or a NaN has scale and values that are not finite.  Scales are not
+ * negative; 0 is a slot of zeros, as a ring of zero bytes holds them.  Dims as for
  * rglru_mqa_decode (codes, cache: 16-byte aligned; scales: 4-byte), batch <= 65535,
  * batch * window <= 2^29. */
 
@@ -317,7 +318,8 @@ RGLRU_API rglru_status rglru_mqa_cache8_write(const rglru_mqa_dims* dims, const 
 /* One decode token per row against the 8-bit ring: as rglru_mqa_decode, with the new key and value
  * quantised into slot pos[b] mod w before the token attends to the ring's values (its own
  * among them).  pos[b] < 0 marks a row without a token: its out is zero, its ring untouched.  Slots
- * past a ring that is not full yet may hold anything. */
+ * past a ring that is not full yet may hold anything.  What a slot adds to out counts down to 2^-35
+ * of the row's heaviest (softmax weight times scale), whatever the other scales are. */
 RGLRU_API size_t rglru_mqa_decode8_workspace_size(const rglru_mqa_dims* dims);
 RGLRU_API rglru_status rglru_mqa_decode8(const rglru_mqa_dims* dims, const void* q, const void* k, const void* v,
                                          const int* pos, void* codes, float* scales, void* out, void* workspace,
