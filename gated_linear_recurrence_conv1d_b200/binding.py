@@ -390,6 +390,14 @@ def _addresses(where: str, *wanted):
     return out
 
 
+def _position(where: str, pos0) -> int:
+    """pos0 as the C int that it becomes: a number past it would arrive as another, not be refused there."""
+    p = int(pos0)
+    if not -2 ** 31 <= p < 2 ** 31:
+        raise ValueError(f"{where}: pos0 must fit 32 bits, got {p}")
+    return p
+
+
 def mqa_save_size(dims: MqaDims) -> int:
     return load().rglru_mqa_save_size(ctypes.byref(dims))
 
@@ -405,11 +413,12 @@ def mqa_forward(dims: MqaDims, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     (mqa_save_size bytes) keeps what mqa_backward needs."""
     B, T, H, d = dims.batch, dims.seq_len, dims.q_heads, dims.head_dim
     where = "rglru_mqa_forward"
+    p0 = _position(where, pos0)
     q_, k_, v_, out_, reset_, save_, ws_ = _addresses(
         where, ("q", q, (B, T, H, d), _BF16), ("k", k, (B, T, d), _BF16), ("v", v, (B, T, d), _BF16),
         ("out", out, (B, T, H, d), _BF16), ("reset", reset, (B, T), _BYTES), ("save", save, None, _BYTES),
         ("workspace", workspace, None, _BYTES))
-    rc = load().rglru_mqa_forward(ctypes.byref(dims), q_, k_, v_, reset_, int(pos0), out_, save_, save.numel(), ws_,
+    rc = load().rglru_mqa_forward(ctypes.byref(dims), q_, k_, v_, reset_, p0, out_, save_, save.numel(), ws_,
                                   workspace.numel(), _stream(stream))
     if rc:
         _check(rc, where)
@@ -436,10 +445,11 @@ def mqa_cache8_write(dims: MqaDims, k: torch.Tensor, v: torch.Tensor, codes: tor
     its bytes), scales [B, 2, w] fp32."""
     B, T, w, d = dims.batch, dims.seq_len, dims.window, dims.head_dim
     where = "rglru_mqa_cache8_write"
+    p0 = _position(where, pos0)
     k_, v_, codes_, scales_, lengths_ = _addresses(
         where, ("k", k, (B, T, d), _BF16), ("v", v, (B, T, d), _BF16), ("codes", codes, (B, 2, w, d), _CODES),
         ("scales", scales, (B, 2, w), _F32), ("lengths", lengths, (B,), _I32))
-    rc = load().rglru_mqa_cache8_write(ctypes.byref(dims), k_, v_, lengths_, int(pos0), codes_, scales_, _stream(stream))
+    rc = load().rglru_mqa_cache8_write(ctypes.byref(dims), k_, v_, lengths_, p0, codes_, scales_, _stream(stream))
     if rc:
         _check(rc, where)
 
